@@ -285,7 +285,7 @@ def _own(s):
     import mla_latent_kv_44_b200 as mla
 
     op = s["op"]
-    if "cfg" not in s:
+    if "bs" in s and "cfg" not in s:
         s["cfg"] = _config(s)
     if op == "tables":
         mla.build_tables(s["cfg"], s["lens"], s["new"], s["table"], s["held"], s["free"],
