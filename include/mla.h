@@ -84,6 +84,8 @@ typedef struct {
 #define MLA_DEV_OOB_POS 2u      /* sequence index or position outside the block table         */
 #define MLA_DEV_WAIT_TIMEOUT 4u /* a bounded wait inside a kernel gave up; results invalid    */
 #define MLA_DEV_BAD_LENGTH 8u   /* seq_lens[b] < q_per_seq or > max_blocks * block_size      */
+#define MLA_DEV_BAD_TREE 16u    /* a parent index or an accepted path that no tree has        */
+#define MLA_DEV_NO_BLOCKS 32u   /* a request's blocks do not fit the free list                */
 
 /* Rows of the packed absorbed query and of the cache: r + d_r values. */
 
@@ -368,6 +370,145 @@ MLA_API mla_status mla_decode_fp8(const mla_config* cfg, const void* q, const ui
 MLA_API mla_status mla_combine_partials(const mla_config* cfg, const float* part_latent,
                                         const float* part_lse, int32_t parts, int32_t n,
                                         float* out_latent, float* lse, void* stream);
+
+/*
+ * Speculative decoding with a tree of drafted tokens. A step drafts q_per_seq = T nodes for every
+ * sequence: node 0, 1, ... with parent[t] < t (or -1: the node follows the cached rows). Node t's
+ * cache row is row P + t of its sequence, P = seq_lens[b] - T, while its RoPE position is P plus
+ * its depth; it attends the P rows before the tree, its ancestors and itself. After the
+ * verification the accepted path's rows are moved together behind row P. One step:
+ *   mla_build_tables (blocks and slots for P + T rows), mla_tree_masks (masks, positions),
+ *   mla_absorb_query, mla_append_slots, mla_decode_tree, then mla_commit_tree.
+ * A sequence whose length is 0 is an empty place of a padded batch: no call reads its rows or
+ * flags it.
+ */
+
+/* Most requests mla_build_tables takes in one call, and most nodes of a drafted tree. */
+#define MLA_MAX_TABLE_BATCH 8192
+#define MLA_MAX_TREE 256
+
+/*
+ * mla_build_tables -- a step's block table and slot map from the requests' lengths (paged cache:
+ * "MLA from scratch in PyTorch", What's not in this implementation; the tables are what
+ * mla_append_latent, mla_append_slots and the decode calls read). For request b, with
+ * want = ceil(seq_lens[b] / block_size):
+ *   - blocks: entries blocks_held[b] .. want - 1 of its table row are filled from the free list
+ *     (want > blocks_held[b]), or entries want .. blocks_held[b] - 1 are given back to it
+ *     (want < blocks_held[b]; seq_lens[b] = 0 gives back everything). All blocks given back are
+ *     pushed on the free list first, in order of request and entry; blocks are then taken from
+ *     its end, request after request. A request whose blocks run past the list gets none, nor
+ *     does any later one that needs some: MLA_DEV_NO_BLOCKS, its blocks_held stays and its slots
+ *     are -1. Entries that are given back keep their old value; only the first blocks_held_out[b]
+ *     entries of a row mean anything.
+ *   - tokens: its new_lens[b] last rows are this step's tokens, numbered request after request:
+ *     cu_new (batch + 1) int32 are the offsets (usable as mla_prefill's cu_seqlens where every
+ *     row is new), and token i of request b has seq_idx[i] = b, pos[i] = its row and
+ *     slots[i] = block * block_size + row % block_size, its row of the pool. Entries behind the
+ *     last token, up to max_tokens, get seq_idx -1, pos 0 and slot -1.
+ * seq_lens, new_lens, blocks_held, blocks_held_out (batch) int32; block_table
+ * (batch, max_blocks) int32, in and out; free_blocks (num_blocks) int32, in and out, of which the
+ * first free_count[0] are free; free_count, free_count_out (1) int32; seq_idx, pos
+ * (max_tokens) int32; slots (max_tokens) int64. blocks_held_out and free_count_out may be
+ * blocks_held and free_count; no other arrays may overlap. Of cfg only block_size is used.
+ * Data errors: MLA_DEV_BAD_LENGTH for a length outside [0, max_blocks * block_size], new_lens[b]
+ * outside [0, seq_lens[b]] or blocks_held[b] outside [0, max_blocks] (the request keeps its blocks
+ * and has no tokens), for more than max_tokens tokens (those behind are dropped, cu_new stops
+ * there) and for a free_count outside [0, num_blocks] or more blocks given back than the list
+ * has room for (no block moves); MLA_DEV_OOB_BLOCK for a block id outside the pool (slot -1).
+ * One launch; deterministic. batch <= MLA_MAX_TABLE_BATCH, max_tokens <= 2^26 and
+ * batch * max_blocks <= 2^30 (MLA_ERR_UNSUPPORTED). max_tokens may be 0.
+ */
+MLA_API mla_status mla_build_tables(const mla_config* cfg, const int32_t* seq_lens,
+                                    const int32_t* new_lens, int32_t batch, int32_t* block_table,
+                                    int32_t max_blocks, const int32_t* blocks_held,
+                                    int32_t* free_blocks, const int32_t* free_count,
+                                    int32_t num_blocks, int32_t* blocks_held_out,
+                                    int32_t* free_count_out, int32_t* cu_new, int32_t* seq_idx,
+                                    int32_t* pos, int64_t* slots, int32_t max_tokens,
+                                    uint32_t* dev_err, void* stream);
+
+/*
+ * mla_tree_masks -- what a drafted tree's parent indices mean to the attention: for node t of
+ * sequence b (n = b * T + t)
+ *   A_t = {t} + A_parent(t),  mask[n] = the bits of A_t (bit j % 32 of word j / 32 for node j),
+ *   pos[n] = seq_lens[b] - T + |A_t| - 1 (its RoPE position).
+ * parents (parents_batch, T) int32 with parents_batch = batch, or 1 for one tree that all
+ * sequences share; seq_lens (batch) int32, the drafted rows counted; mask
+ * (batch * T, ceil(T / 32)) uint32; pos (batch * T) int32. A parent outside [-1, t) sets
+ * MLA_DEV_BAD_TREE and counts as -1; 0 < seq_lens[b] < T sets MLA_DEV_BAD_LENGTH (positions 0, as
+ * for an empty sequence). 1 <= q_per_seq <= MLA_MAX_TREE (MLA_ERR_UNSUPPORTED above).
+ */
+MLA_API mla_status mla_tree_masks(const int32_t* parents, int32_t parents_batch,
+                                  const int32_t* seq_lens, int32_t batch, int32_t q_per_seq,
+                                  uint32_t* mask, int32_t* pos, uint32_t* dev_err, void* stream);
+
+/*
+ * mla_append_slots -- mla_append_latent's row [RMSNorm(ckv_raw[n]) * gamma || RoPE(krope_raw[n],
+ * pos[n])], written to row slots[n] of the pool (its rows numbered block after block: slot =
+ * block * block_size + row in block, as mla_build_tables gives them). The position and the place
+ * are apart: a drafted token's position comes from its depth. A negative slot is skipped (a
+ * step's padding); one outside the pool sets MLA_DEV_OOB_BLOCK and is skipped. Slots must differ:
+ * of two tokens with one slot either's values may stay. ckv_raw (n_tokens, r), krope_raw
+ * (n_tokens, d_r), pool (num_blocks, block_size, r + d_r) dtype; gamma (r) float32; pos
+ * (n_tokens) int32; slots (n_tokens) int64. ckv_raw, gamma and pool must be 16-byte aligned.
+ * fp32 statistics, angles in double; the sum of squares is taken in another order than
+ * mla_append_latent's, so a value may round the other way.
+ */
+MLA_API mla_status mla_append_slots(const mla_config* cfg, const void* ckv_raw,
+                                    const void* krope_raw, const float* gamma, const int32_t* pos,
+                                    const int64_t* slots, void* pool, int32_t num_blocks,
+                                    int32_t n_tokens, uint32_t* dev_err, void* stream);
+
+/* Workspace of mla_decode_tree in bytes (0 for an invalid configuration); 256-byte aligned. */
+MLA_API size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t batch,
+                                              int32_t q_per_seq);
+
+/*
+ * mla_decode_tree -- attention of T = q_per_seq drafted tokens per sequence and the value
+ * up-projection ([B] Absorbing projections; [C] the output rearrangement). For node t of sequence
+ * b (n = b * T + t), P = seq_lens[b] - T, head h, over the rows j < P and the rows P + i whose
+ * bit i is set in the node's mask:
+ *   s_j = softmax_scale * Q[n, h, :] . row_j,  p = softmax(s),  lse[n, h] = log(sum_j exp(s_j)),
+ *   o[n, h, :] = W_UV[h] sum_j p_j row_j[0:r].
+ * q (batch * T, H, r + d_r) dtype, as mla_absorb_query writes it; pool, block_table and seq_lens
+ * as in mla_decode (the drafted rows are in the pool and counted); tree_mask
+ * (batch * T, ceil(T / 32)) uint32 as mla_tree_masks writes it, any bits, or NULL for a chain (node
+ * t attends rows 0 .. P + t: mla_decode's rule); w_uv (H, d_v, r) dtype; o (batch * T, H, d_v)
+ * dtype; lse (batch * T, H) float32 or NULL. A drafted row that a node's mask leaves out does not
+ * reach that node's result, whatever it holds (NaN, infinities, a row never written). A node
+ * that attends nothing gets o = 0 and lse = -inf, and so does every node of an empty sequence
+ * (seq_lens[b] = 0); a length in (0, T) or above max_blocks * block_size does too and sets
+ * MLA_DEV_BAD_LENGTH. q, pool, w_uv and o must be 16-byte aligned. The latent sums are held in
+ * fp32 (in the workspace) between the attention and W_UV. Deterministic.
+ * 1 <= q_per_seq <= MLA_MAX_TREE (MLA_ERR_UNSUPPORTED above).
+ */
+MLA_API mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* pool,
+                                   const int32_t* block_table, int32_t max_blocks,
+                                   int32_t num_blocks, const int32_t* seq_lens, int32_t batch,
+                                   int32_t q_per_seq, const uint32_t* tree_mask, const void* w_uv,
+                                   void* workspace, size_t workspace_bytes, void* o, float* lse,
+                                   uint32_t* dev_err, void* stream);
+
+/*
+ * mla_commit_tree -- keep the accepted path of every sequence's tree: with
+ * P = seq_lens[b] - q_per_seq, row P + d becomes row P + path[b, d] for d < path_len[b] (in the
+ * pool, through the block table), and seq_lens_out[b] = P + path_len[b]. Rows behind are left as
+ * they are. A node's RoPE position is its depth's, so its row is right in its new place. path
+ * (batch, path_width) int32, strictly increasing node numbers; path_len (batch) int32, 0 where
+ * nothing is accepted; seq_lens, seq_lens_out (batch) int32, which may be the same array;
+ * pool (num_blocks, block_size, r + d_r) dtype, 16-byte aligned, in and out. A path that is
+ * not strictly increasing in [0, q_per_seq), or path_len[b] outside [0, min(q_per_seq,
+ * path_width)], sets MLA_DEV_BAD_TREE; a bad length sets MLA_DEV_BAD_LENGTH; such a sequence keeps
+ * its rows and its length. A block id outside the pool sets MLA_DEV_OOB_BLOCK (that row is not
+ * moved). An empty sequence stays empty. The blocks behind the new length stay held: the next
+ * mla_build_tables uses them or gives them back.
+ */
+MLA_API mla_status mla_commit_tree(const mla_config* cfg, const int32_t* path,
+                                   const int32_t* path_len, int32_t path_width, int32_t q_per_seq,
+                                   const int32_t* block_table, int32_t max_blocks, void* pool,
+                                   int32_t num_blocks, const int32_t* seq_lens,
+                                   int32_t* seq_lens_out, int32_t batch, uint32_t* dev_err,
+                                   void* stream);
 
 /* Human-readable name of a status code (static storage). */
 MLA_API const char* mla_status_string(mla_status status);

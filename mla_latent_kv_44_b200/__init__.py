@@ -23,9 +23,11 @@ STATIC_WORKSPACE_BYTES = 40 << 20
 MLA_F32, MLA_BF16 = 0, 1
 DECODE_AUTO, DECODE_SIMT, DECODE_TENSOR = 0, 1, 2
 DEV_OOB_BLOCK, DEV_OOB_POS, DEV_WAIT_TIMEOUT, DEV_BAD_LENGTH = 1, 2, 4, 8
+DEV_BAD_TREE, DEV_NO_BLOCKS = 16, 32
 STAGE_PLAN, STAGE_ATTEND, STAGE_COMBINE = 1, 2, 4
 STAGES_ALL = STAGE_PLAN | STAGE_ATTEND | STAGE_COMBINE
 MAX_COMBINE_PARTS = 256  # MLA_MAX_COMBINE_PARTS
+MAX_TABLE_BATCH, MAX_TREE = 8192, 256  # MLA_MAX_TABLE_BATCH, MLA_MAX_TREE
 
 _c_i32, _c_f32, _vp, _sz = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -80,6 +82,15 @@ def _load():
         "mla_project_workspace_size": (_sz, [P, ctypes.POINTER(MlaFrontConfig), _c_i32]),
         "mla_project": (_c_i32, [P, ctypes.POINTER(MlaFrontConfig), _vp, _vp, _vp, _vp, _vp,
                                  _vp, _vp, _vp, _vp, _vp, _vp, _c_i32, _vp, _sz, _vp, _vp]),
+        "mla_build_tables": (_c_i32, [P, _vp, _vp, _c_i32, _vp, _c_i32, _vp, _vp, _vp, _c_i32, _vp,
+                                      _vp, _vp, _vp, _vp, _vp, _c_i32, _vp, _vp]),
+        "mla_tree_masks": (_c_i32, [_vp, _c_i32, _vp, _c_i32, _c_i32, _vp, _vp, _vp, _vp]),
+        "mla_append_slots": (_c_i32, [P, _vp, _vp, _vp, _vp, _vp, _vp, _c_i32, _c_i32, _vp, _vp]),
+        "mla_decode_tree_workspace_size": (_sz, [P, _c_i32, _c_i32]),
+        "mla_decode_tree": (_c_i32, [P, _vp, _vp, _vp, _c_i32, _c_i32, _vp, _c_i32, _c_i32, _vp,
+                                     _vp, _vp, _sz, _vp, _vp, _vp, _vp]),
+        "mla_commit_tree": (_c_i32, [P, _vp, _vp, _c_i32, _c_i32, _vp, _c_i32, _vp, _c_i32, _vp,
+                                     _vp, _c_i32, _vp, _vp]),
         "mla_status_string": (ctypes.c_char_p, [_c_i32]),
         "mla_abi_version": (_c_i32, []),
     }
@@ -126,6 +137,17 @@ class Config:
                          self.kv_rank, self.rope_dim, self.block_size, self.rope_base,
                          self.rms_eps, scale, MLA_BF16 if self.dtype == "bf16" else MLA_F32,
                          self.decode_kernel)
+
+    def ref(self):
+        """A reference to the C struct for a call; built again only when a field has changed."""
+        key = (self.num_heads, self.head_dim, self.kv_rank, self.rope_dim, self.block_size,
+               self.dtype, self.head_dim_v, self.rope_base, self.rms_eps, self.softmax_scale,
+               self.decode_kernel)
+        held = self.__dict__.get("_ref")
+        if held is None or held[0] != key:
+            held = (key, ctypes.byref(self.c()))
+            self.__dict__["_ref"] = held
+        return held[1]
 
     @property
     def row_width(self) -> int:
@@ -305,6 +327,168 @@ def prefill(cfg: Config, q_nope, q_rope, pos, rows, w_uk, w_uv, cu_seqlens, max_
                            int(max_seqlen), int(q_nope.shape[0]), _ptr(o), _ptr(workspace),
                            workspace.numel() * workspace.element_size(), _ptr(dev_err),
                            _stream(stream)), "mla_prefill")
+
+
+# ---- speculative decoding with a drafted tree ------------------------------------------------
+# These calls check what a raw pointer cannot carry (device, dtype, shape, contiguity) and raise
+# MlaError before anything is launched; they launch on the tensors' device whichever device is
+# current.
+
+def _expect(where: str, name: str, t, dtype, device, *shape):
+    """t is a contiguous tensor of dtype on device; a None in shape stands for any size."""
+    ok = t.dtype is dtype and t.device == device and t.is_contiguous()
+    if ok:
+        got = t.shape
+        ok = len(got) == len(shape)
+        if ok:
+            for n, want in zip(got, shape):
+                if want is not None and n != want:
+                    ok = False
+    if not ok:
+        raise MlaError(MLA_ERR_INVALID_ARG,
+                       f"{where}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}"
+                       f"{'' if t.is_contiguous() else ' (not contiguous)'}, wanted {dtype} "
+                       f"({', '.join('any' if n is None else str(n) for n in shape)}) on {device}")
+
+
+def _launch(where: str, fn, device, stream, *args):
+    """Call fn(*args, stream) with `device` current."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream(stream)), where)
+
+
+def _device_of(where: str, name: str, t):
+    if not t.is_cuda:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is on {t.device}, not on a GPU")
+    return t.device
+
+
+def build_tables(cfg: Config, seq_lens, new_lens, block_table, blocks_held, free_blocks,
+                 free_count, blocks_held_out, free_count_out, cu_new, seq_idx, pos, slots, dev_err,
+                 stream=None):
+    """mla_build_tables: a step's block table and slot map from the requests' lengths.
+
+    The pool has free_blocks.shape[0] blocks; blocks_held_out and free_count_out may be
+    blocks_held and free_count.
+    """
+    import torch
+    w, i32 = "mla_build_tables", torch.int32
+    dev = _device_of(w, "seq_lens", seq_lens)
+    n, tokens = seq_lens.shape[0], slots.shape[0]
+    _expect(w, "seq_lens", seq_lens, i32, dev, n)
+    _expect(w, "new_lens", new_lens, i32, dev, n)
+    _expect(w, "block_table", block_table, i32, dev, n, None)
+    _expect(w, "blocks_held", blocks_held, i32, dev, n)
+    _expect(w, "free_blocks", free_blocks, i32, dev, None)
+    _expect(w, "free_count", free_count, i32, dev, 1)
+    _expect(w, "blocks_held_out", blocks_held_out, i32, dev, n)
+    _expect(w, "free_count_out", free_count_out, i32, dev, 1)
+    _expect(w, "cu_new", cu_new, i32, dev, n + 1)
+    _expect(w, "seq_idx", seq_idx, i32, dev, tokens)
+    _expect(w, "pos", pos, i32, dev, tokens)
+    _expect(w, "slots", slots, torch.int64, dev, tokens)
+    _expect(w, "dev_err", dev_err, i32, dev, 1)
+    _launch(w, lib.mla_build_tables, dev, stream, cfg.ref(), seq_lens.data_ptr(),
+            new_lens.data_ptr(), n, block_table.data_ptr(), block_table.shape[1],
+            blocks_held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
+            free_blocks.shape[0], blocks_held_out.data_ptr(), free_count_out.data_ptr(),
+            cu_new.data_ptr(), seq_idx.data_ptr(), pos.data_ptr(), slots.data_ptr(), tokens,
+            dev_err.data_ptr())
+
+
+def tree_masks(parents, seq_lens, mask, pos, dev_err, stream=None):
+    """mla_tree_masks: ancestor masks (int32 words) and RoPE positions of drafted trees given by
+    their parent indices, (batch, T), or (1, T) for one tree that all sequences share."""
+    import torch
+    w, i32 = "mla_tree_masks", torch.int32
+    dev = _device_of(w, "parents", parents)
+    n = seq_lens.shape[0]
+    _expect(w, "parents", parents, i32, dev, None, None)
+    T = parents.shape[1]
+    _expect(w, "seq_lens", seq_lens, i32, dev, n)
+    _expect(w, "mask", mask, i32, dev, n * T, (T + 31) // 32)
+    _expect(w, "pos", pos, i32, dev, n * T)
+    _expect(w, "dev_err", dev_err, i32, dev, 1)
+    _launch(w, lib.mla_tree_masks, dev, stream, parents.data_ptr(), parents.shape[0],
+            seq_lens.data_ptr(), n, T, mask.data_ptr(), pos.data_ptr(), dev_err.data_ptr())
+
+
+def append_slots(cfg: Config, ckv_raw, krope_raw, gamma, pos, slots, pool, dev_err, stream=None):
+    """mla_append_slots: mla_append_latent's rows written to the pool rows `slots` (a negative
+    slot is skipped), RoPE positions given apart. krope_raw may be None when rope_dim is 0."""
+    import torch
+    w, dt = "mla_append_slots", cfg.torch_dtype
+    dev = _device_of(w, "pool", pool)
+    n = slots.shape[0]
+    _expect(w, "ckv_raw", ckv_raw, dt, dev, n, cfg.kv_rank)
+    if cfg.rope_dim:
+        _expect(w, "krope_raw", krope_raw, dt, dev, n, cfg.rope_dim)
+    _expect(w, "gamma", gamma, torch.float32, dev, cfg.kv_rank)
+    _expect(w, "pos", pos, torch.int32, dev, n)
+    _expect(w, "slots", slots, torch.int64, dev, n)
+    _expect(w, "pool", pool, dt, dev, None, cfg.block_size, cfg.kv_rank + cfg.rope_dim)
+    _expect(w, "dev_err", dev_err, torch.int32, dev, 1)
+    _launch(w, lib.mla_append_slots, dev, stream, cfg.ref(), ckv_raw.data_ptr(), _ptr(krope_raw),
+            gamma.data_ptr(), pos.data_ptr(), slots.data_ptr(), pool.data_ptr(), pool.shape[0], n,
+            dev_err.data_ptr())
+
+
+def decode_tree_workspace_size(cfg: Config, batch: int, q_per_seq: int) -> int:
+    return int(lib.mla_decode_tree_workspace_size(cfg.ref(), batch, q_per_seq))
+
+
+def decode_tree(cfg: Config, q, pool, block_table, seq_lens, q_per_seq: int, tree_mask, w_uv,
+                workspace, o, lse, dev_err, stream=None):
+    """mla_decode_tree: attention of every drafted token over its sequence's cache and the drafted
+    rows its mask names (None: a chain), then W_UV. lse may be None."""
+    import torch
+    w, dt, i32 = "mla_decode_tree", cfg.torch_dtype, torch.int32
+    dev = _device_of(w, "pool", pool)
+    n = seq_lens.shape[0]
+    nt, H, D = n * q_per_seq, cfg.num_heads, cfg.kv_rank + cfg.rope_dim
+    dv = cfg.head_dim_v or cfg.head_dim
+    _expect(w, "q", q, dt, dev, nt, H, D)
+    _expect(w, "pool", pool, dt, dev, None, cfg.block_size, D)
+    _expect(w, "block_table", block_table, i32, dev, n, None)
+    _expect(w, "seq_lens", seq_lens, i32, dev, n)
+    if tree_mask is not None:
+        _expect(w, "tree_mask", tree_mask, i32, dev, nt, (q_per_seq + 31) // 32)
+    _expect(w, "w_uv", w_uv, dt, dev, H, dv, cfg.kv_rank)
+    _expect(w, "o", o, dt, dev, nt, H, dv)
+    if lse is not None:
+        _expect(w, "lse", lse, torch.float32, dev, nt, H)
+    _expect(w, "workspace", workspace, torch.uint8, dev, None)
+    _expect(w, "dev_err", dev_err, i32, dev, 1)
+    _launch(w, lib.mla_decode_tree, dev, stream, cfg.ref(), q.data_ptr(), pool.data_ptr(),
+            block_table.data_ptr(), block_table.shape[1], pool.shape[0], seq_lens.data_ptr(), n,
+            q_per_seq, _ptr(tree_mask), w_uv.data_ptr(), workspace.data_ptr(), workspace.shape[0],
+            o.data_ptr(), _ptr(lse), dev_err.data_ptr())
+
+
+def commit_tree(cfg: Config, path, path_len, q_per_seq: int, block_table, pool, seq_lens,
+                seq_lens_out, dev_err, stream=None):
+    """mla_commit_tree: the accepted path's rows moved together, seq_lens_out the lengths with it
+    (may be seq_lens). path: (batch, width) node numbers, path_len of them count."""
+    import torch
+    w, i32 = "mla_commit_tree", torch.int32
+    dev = _device_of(w, "pool", pool)
+    n = seq_lens.shape[0]
+    _expect(w, "path", path, i32, dev, n, None)
+    _expect(w, "path_len", path_len, i32, dev, n)
+    _expect(w, "block_table", block_table, i32, dev, n, None)
+    _expect(w, "pool", pool, cfg.torch_dtype, dev, None, cfg.block_size,
+            cfg.kv_rank + cfg.rope_dim)
+    _expect(w, "seq_lens", seq_lens, i32, dev, n)
+    _expect(w, "seq_lens_out", seq_lens_out, i32, dev, n)
+    _expect(w, "dev_err", dev_err, i32, dev, 1)
+    _launch(w, lib.mla_commit_tree, dev, stream, cfg.ref(), path.data_ptr(), path_len.data_ptr(),
+            path.shape[1], q_per_seq, block_table.data_ptr(), block_table.shape[1],
+            pool.data_ptr(), pool.shape[0], seq_lens.data_ptr(), seq_lens_out.data_ptr(), n,
+            dev_err.data_ptr())
 
 
 def abi_version() -> int:

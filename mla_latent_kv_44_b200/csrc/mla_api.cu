@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "tree.cuh"
 
 using namespace mla;
 
@@ -511,6 +512,204 @@ mla_status mla_decode_step(const mla_config* cfg, const void* q_nope, const void
   if (e == cudaSuccess) e = launch_combine(p, st);
   if (e == cudaSuccess) e = launch_output_tc(*cfg, out_latent, w_uv, o, n, dev_err, st);
   return from_cuda(e);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// Speculative decoding with a drafted tree
+// ------------------------------------------------------------------------------------------
+namespace {
+
+// Workspace of mla_decode_tree: the latent sums and the partial results of split key ranges;
+// on the tensor-core path the schedule too.
+struct TreeLayout {
+  bool tc;
+  size_t latent, part_lse, part_o, header, range_begin, segments, items[5], total;
+  int tile_rows, tiles, splits, team, groups, ranges;
+};
+
+TreeLayout tree_layout(const mla_config& c, int batch, int T) {
+  TreeLayout L{};
+  const size_t n = (size_t)batch * T * c.num_heads;
+  L.tc = c.decode_kernel != MLA_DECODE_SIMT && tree_tc_supported(c);
+  L.tile_rows = L.tc ? kTreeTile : tree_simt_tile_rows(c);
+  L.tiles = (T * c.num_heads + L.tile_rows - 1) / L.tile_rows;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
+  L.latent = take(n * c.kv_rank * sizeof(float));
+  if (L.tc) {
+    tree_team(L.tiles, &L.team, &L.ranges);
+    L.groups = (L.tiles + L.team - 1) / L.team;
+    const size_t items = (size_t)batch * L.groups;
+    L.part_lse = take((size_t)kMaxPartials * kTreeTile * sizeof(float));
+    L.part_o = take((size_t)kMaxPartials * kTreeTile * c.kv_rank * sizeof(float));
+    L.header = take(64 * sizeof(int32_t));
+    L.range_begin = take((kRanges + 1) * sizeof(int32_t));
+    L.segments = take((kRanges + items) * sizeof(Segment));
+    for (size_t& it : L.items) it = take(items * sizeof(int32_t));
+  } else {
+    // enough CTAs for four on each of 148 SMs
+    const int64_t ctas = (int64_t)batch * L.tiles;
+    L.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTreeMaxSplits, 4 * 148 / ctas));
+    L.part_lse = take(L.splits > 1 ? L.splits * n * sizeof(float) : 0);
+    L.part_o = take(L.splits > 1 ? L.splits * n * c.kv_rank * sizeof(float) : 0);
+  }
+  L.total = off;
+  return L;
+}
+
+bool tree_shape_ok(int32_t batch, int32_t T) { return batch >= 1 && T >= 1 && T <= MLA_MAX_TREE; }
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_build_tables(const mla_config* cfg, const int32_t* seq_lens,
+                            const int32_t* new_lens, int32_t batch, int32_t* block_table,
+                            int32_t max_blocks, const int32_t* blocks_held, int32_t* free_blocks,
+                            const int32_t* free_count, int32_t num_blocks,
+                            int32_t* blocks_held_out, int32_t* free_count_out, int32_t* cu_new,
+                            int32_t* seq_idx, int32_t* pos, int64_t* slots, int32_t max_tokens,
+                            uint32_t* dev_err, void* stream) {
+  if (!valid_config(cfg) || batch < 0 || max_tokens < 0) return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (!seq_lens || !new_lens || !block_table || !blocks_held || !free_blocks || !free_count ||
+      !blocks_held_out || !free_count_out || !cu_new || !dev_err ||
+      (max_tokens > 0 && (!seq_idx || !pos || !slots)))
+    return MLA_ERR_INVALID_ARG;
+  if (max_blocks < 1 || num_blocks < 1) return MLA_ERR_INVALID_ARG;
+  if (batch > MLA_MAX_TABLE_BATCH || max_tokens > (1 << 26) ||
+      (int64_t)batch * max_blocks > (1 << 30))
+    return MLA_ERR_UNSUPPORTED;
+  return from_cuda(launch_build_tables(seq_lens, new_lens, batch, block_table, max_blocks,
+                                       cfg->block_size, blocks_held, free_blocks, free_count,
+                                       num_blocks, blocks_held_out, free_count_out, cu_new,
+                                       seq_idx, pos, slots, max_tokens, dev_err,
+                                       (cudaStream_t)stream));
+}
+
+mla_status mla_tree_masks(const int32_t* parents, int32_t parents_batch, const int32_t* seq_lens,
+                          int32_t batch, int32_t q_per_seq, uint32_t* mask, int32_t* pos,
+                          uint32_t* dev_err, void* stream) {
+  if (batch < 0 || q_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (!parents || !seq_lens || !mask || !pos || !dev_err) return MLA_ERR_INVALID_ARG;
+  if (parents_batch != 1 && parents_batch != batch) return MLA_ERR_INVALID_ARG;
+  if (q_per_seq > MLA_MAX_TREE || (int64_t)batch * q_per_seq > (1 << 24))
+    return MLA_ERR_UNSUPPORTED;
+  return from_cuda(launch_tree_masks(parents, parents_batch, seq_lens, batch, q_per_seq, mask, pos,
+                                     dev_err, (cudaStream_t)stream));
+}
+
+mla_status mla_append_slots(const mla_config* cfg, const void* ckv_raw, const void* krope_raw,
+                            const float* gamma, const int32_t* pos, const int64_t* slots,
+                            void* pool, int32_t num_blocks, int32_t n_tokens, uint32_t* dev_err,
+                            void* stream) {
+  if (!valid_config(cfg) || n_tokens < 0) return MLA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return MLA_OK;
+  if (!ckv_raw || (cfg->rope_dim > 0 && !krope_raw) || !gamma || !pos || !slots || !pool ||
+      !dev_err || num_blocks < 1)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(ckv_raw, 16) || !aligned(gamma, 16) || !aligned(pool, 16))
+    return MLA_ERR_INVALID_ARG;
+  if (n_tokens > (1 << 26)) return MLA_ERR_UNSUPPORTED;
+  return from_cuda(launch_append_slots(*cfg, ckv_raw, krope_raw, gamma, pos, slots, pool,
+                                       num_blocks, n_tokens, dev_err, (cudaStream_t)stream));
+}
+
+size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t batch, int32_t q_per_seq) {
+  if (!valid_config(cfg) || !tree_shape_ok(batch, q_per_seq)) return 0;
+  if ((int64_t)batch * q_per_seq * cfg->num_heads > (1 << 28)) return 0;
+  return tree_layout(*cfg, batch, q_per_seq).total;
+}
+
+mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* pool,
+                           const int32_t* block_table, int32_t max_blocks, int32_t num_blocks,
+                           const int32_t* seq_lens, int32_t batch, int32_t q_per_seq,
+                           const uint32_t* tree_mask, const void* w_uv, void* workspace,
+                           size_t workspace_bytes, void* o, float* lse, uint32_t* dev_err,
+                           void* stream) {
+  if (!valid_config(cfg) || batch < 0 || q_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (!q || !pool || !block_table || !seq_lens || !w_uv || !workspace || !o || !dev_err)
+    return MLA_ERR_INVALID_ARG;
+  if (max_blocks < 1 || num_blocks < 1) return MLA_ERR_INVALID_ARG;
+  if (q_per_seq > MLA_MAX_TREE ||
+      (int64_t)batch * q_per_seq * cfg->num_heads > (1 << 28) ||
+      (int64_t)batch * q_per_seq > (1 << 24))
+    return MLA_ERR_UNSUPPORTED;
+  if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(w_uv, 16) || !aligned(o, 16))
+    return MLA_ERR_INVALID_ARG;
+  const mla_config& c = *cfg;
+  const TreeLayout L = tree_layout(c, batch, q_per_seq);
+  if (workspace_bytes < L.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+  if (c.decode_kernel == MLA_DECODE_TENSOR && !L.tc) return MLA_ERR_UNSUPPORTED;
+  char* ws = (char*)workspace;
+  TreeParams p{};
+  p.q = q;
+  p.pool = pool;
+  p.table = block_table;
+  p.seq_lens = seq_lens;
+  p.mask = tree_mask;
+  p.latent = (float*)(ws + L.latent);
+  p.lse = lse;
+  p.err = dev_err;
+  p.part_lse = (float*)(ws + L.part_lse);
+  p.part_o = (float*)(ws + L.part_o);
+  p.H = c.num_heads;
+  p.r = c.kv_rank;
+  p.dr = c.rope_dim;
+  p.D = c.kv_rank + c.rope_dim;
+  p.bs = c.block_size;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.batch = batch;
+  p.T = q_per_seq;
+  p.BT = batch * q_per_seq;
+  p.words = (q_per_seq + 31) / 32;
+  p.scale = c.softmax_scale;
+  p.tile_rows = L.tile_rows;
+  p.tiles = L.tiles;
+  cudaError_t e;
+  if (L.tc) {
+    p.team = L.team;
+    p.groups = L.groups;
+    p.ranges = L.ranges;
+    p.header = (int32_t*)(ws + L.header);
+    p.range_begin = (int32_t*)(ws + L.range_begin);
+    p.segments = (Segment*)(ws + L.segments);
+    p.item_len = (int32_t*)(ws + L.items[0]);
+    p.item_chunk0 = (int32_t*)(ws + L.items[1]);
+    p.item_slot0 = (int32_t*)(ws + L.items[2]);
+    p.item_nseg = (int32_t*)(ws + L.items[3]);
+    p.merge_list = (int32_t*)(ws + L.items[4]);
+    e = launch_tree_tc(c, p, (cudaStream_t)stream);
+  } else {
+    // no more ranges than 64-row pieces of the longest sequence the table can hold
+    p.splits = (int)std::min<int64_t>(
+        L.splits, std::max<int64_t>(1, ((int64_t)max_blocks * c.block_size + 63) / 64));
+    e = launch_tree_simt(c, p, (cudaStream_t)stream);
+  }
+  if (e != cudaSuccess) return from_cuda(e);
+  return mla_output(cfg, p.latent, w_uv, o, p.BT, dev_err, stream);
+}
+
+mla_status mla_commit_tree(const mla_config* cfg, const int32_t* path, const int32_t* path_len,
+                           int32_t path_width, int32_t q_per_seq, const int32_t* block_table,
+                           int32_t max_blocks, void* pool, int32_t num_blocks,
+                           const int32_t* seq_lens, int32_t* seq_lens_out, int32_t batch,
+                           uint32_t* dev_err, void* stream) {
+  if (!valid_config(cfg) || batch < 0 || q_per_seq < 1 || path_width < 1)
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (!path || !path_len || !block_table || !pool || !seq_lens || !seq_lens_out || !dev_err)
+    return MLA_ERR_INVALID_ARG;
+  if (max_blocks < 1 || num_blocks < 1 || !aligned(pool, 16)) return MLA_ERR_INVALID_ARG;
+  if (q_per_seq > MLA_MAX_TREE) return MLA_ERR_UNSUPPORTED;
+  return from_cuda(launch_commit_tree(*cfg, path, path_len, path_width, q_per_seq, block_table,
+                                      max_blocks, pool, num_blocks, seq_lens, seq_lens_out, batch,
+                                      dev_err, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,352 @@
+// mla_build_tables and mla_tree_masks: the integer work of a serving step, from the requests'
+// lengths (and a drafted tree's parent indices) to the block tables, slot maps, masks and
+// positions that the other calls read.
+//
+// build_tables. One thread-block cluster does the whole call in one launch. Every CTA scans the
+// requests (new tokens, blocks given back, blocks taken: three prefix sums) into its own shared
+// memory, so that no offsets travel between CTAs; the CTAs then share the moves and the slot
+// map. Three phases are separated by cluster barriers, because each reads what the one before
+// wrote in global memory: blocks given back are pushed on the free stack; blocks taken come off
+// its top into the table; slots are read from the table. Everything is placed by prefix sums,
+// none by atomics: the same inputs give the same tables.
+// What bounds it: latency (a chain of dependent loads and two barriers) at decode sizes; 16 B
+// written per token for prompts.
+#include <algorithm>
+
+#include "tree.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kTabThreads = 1024;
+constexpr int kTabMaxCtas = 8;  // portable cluster size
+
+struct TableParams {
+  const int32_t *seq_lens, *new_lens, *held;
+  int32_t *table, *free_blocks;
+  const int32_t* free_count;
+  int32_t *held_out, *free_count_out, *cu, *seq_idx, *pos;
+  int64_t* slots;
+  uint32_t* err;
+  int batch, max_blocks, num_blocks, bs, max_tokens;
+};
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+
+// Token counts saturate here: above any max_tokens (at most 2^26), below overflow. A request's
+// own count is capped at kTokenCap, so that every offset below 2^28 is exact.
+constexpr int kTokenSat = 1 << 29, kTokenCap = 1 << 28;
+
+// Inclusive scan of three ints over the CTA (a saturating); s holds 3 x 32 ints.
+__device__ void scan3(int* s, int& a, int& b, int& c) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o),
+              vc = __shfl_up_sync(0xffffffffu, c, o);
+    if (lane >= o) {
+      a = min(a + va, kTokenSat);
+      b += vb;
+      c += vc;
+    }
+  }
+  if (lane == 31) {
+    s[warp] = a;
+    s[32 + warp] = b;
+    s[64 + warp] = c;
+  }
+  __syncthreads();
+  if (warp < 3) {
+    int v = s[32 * warp + lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = warp == 0 ? min(v + u, kTokenSat) : v + u;
+    }
+    s[32 * warp + lane] = v;
+  }
+  __syncthreads();
+  if (warp > 0) {
+    a = min(a + s[warp - 1], kTokenSat);
+    b += s[32 + warp - 1];
+    c += s[64 + warp - 1];
+  }
+  __syncthreads();
+}
+
+// One request as the phases see it.
+struct Request {
+  int len, fresh, held, want;
+  bool ok;
+};
+
+__device__ __forceinline__ Request load_request(const TableParams& p, int b) {
+  Request q;
+  q.len = p.seq_lens[b];
+  q.fresh = p.new_lens[b];
+  q.held = p.held[b];
+  q.ok = q.len >= 0 && (int64_t)q.len <= (int64_t)p.max_blocks * p.bs && q.fresh >= 0 &&
+         q.fresh <= q.len && q.held >= 0 && q.held <= p.max_blocks;
+  q.want = q.ok ? (int)(((int64_t)q.len + p.bs - 1) / p.bs) : q.held;
+  if (!q.ok) q.fresh = 0;
+  return q;
+}
+
+__global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TableParams p) {
+  extern __shared__ int s_dyn[];
+  int* s_cu = s_dyn;                   // batch + 1: new tokens before request b
+  int* s_back = s_cu + p.batch + 1;    // batch: blocks given back by earlier requests
+  int* s_take = s_back + p.batch;      // batch: blocks due to earlier requests
+  int* s_start = s_take + p.batch;     // batch: first new row, or -1 - row when not served
+  __shared__ int s_scan[96], s_carry[3];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  wait_prior_grid();
+
+  // requests, scanned by every CTA
+  const int count = p.free_count[0];
+  if (tid < 3) s_carry[tid] = 0;
+  __syncthreads();
+  for (int base = 0; base < p.batch; base += kTabThreads) {
+    const int b = base + tid;
+    int n = 0, back = 0, take = 0;
+    if (b < p.batch) {
+      const Request q = load_request(p, b);
+      if (!q.ok && cta == 0) set_error(p.err, MLA_DEV_BAD_LENGTH);
+      n = min(q.fresh, kTokenCap);
+      back = max(q.held - q.want, 0);
+      take = max(q.want - q.held, 0);
+      s_start[b] = q.ok ? q.len - q.fresh : 0;
+    }
+    int a0 = n, a1 = back, a2 = take;
+    scan3(s_scan, a0, a1, a2);
+    if (b < p.batch) {
+      s_cu[b] = min(s_carry[0] + a0, kTokenSat) - n;
+      s_back[b] = s_carry[1] + a1 - back;
+      s_take[b] = s_carry[2] + a2 - take;
+    }
+    __syncthreads();
+    if (tid == kTabThreads - 1) {
+      s_carry[0] = min(s_carry[0] + a0, kTokenSat);
+      s_carry[1] += a1;
+      s_carry[2] += a2;
+    }
+    __syncthreads();
+  }
+  const int tokens = s_carry[0], backs = s_carry[1], takes = s_carry[2];
+  if (tid == 0) s_cu[p.batch] = tokens;
+  // a stack that cannot be one: no block moves
+  const bool stack_ok = count >= 0 && count <= p.num_blocks && backs <= p.num_blocks - count;
+  if (!stack_ok && cta == 0 && tid == 0) set_error(p.err, MLA_DEV_BAD_LENGTH);
+  const int stack = stack_ok ? count + backs : 0;
+
+  // blocks given back, in (request, index) order; a warp per request
+  const int gwarp = cta * (kTabThreads / 32) + (tid >> 5), gwarps = ctas * (kTabThreads / 32);
+  if (stack_ok && backs > 0) {
+    for (int b = gwarp; b < p.batch; b += gwarps) {
+      const Request q = load_request(p, b);
+      for (int i = q.want + lane; i < q.held; i += 32)
+        p.free_blocks[count + s_back[b] + i - q.want] = p.table[(size_t)b * p.max_blocks + i];
+    }
+  }
+  cluster_barrier();
+
+  // blocks taken: the k-th off the top; a request whose share runs past the bottom gets none
+  if (takes > 0) {
+    for (int b = gwarp; b < p.batch; b += gwarps) {
+      const Request q = load_request(p, b);
+      const int take = q.want - q.held;
+      if (take <= 0 || s_take[b] > stack - take) continue;
+      for (int i = lane; i < take; i += 32) {
+        const int blk = __ldcg(p.free_blocks + (stack - 1 - s_take[b] - i));
+        if (blk < 0 || blk >= p.num_blocks) set_error(p.err, MLA_DEV_OOB_BLOCK);
+        p.table[(size_t)b * p.max_blocks + q.held + i] = blk;
+      }
+    }
+  }
+  __syncthreads();
+  for (int b = tid; b < p.batch; b += kTabThreads) {
+    const Request q = load_request(p, b);
+    const int take = q.want - q.held;
+    if (take > 0 && s_take[b] > stack - take) {
+      s_start[b] = -1 - s_start[b];
+      if (cta == 0) set_error(p.err, MLA_DEV_NO_BLOCKS);
+    }
+  }
+  cluster_barrier();  // the table is complete, and held and free_count are read
+
+  // counts
+  if (cta == 0) {
+    int last = 0;  // blocks taken by the requests that were served
+    for (int b = tid; b < p.batch; b += kTabThreads) {
+      const Request q = load_request(p, b);
+      const int take = q.want - q.held;
+      const bool served = s_start[b] >= 0;
+      if (take > 0 && served) last = max(last, s_take[b] + take);
+      p.held_out[b] = (take > 0 ? served : stack_ok) ? q.want : q.held;
+      p.cu[b] = min(s_cu[b], p.max_tokens);
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0) s_scan[tid >> 5] = last;
+    __syncthreads();
+    if (tid < 32) {
+      last = __reduce_max_sync(0xffffffffu, s_scan[tid]);
+      if (tid == 0) {
+        p.free_count_out[0] = stack_ok ? stack - last : count;
+        p.cu[p.batch] = min(tokens, p.max_tokens);
+        if (tokens > p.max_tokens) set_error(p.err, MLA_DEV_BAD_LENGTH);
+      }
+    }
+  }
+
+  // tokens: four independent ones per thread and pass, so that their table reads overlap
+  const int step = ctas * kTabThreads;
+  for (int i0 = cta * kTabThreads + tid; i0 < p.max_tokens; i0 += 4 * step) {
+    int seq[4], row[4], blk[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * step;
+      seq[u] = -1;
+      row[u] = 0;
+      blk[u] = -1;
+      if (i < p.max_tokens && i < tokens) {
+        int lo = 0, hi = p.batch - 1;  // last request with s_cu <= i
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (s_cu[mid] <= i) lo = mid;
+          else hi = mid - 1;
+        }
+        const int start = s_start[lo];
+        seq[u] = lo;
+        row[u] = (start < 0 ? -1 - start : start) + i - s_cu[lo];
+        if (start >= 0) {
+          blk[u] = __ldcg(p.table + (size_t)lo * p.max_blocks + row[u] / p.bs);
+          if (blk[u] < 0 || blk[u] >= p.num_blocks) {
+            set_error(p.err, MLA_DEV_OOB_BLOCK);
+            blk[u] = -1;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * step;
+      if (i < p.max_tokens) {
+        p.seq_idx[i] = seq[u];
+        p.pos[i] = row[u];
+        p.slots[i] = blk[u] < 0 ? -1 : (int64_t)blk[u] * p.bs + row[u] % p.bs;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens, int batch,
+                                int32_t* table, int max_blocks, int bs, const int32_t* held,
+                                int32_t* free_blocks, const int32_t* free_count, int num_blocks,
+                                int32_t* held_out, int32_t* free_count_out, int32_t* cu,
+                                int32_t* seq_idx, int32_t* pos, int64_t* slots, int max_tokens,
+                                uint32_t* err, cudaStream_t st) {
+  TableParams p{seq_lens, new_lens, held,    table, free_blocks, free_count, held_out,
+                free_count_out, cu, seq_idx, pos,   slots,       err,        batch,
+                max_blocks, num_blocks, bs, max_tokens};
+  const size_t smem = sizeof(int) * (4 * (size_t)batch + 1);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  // one CTA while a pass of it covers the tokens and the requests, else a full cluster
+  const int ctas = max_tokens <= kTabThreads && batch <= kTabThreads ? 1 : kTabMaxCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kTabThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
+}
+
+// ------------------------------------------------------------------------------------------
+// tree_masks: A_t = {t} u A_parent(t), and pos_t = seq_len - T + |A_t| - 1. One thread per node
+// walks up its ancestors in shared memory: random trees of T nodes are O(log T) deep, and a
+// chain of 256 costs 256 shared-memory reads. Several sequences share a CTA when T is small.
+// ------------------------------------------------------------------------------------------
+namespace {
+
+template <int W>
+__global__ void __launch_bounds__(256)
+tree_masks_kernel(const int32_t* __restrict__ parents, int parents_batch,
+                  const int32_t* __restrict__ seq_lens, int batch, int T, uint32_t* mask,
+                  int32_t* pos, uint32_t* err) {
+  __shared__ int s_parent[256];
+  wait_prior_grid();
+  const int per = 256 / T;  // sequences per CTA (T <= 256)
+  const int k = threadIdx.x / T, t = threadIdx.x - k * T;
+  const int b = blockIdx.x * per + k;
+  const bool live = k < per && b < batch;
+  if (live) {
+    int a = parents[(parents_batch == 1 ? 0 : (size_t)b * T) + t];
+    if (a < -1 || a >= t) {
+      set_error(err, MLA_DEV_BAD_TREE);
+      a = -1;
+    }
+    s_parent[threadIdx.x] = a;
+  }
+  __syncthreads();
+  if (!live) return;
+  uint32_t w[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = 0;
+  int depth = -1;
+  for (int a = t; a >= 0; a = s_parent[k * T + a]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (W == 1 || i == (a >> 5)) w[i] |= 1u << (a & 31);
+    ++depth;
+  }
+  const size_t n = (size_t)b * T + t;
+  const int words = (T + 31) / 32;
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (i < words) mask[n * words + i] = w[i];
+  const int len = seq_lens[b];
+  const bool bad = len < T;
+  if (bad && len != 0 && t == 0) set_error(err, MLA_DEV_BAD_LENGTH);
+  pos[n] = bad ? 0 : len - T + depth;
+}
+
+}  // namespace
+
+cudaError_t launch_tree_masks(const int32_t* parents, int parents_batch, const int32_t* seq_lens,
+                              int batch, int T, uint32_t* mask, int32_t* pos, uint32_t* err,
+                              cudaStream_t st) {
+  const int per = 256 / T;
+  const dim3 grid((batch + per - 1) / per);
+  const int words = (T + 31) / 32;
+  if (words == 1)
+    return launch_pdl(tree_masks_kernel<1>, grid, dim3(256), 0, st, parents, parents_batch,
+                      seq_lens, batch, T, mask, pos, err);
+  if (words == 2)
+    return launch_pdl(tree_masks_kernel<2>, grid, dim3(256), 0, st, parents, parents_batch,
+                      seq_lens, batch, T, mask, pos, err);
+  if (words <= 4)
+    return launch_pdl(tree_masks_kernel<4>, grid, dim3(256), 0, st, parents, parents_batch,
+                      seq_lens, batch, T, mask, pos, err);
+  return launch_pdl(tree_masks_kernel<8>, grid, dim3(256), 0, st, parents, parents_batch,
+                    seq_lens, batch, T, mask, pos, err);
+}
+
+}  // namespace mla

@@ -1,0 +1,239 @@
+// mla_append_slots and mla_commit_tree: cache rows written through a slot map, and the accepted
+// path's rows moved together.
+//
+// append_slots. row = [ RMSNorm(ckv) * gamma || RoPE(krope, pos) ], written to pool row slots[n].
+// A drafted token's RoPE position is its depth's while its row is its own, so the position and
+// the place are two inputs here. One warp per row, rows dealt round the grid: a lane holds up to
+// NP 16-byte pieces of the row (coalesced across the warp), fp32 statistics by a butterfly. The
+// angles are p * theta_i in double, as everywhere in the library; theta_i = base^(-2i/d_r) costs
+// a double pow, so a lane takes it once for its pairs and keeps it over all its rows.
+// What bounds it: HBM for prompts (the row in and out), latency for a decode step.
+#include <algorithm>
+
+#include "tree.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kAppendWarps = 8;
+
+template <typename T> struct Piece;  // 16 bytes of a row
+template <> struct Piece<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *(const uint4*)p;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *(const uint32_t*)&h;
+    }
+    *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Piece<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
+    const float4 u = *(const float4*)p;
+    v[0] = u.x;
+    v[1] = u.y;
+    v[2] = u.z;
+    v[3] = u.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
+    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+
+template <typename T, int NP>
+__global__ void __launch_bounds__(kAppendWarps * 32)
+append_slots_kernel(const T* __restrict__ ckv, const T* __restrict__ kr,
+                    const float* __restrict__ gamma, const int32_t* __restrict__ pos,
+                    const int64_t* __restrict__ slots, T* pool, int64_t pool_rows, int n, int r,
+                    int dr, float eps, float base, uint32_t* err) {
+  constexpr int E = Piece<T>::N;
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * kAppendWarps;
+  const int half = dr / 2, D = r + dr;
+  const double theta0 =
+      lane < half ? pow((double)base, -2.0 * (double)lane / (double)dr) : 0.0;
+  wait_prior_grid();
+  for (int row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5); row < n; row += warps) {
+    const int64_t slot = slots[row];
+    if (slot < 0) continue;  // a step's padding
+    if (slot >= pool_rows) {
+      if (lane == 0) set_error(err, MLA_DEV_OOB_BLOCK);
+      continue;
+    }
+    const T* x = ckv + (size_t)row * r;
+    float v[NP][E];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int at = (lane + 32 * k) * E;
+      if (at < r) {
+        Piece<T>::load(x + at, v[k]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) ss = fmaf(v[k][e], v[k][e], ss);
+      }
+    }
+    T* dst = pool + (size_t)slot * D;
+    const double p = (double)pos[row];
+    const T* kx = kr + (size_t)row * dr;
+    for (int i = lane; i < half; i += 32) {
+      const double theta =
+          i < 32 ? theta0 : pow((double)base, -2.0 * (double)i / (double)dr);
+      double c, s;
+      sincos(p * theta, &s, &c);
+      const double x0 = to_f32(kx[2 * i]), x1 = to_f32(kx[2 * i + 1]);
+      dst[r + 2 * i] = from_f32<T>((float)(x0 * c - x1 * s));
+      dst[r + 2 * i + 1] = from_f32<T>((float)(x0 * s + x1 * c));
+    }
+    ss = warp_sum(ss);
+    const float inv = 1.0f / sqrtf(ss / (float)r + eps);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int at = (lane + 32 * k) * E;
+      if (at < r) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 g = *(const float4*)(gamma + at + e);
+          v[k][e] *= inv * g.x;
+          v[k][e + 1] *= inv * g.y;
+          v[k][e + 2] *= inv * g.z;
+          v[k][e + 3] *= inv * g.w;
+        }
+        Piece<T>::store(dst + at, v[k]);
+      }
+    }
+  }
+}
+
+template <typename T, int NP>
+cudaError_t append_slots_go(const mla_config& c, const void* ckv, const void* kr,
+                            const float* gamma, const int32_t* pos, const int64_t* slots,
+                            void* pool, int num_blocks, int n, uint32_t* err, cudaStream_t st) {
+  const int grid = std::min((n + kAppendWarps - 1) / kAppendWarps, 148 * 8);
+  return launch_pdl(append_slots_kernel<T, NP>, dim3(grid), dim3(kAppendWarps * 32), 0, st,
+                    (const T*)ckv, (const T*)kr, gamma, pos, slots, (T*)pool,
+                    (int64_t)num_blocks * c.block_size, n, c.kv_rank, c.rope_dim, c.rms_eps,
+                    c.rope_base, err);
+}
+
+}  // namespace
+
+cudaError_t launch_append_slots(const mla_config& c, const void* ckv, const void* kr,
+                                const float* gamma, const int32_t* pos, const int64_t* slots,
+                                void* pool, int num_blocks, int n, uint32_t* err,
+                                cudaStream_t st) {
+  // pieces per lane: r values in 16-byte pieces over 32 lanes
+  const int np = (c.kv_rank * (c.dtype == MLA_BF16 ? 2 : 4) / 16 + 31) / 32;
+#define MLA_GO(T, NP) \
+  append_slots_go<T, NP>(c, ckv, kr, gamma, pos, slots, pool, num_blocks, n, err, st)
+  if (c.dtype == MLA_BF16) {
+    if (np <= 1) return MLA_GO(__nv_bfloat16, 1);
+    if (np <= 2) return MLA_GO(__nv_bfloat16, 2);
+    return MLA_GO(__nv_bfloat16, 4);
+  }
+  if (np <= 1) return MLA_GO(float, 1);
+  if (np <= 2) return MLA_GO(float, 2);
+  if (np <= 4) return MLA_GO(float, 4);
+  return MLA_GO(float, 8);
+#undef MLA_GO
+}
+
+// ------------------------------------------------------------------------------------------
+// commit_tree: row P + d <- row P + path[d], d < count, and the new length P + count. A path
+// goes down the tree, so it is strictly increasing and path[d] >= d: a row is never overwritten
+// before every later d has another source, and moving in order of d is safe in place. One CTA
+// per sequence; a thread owns one 16-byte (8-byte) column of the rows and moves it for all d, so
+// no two threads touch the same bytes and nothing has to be waited for between rows: kMove loads
+// are in flight, then their stores (the stores of rows d .. d + kMove - 1 cannot reach a source
+// path[d'] >= d' >= d + kMove). The path is checked before anything moves.
+// ------------------------------------------------------------------------------------------
+namespace {
+
+constexpr int kMove = 8;
+constexpr int kCommitThreads = 128;
+
+template <typename V>
+__global__ void __launch_bounds__(kCommitThreads)
+commit_tree_kernel(const int32_t* __restrict__ path, const int32_t* __restrict__ count,
+                   int width, int T, const int32_t* __restrict__ table, int max_blocks,
+                   uint8_t* pool, int num_blocks, int bs, int row_vecs, const int32_t* seq_lens,
+                   int32_t* seq_lens_out, uint32_t* err) {
+  __shared__ int64_t s_from[MLA_MAX_TREE], s_to[MLA_MAX_TREE];  // rows of the pool, -1: skip
+  wait_prior_grid();
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int len = seq_lens[b];
+  if (len == 0) {  // an empty place of the batch
+    __syncthreads();
+    if (tid == 0) seq_lens_out[b] = 0;
+    return;
+  }
+  const int n = count[b];
+  bool ok = len >= T && (int64_t)len <= (int64_t)max_blocks * bs && n >= 0 && n <= width && n <= T;
+  const bool len_ok = len >= T && (int64_t)len <= (int64_t)max_blocks * bs;
+  const int first = len - T;
+  if (ok) {
+    for (int d = tid; d < n; d += kCommitThreads) {
+      const int a = path[(size_t)b * width + d];
+      const int before = d > 0 ? path[(size_t)b * width + d - 1] : -1;
+      if (a <= before || a < 0 || a >= T) {
+        ok = false;
+        continue;
+      }
+      const int from = first + a, to = first + d;
+      const int bf = table[(size_t)b * max_blocks + from / bs];
+      const int bt = table[(size_t)b * max_blocks + to / bs];
+      const bool in = bf >= 0 && bf < num_blocks && bt >= 0 && bt < num_blocks;
+      if (!in) set_error(err, MLA_DEV_OOB_BLOCK);
+      s_from[d] = in && a != d ? (int64_t)bf * bs + from % bs : -1;
+      s_to[d] = (int64_t)bt * bs + to % bs;
+    }
+  }
+  ok = __syncthreads_and(ok);
+  if (!ok) {
+    if (tid == 0) {
+      set_error(err, len_ok ? MLA_DEV_BAD_TREE : MLA_DEV_BAD_LENGTH);
+      seq_lens_out[b] = len;
+    }
+    return;
+  }
+  if (tid == 0) seq_lens_out[b] = first + n;
+  V* rows = (V*)pool;
+  for (int c = tid; c < row_vecs; c += kCommitThreads) {
+    for (int d0 = 0; d0 < n; d0 += kMove) {
+      V v[kMove];
+#pragma unroll
+      for (int u = 0; u < kMove; ++u)
+        if (d0 + u < n && s_from[d0 + u] >= 0) v[u] = rows[s_from[d0 + u] * row_vecs + c];
+#pragma unroll
+      for (int u = 0; u < kMove; ++u)
+        if (d0 + u < n && s_from[d0 + u] >= 0) rows[s_to[d0 + u] * row_vecs + c] = v[u];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_commit_tree(const mla_config& c, const int32_t* path, const int32_t* count,
+                               int width, int T, const int32_t* table, int max_blocks, void* pool,
+                               int num_blocks, const int32_t* seq_lens, int32_t* seq_lens_out,
+                               int batch, uint32_t* err, cudaStream_t st) {
+  // rows are r + d_r values, a multiple of 8: whole 16-byte pieces in both types
+  const int row_vecs = (c.kv_rank + c.rope_dim) * (c.dtype == MLA_BF16 ? 2 : 4) / 16;
+  return launch_pdl(commit_tree_kernel<uint4>, dim3(batch), dim3(kCommitThreads), 0, st, path,
+                    count, width, T, table, max_blocks, (uint8_t*)pool, num_blocks,
+                    c.block_size, row_vecs, seq_lens, seq_lens_out, err);
+}
+
+}  // namespace mla

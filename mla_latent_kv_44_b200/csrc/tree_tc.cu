@@ -1,0 +1,960 @@
+// Tensor-core attention of mla_decode_tree (bf16, r = 512, d_r = 64, cache blocks of a multiple of
+// 64 rows, any number of heads), for sm_100a.
+//
+// A sequence's T drafted tokens and H heads are T * H query rows over the same cache rows. They
+// are tiled by 128, whatever token or head a row belongs to; per tile of query rows
+//   S = Q . K^T   (128 x keys, K = 576)      O += P . V   (128 x 512, K = keys; V = the latent
+//                                                          part of the same rows)
+// are dense contractions that a pair of SMs does together (cta_group::2, M = 128: each CTA of a
+// cluster of two holds 64 query rows of Q, P, S and O in its own memories, and half of every
+// B operand: half of the keys for S, half of the latent dims for O). So a CTA's O takes 256
+// tensor-memory columns (its 64 rows in lanes 0-63 for one half of the dims and again in lanes
+// 64-127 for the other), which leaves room for two buffers of S over 256 keys; and P stays in the
+// SM that computed it: nothing but MMA operands crosses between the two.
+//
+// Per 256 keys a CTA streams 9 stages of K (128 keys x 64 dims) and 8 of V (64 keys x 128 dims), 16
+// KB each, through one ring in the order the products use them: K(0), K(1), V(0), K(2), V(1) ...
+// so the scores of tile t + 1 run on the tensor core while the softmax of tile t does, and
+// P . V of tile t while the softmax of tile t + 1 reads its scores. Four MMAs (64 cycles each)
+// use a stage. The whole MMA warp runs the issue loop and one elected lane issues: with a single
+// thread in a divergent branch an MMA took 132 cycles to issue whatever its size (measured),
+// with the warp converged 45.
+//
+// Softmax: four warps, a thread holds one query row and half of the tile's keys (TMEM lane), two
+// threads of a row exchange their maxima; base-2 exponents, the running maximum moved only when
+// a tile exceeds it by 2^8, the sum l of the fp32 weights. The same warps rescale O when the
+// maximum moves and write O / l at a segment's end.
+//
+// Rows that a token does not see: the prefix (rows before the drafted ones) is seen by all; for
+// the drafted rows a thread builds the 32-bit words of its keys from its token's mask, and a
+// masked score becomes -inf by selection. P = 0 times a masked row's V would still be NaN if the
+// row held NaN, so the V stages that hold drafted rows (or rows past the end) pass through the
+// fixer warp, which replaces what is not finite by 0 before the MMA may read it.
+//
+// Warps: 0 TMA, 1 MMA issue (in the pair's first CTA), 2 fixer, 4-7 softmax and epilogue. Every
+// wait is bounded: on timeout the kernel sets MLA_DEV_WAIT_TIMEOUT, drains what it issued, frees
+// TMEM and returns. No TMA multicast is used.
+#include <atomic>
+
+#include "plan_body.cuh"
+#include "tc_ptx.cuh"
+#include "tma_map.h"
+#include "tree.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kR = 512;
+constexpr int kDR = 64;
+constexpr int kD = kR + kDR;
+constexpr int kM = kTreeTile;             // query rows per pair of CTAs
+constexpr int kMH = kM / 2;               // query rows per CTA
+constexpr int kRows = 64;                 // cache rows per block of keys
+constexpr int kTileBlocks = 4;            // blocks per tile: 256 keys
+constexpr int kSlabBytes = 64 * 64 * 2;   // 64 rows x 64 dims bf16: 8 KB
+constexpr int kStageBytes = 2 * kSlabBytes;
+constexpr int kStages = 7;
+constexpr int kKStages = kD / 64;         // stages of a tile's K
+constexpr int kQBytes = kKStages * kSlabBytes;
+constexpr int kPBytes = kTileBlocks * kSlabBytes;
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;           // S buffers at columns 0 and 128
+constexpr unsigned long long kTimeoutNs = 1000000000ull;  // 1 s per wait
+
+constexpr int kS_Ring = 0;
+constexpr int kS_Q = kS_Ring + kStages * kStageBytes;     // 112 KB
+constexpr int kS_P = kS_Q + kQBytes;                      // 184 KB
+constexpr int kS_Red = kS_P + kPBytes;                    // 216 KB: max[2 tiles][2 halves][64]
+constexpr int kS_Sum = kS_Red + 4 * kMH * 4;              // l[2 segments][2 halves][64]
+constexpr int kS_Seg = kS_Sum + 4 * kMH * 4;
+constexpr int kSegCache = 32;
+constexpr int kS_Bar = kS_Seg + kSegCache * 32;
+
+enum Bar {
+  // in the first CTA only (the MMA warp waits): arrivals come from both CTAs
+  kFull = 0,                   // kStages: both CTAs' parts of a stage landed (or were fixed)
+  kQFull = kFull + kStages,    // both CTAs' query rows landed
+  kSFree,                      // 2: softmax warps of both CTAs copied an S buffer out
+  kPReady = kSFree + 2,        // P written and O rescaled in both CTAs
+  // in each CTA
+  kEmpty,                      // kStages: the MMAs reading a stage are complete
+  kQEmpty = kEmpty + kStages,  // the segment's last S is complete
+  kSFull,                      // 2: an S buffer is complete
+  kPvDone = kSFull + 2,        // a tile's P . V is complete
+  kRed,                        // the four softmax warps posted their maxima
+  kSum,                        // ... their sums
+  kFix,                        // kStages: a stage for the fixer landed
+  kFinal = kFix + kStages,
+  kNumBars
+};
+constexpr int kSmemBytes = kS_Bar + kNumBars * 8 + 16 + 1024;  // + alignment to 1 KB
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+
+// ------------------------------------------------------------------------------ PTX helpers
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+// D[tmem of both CTAs] (+)= A[smem] . B[smem]; descriptors as low words, the high word constant
+// (stride 1024, version 1, 128-byte swizzle)
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFF) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id,
+                                     uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(id), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
+// arrives on the barrier at this offset in both CTAs of the pair once the MMAs issued before are
+// complete
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar), "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+// load into this CTA's shared memory, bytes counted on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                              int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void expect_tx_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;"
+      "\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
+struct Ctl {
+  uint32_t* err;
+  volatile int* abort;
+};
+
+// Warp-collective bounded wait; the result is the same in all 32 lanes.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t* err,
+                                       volatile int* abort) {
+  uint64_t t0 = 0;
+  for (int it = 0;; ++it) {
+    if (__all_sync(0xffffffffu, try_cluster(bar, parity))) return true;
+    if (it == 0) t0 = globaltimer();
+    const bool late = (globaltimer() - t0) > kTimeoutNs;
+    if (__any_sync(0xffffffffu, *abort != 0 || late)) {
+      if ((threadIdx.x & 31) == 0 && late) {
+        set_error(err, MLA_DEV_WAIT_TIMEOUT);
+        *abort = 1;
+      }
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
+  if (__all_sync(0xffffffffu, try_cluster(bar, parity))) return true;
+  return wait_slow(bar, parity, c.err, c.abort);
+}
+// Bounded wait for a phase that normally completed long ago (drains at teardown).
+__device__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
+  const uint64_t t0 = globaltimer();
+  bool done = false;
+  while (!done && globaltimer() - t0 < kTimeoutNs)
+    done = __all_sync(0xffffffffu, try_cluster(bar, parity));
+  if (!done && (threadIdx.x & 31) == 0) set_error(err, MLA_DEV_WAIT_TIMEOUT);
+}
+
+// A segment of this team's work range as one member sees it.
+struct SegInfo {
+  int b, row0, chunk_lo, chunk_hi, slot, chunk0, len, pad;
+};
+
+__device__ __forceinline__ SegInfo load_segment(const TreeParams& p, int s, int member) {
+  const Segment sg = p.segments[s];
+  const int b = sg.bt / p.groups, mt = (sg.bt - b * p.groups) * p.team + member;
+  return SegInfo{b, mt * kM, sg.chunk_lo, sg.chunk_hi, sg.slot < 0 ? -1 : sg.slot * p.team + member,
+                 p.item_chunk0[sg.bt], p.item_len[sg.bt], 0};
+}
+
+// One tile: up to four consecutive 64-row chunks of one segment.
+struct Tile {
+  int b, row0, chunk, nb, ntok, len, slot;
+  bool first, last;
+  __device__ int half_blocks() const { return nb > 2 ? 2 : 1; }  // blocks of keys per CTA
+};
+
+// Walks the tiles of segments [s, se) in order, identically in every warp of both CTAs.
+struct TileWalk {
+  const TreeParams* p;
+  const SegInfo* cache;  // shared memory, segments sb .. sb + kSegCache - 1
+  int sb, s, se, c, member, loaded;
+  SegInfo cur;
+  __device__ bool next(Tile& tl) {
+    while (s < se) {
+      if (loaded != s) {
+        cur = (s - sb < kSegCache) ? cache[s - sb] : load_segment(*p, s, member);
+        loaded = s;
+      }
+      // a member whose tile of query rows lies behind the last one has nothing to do
+      if (cur.row0 < p->T * p->H) {
+        if (c < cur.chunk_lo) c = cur.chunk_lo;
+        if (c < cur.chunk_hi) {
+          tl.b = cur.b;
+          tl.row0 = cur.row0;
+          tl.chunk = c - cur.chunk0;
+          tl.nb = min(kTileBlocks, cur.chunk_hi - c);
+          tl.len = cur.len;
+          tl.ntok = min(tl.nb * kRows, cur.len - tl.chunk * kRows);
+          tl.slot = cur.slot;
+          tl.first = (c == cur.chunk_lo);
+          tl.last = (c + tl.nb == cur.chunk_hi);
+          c += tl.nb;
+          return true;
+        }
+      }
+      ++s;
+      c = -1;
+    }
+    return false;
+  }
+};
+
+// First pool row of a sequence's 64-row chunks, 32 table entries read at a time: lane i holds
+// that of chunk base + i. Blocks outside the pool are flagged at use and replaced by block 0.
+struct RowWindow {
+  int b = -1, base = 0, blk = 0;
+  __device__ int get(const TreeParams& p, int seq, int chunk, int lane) {
+    const int per = p.bs / kRows;  // chunks per cache block
+    const int at = chunk / per;
+    if (seq != b || at < base || at >= base + 32) {  // warp-uniform
+      b = seq;
+      base = at;
+      blk = at + lane < p.max_blocks ? p.table[(size_t)seq * p.max_blocks + at + lane] : 0;
+    }
+    int id = __shfl_sync(0xffffffffu, blk, at - base);
+    if (id < 0 || id >= p.num_blocks) {
+      if (lane == 0) set_error(p.err, MLA_DEV_OOB_BLOCK);
+      id = 0;
+    }
+    return id * p.bs + (chunk - at * per) * kRows;
+  }
+};
+
+// Whether chunk j of a tile holds drafted rows or rows past the end: its V goes by the fixer.
+__device__ __forceinline__ bool needs_fix(const Tile& tl, int j, int T) {
+  return (tl.chunk + j + 1) * kRows > tl.len - T;
+}
+
+// Bits of the 32 keys from drafted node n0 on (negative: prefix rows, always seen) that token t of
+// sequence b sees.
+__device__ __forceinline__ uint32_t seen_word(const TreeParams& p, int b, int t, int n0) {
+  if (n0 <= -32) return 0xffffffffu;
+  auto word = [&](int w) -> uint32_t {  // nodes 32w .. 32w + 31
+    if (w < 0 || 32 * w >= p.T) return 0;
+    uint32_t m;
+    if (p.mask) {
+      m = p.mask[((size_t)b * p.T + t) * p.words + w];
+    } else {
+      m = 32 * w + 31 <= t ? 0xffffffffu : 32 * w > t ? 0 : 0xffffffffu >> (31 - (t & 31));
+    }
+    const int left = p.T - 32 * w;
+    return left < 32 ? m & ((1u << left) - 1) : m;
+  };
+  if (n0 < 0) return (word(0) << -n0) | ((1u << -n0) - 1);
+  const uint32_t lo = word(n0 >> 5), hi = word((n0 >> 5) + 1);
+  return __funnelshift_r(lo, hi, n0 & 31);
+}
+
+// the 16-byte piece with every bf16 that is not finite replaced by 0
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+  if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+  if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
+  return v;
+}
+
+}  // namespace
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_q,
+               const TreeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t s_base = saddr(smem);
+  uint32_t* tmem_slot = (uint32_t*)(smem + kS_Bar + kNumBars * 8);
+  volatile int* abort_flag = (volatile int*)(smem + kS_Bar + kNumBars * 8 + 4);
+  SegInfo* seg_cache = (SegInfo*)(smem + kS_Seg);
+  auto bar = [&](int i) { return s_base + kS_Bar + 8u * (uint32_t)i; };
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const Ctl ctl{p.err, abort_flag};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(kFull + i), 2);
+      mbar_init(bar(kEmpty + i), 1);
+      mbar_init(bar(kFix + i), 1);
+    }
+    mbar_init(bar(kQFull), 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kSFree + i), 8);
+      mbar_init(bar(kSFull + i), 1);
+    }
+    mbar_init(bar(kPReady), 8);
+    mbar_init(bar(kQEmpty), 1);
+    mbar_init(bar(kPvDone), 1);
+    mbar_init(bar(kRed), 4);
+    mbar_init(bar(kSum), 4);
+    mbar_init(bar(kFinal), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     saddr(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  wait_prior_grid();  // the schedule, Q and the cache rows come from earlier kernels
+
+  const int cluster = blockIdx.x >> 1;
+  const int range = cluster / p.team, member = cluster - range * p.team;
+  int sb = 0, se = 0;
+  if (range < p.header[1]) {
+    sb = p.range_begin[range];
+    se = p.range_begin[range + 1];
+  }
+  for (int i = threadIdx.x; i < min(se - sb, kSegCache); i += blockDim.x)
+    seg_cache[i] = load_segment(p, sb + i, member);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  cluster_sync();  // barriers of both CTAs initialised before any remote traffic
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+  TileWalk walk{&p, seg_cache, sb, sb, se, -1, member, -1, {}};
+  Tile cur, nxt;
+  bool has = walk.next(cur);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------------- TMA producer
+    RowWindow wk, wv;
+    int kt = 0, seg = 0;
+    uint32_t fixes = 0, fix_live = 0;  // per stage: parity of its next fix phase; ever used
+    bool ok = true;
+    const uint32_t first_cta = 0;
+    auto acquire = [&](int& stage) {
+      stage = kt % kStages;
+      if (kt >= kStages) ok = wait(bar(kEmpty + stage), ((kt / kStages) - 1) & 1, ctl);
+      return ok;
+    };
+    auto load_k = [&](const Tile& t) {
+      if (t.first) {
+        // the previous segment's S products are done with Q
+        if (seg > 0) ok = wait(bar(kQEmpty), (seg - 1) & 1, ctl);
+        if (!ok) return;
+        if (elect_one()) {
+          const uint32_t full = peer_addr(bar(kQFull), first_cta);
+          expect_tx_cluster(full, kQBytes);
+          const int y = t.b * p.T * p.H + t.row0 + kMH * (int)rank;
+#pragma unroll
+          for (int k = 0; k < kKStages; ++k)
+            tma_load_pair(s_base + kS_Q + k * kSlabBytes, &tm_q, full, 64 * k, y);
+        }
+        __syncwarp();
+        ++seg;
+      }
+      // this CTA's blocks of keys; one that the segment does not have is another's again (its
+      // scores are masked)
+      const int hb = t.half_blocks();
+      int y[2];
+      for (int j = 0; j < hb; ++j) {
+        const int blk = min((int)rank * hb + j, t.nb - 1);
+        y[j] = wk.get(p, t.b, t.chunk + blk, lane);
+      }
+      for (int k = 0; k < kKStages; ++k, ++kt) {
+        int stage;
+        if (!acquire(stage)) return;
+        if (elect_one()) {
+          const uint32_t full = peer_addr(bar(kFull + stage), first_cta);
+          const uint32_t dst = s_base + kS_Ring + stage * kStageBytes;
+          expect_tx_cluster(full, hb * kSlabBytes);
+          tma_load_pair(dst, &tm_kv, full, 64 * k, y[0]);
+          if (hb > 1) tma_load_pair(dst + kSlabBytes, &tm_kv, full, 64 * k, y[1]);
+        }
+        __syncwarp();
+      }
+    };
+    auto load_v = [&](const Tile& t) {
+      for (int j = 0; j < t.nb; ++j) {
+        const int y = wv.get(p, t.b, t.chunk + j, lane);
+        const bool fix = needs_fix(t, j, p.T);
+        for (int dh = 0; dh < 2; ++dh, ++kt) {
+          int stage;
+          if (!acquire(stage)) return;
+          if (elect_one()) {
+            const uint32_t dst = s_base + kS_Ring + stage * kStageBytes;
+            const int x = 256 * dh + 128 * (int)rank;
+            if (fix) {
+              mbar_expect_tx(bar(kFix + stage), kStageBytes);
+              tma_load(dst, &tm_kv, bar(kFix + stage), x, y);
+              tma_load(dst + kSlabBytes, &tm_kv, bar(kFix + stage), x + 64, y);
+            } else {
+              const uint32_t full = peer_addr(bar(kFull + stage), first_cta);
+              expect_tx_cluster(full, kStageBytes);
+              tma_load_pair(dst, &tm_kv, full, x, y);
+              tma_load_pair(dst + kSlabBytes, &tm_kv, full, x + 64, y);
+            }
+          }
+          __syncwarp();
+          if (fix) {
+            fixes ^= 1u << stage;
+            fix_live |= 1u << stage;
+          }
+        }
+      }
+    };
+    if (has) load_k(cur);
+    while (ok && has) {
+      const bool more = walk.next(nxt);
+      if (more) load_k(nxt);
+      if (ok) load_v(cur);
+      cur = nxt;
+      has = more;
+    }
+    // what this CTA loaded has landed before it may exit: the fixer's stages here, all others
+    // on the first CTA's barriers (whose bytes are both CTAs'), which the first CTA waits for
+    // while the second waits for it at the cluster barrier
+    for (int i = 0; i < kStages; ++i)
+      if (fix_live >> i & 1) drain(bar(kFix + i), ((fixes >> i) & 1) ^ 1, p.err);
+    if (rank == 0) {
+      for (int k = 1; k <= kStages && k <= kt; ++k)
+        drain(bar(kFull + (kt - k) % kStages), ((kt - k) / kStages) & 1, p.err);
+      if (seg > 0) drain(bar(kQFull), (seg - 1) & 1, p.err);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------------------- MMA issue
+    int kt = 0, t = 0, seg = 0;
+    bool ok = true;
+    const uint32_t q_lo = desc_lo(s_base + kS_Q, 16), p_lo = desc_lo(s_base + kS_P, 16);
+    const uint32_t ring_k = desc_lo(s_base + kS_Ring, 16);
+    const uint32_t ring_v = desc_lo(s_base + kS_Ring, kSlabBytes);
+    constexpr uint32_t kStageLo = kStageBytes >> 4, kSlabLo = kSlabBytes >> 4;
+    int tq = 0;  // tiles whose S was issued
+    auto issue_s = [&](const Tile& tl) {
+      if (tl.first) {
+        ok = wait(bar(kQFull), seg & 1, ctl);
+        ++seg;
+      }
+      // the softmax warps copied out what this buffer held two tiles ago
+      if (ok && tq >= 2) ok = wait(bar(kSFree + (tq & 1)), ((tq >> 1) - 1) & 1, ctl);
+      if (!ok) return;
+      const uint32_t d = tmem + 128u * (uint32_t)(tq & 1);
+      const uint32_t id = idesc(128, 128 * tl.half_blocks(), 0);
+#pragma unroll 1
+      for (int k = 0; k < kKStages; ++k, ++kt) {
+        const int stage = kt % kStages;
+        if (!wait(bar(kFull + stage), (kt / kStages) & 1, ctl)) {
+          ok = false;
+          return;
+        }
+        tc_after();
+        if (elect_one()) {
+          const uint32_t a = q_lo + kSlabLo * k, b = ring_k + kStageLo * stage;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma2(d, a + 2 * i, b + 2 * i, id, (k > 0 || i > 0) ? 1u : 0u);
+          commit_both(bar(kEmpty + stage));
+        }
+        __syncwarp();
+      }
+      if (elect_one()) {
+        commit_both(bar(kSFull + (tq & 1)));
+        if (tl.last) commit_both(bar(kQEmpty));
+      }
+      __syncwarp();
+      ++tq;
+    };
+    if (has) issue_s(cur);
+    while (ok && has) {
+      const bool more = walk.next(nxt);
+      if (more) issue_s(nxt);
+      if (ok) ok = wait(bar(kPReady), t & 1, ctl);
+      if (!ok) break;
+      tc_after();
+      // where P's block of keys j lies: the second half of the keys from slab 2 on
+      const uint32_t slab = cur.half_blocks() > 1 ? kSlabLo : 2 * kSlabLo;
+      constexpr uint32_t id = idesc(128, 256, 1);
+#pragma unroll 1
+      for (int j = 0; j < cur.nb && ok; ++j) {
+#pragma unroll 1
+        for (int dh = 0; dh < 2; ++dh, ++kt) {
+          const int stage = kt % kStages;
+          if (!wait(bar(kFull + stage), (kt / kStages) & 1, ctl)) {
+            ok = false;
+            break;
+          }
+          tc_after();
+          if (elect_one()) {
+            const uint32_t a = p_lo + slab * j, b = ring_v + kStageLo * stage;
+            const uint32_t d = tmem + kColO + 128 * dh;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // 16 keys per step; V MN-major: 2 KB apart
+              mma2(d, a + 2 * i, b + 128 * i, id, (cur.first && j == 0 && i == 0) ? 0u : 1u);
+            commit_both(bar(kEmpty + stage));
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) commit_both(bar(kPvDone));
+      __syncwarp();
+      ++t;
+      cur = nxt;
+      has = more;
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------------------------- fixer
+    int kt = has ? kKStages : 0;
+    uint32_t fixes = 0;
+    bool ok = true;
+    const uint32_t full0 = peer_addr(bar(kFull), 0);
+    while (ok && has) {
+      const bool more = walk.next(nxt);
+      if (more) kt += kKStages;
+      for (int j = 0; j < cur.nb && ok; ++j) {
+        if (!needs_fix(cur, j, p.T)) {
+          kt += 2;
+          continue;
+        }
+        // rows of the block: up to `from` are the prefix; from `to` on they lie past the end
+        const int from = max(cur.len - p.T - (cur.chunk + j) * kRows, 0);
+        const int to = min(cur.len - (cur.chunk + j) * kRows, kRows);
+        for (int dh = 0; dh < 2; ++dh, ++kt) {
+          const int stage = kt % kStages;
+          if (!wait(bar(kFix + stage), fixes >> stage & 1, ctl)) {
+            ok = false;
+            break;
+          }
+          fixes ^= 1u << stage;
+          uint8_t* st = smem + kS_Ring + stage * kStageBytes;
+          // 16-byte pieces of rows from .. 63 of both slabs
+          for (int i = 8 * from + lane; i < 8 * kRows; i += 32) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              uint4* v = (uint4*)(st + s * kSlabBytes) + i;
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (i < 8 * to) {
+                const uint4 y = *v;
+                x = make_uint4(finite2(y.x), finite2(y.y), finite2(y.z), finite2(y.w));
+                if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
+              }
+              *v = x;
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_peer(full0 + 8u * (uint32_t)stage);
+          __syncwarp();
+        }
+      }
+      cur = nxt;
+      has = more;
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- softmax, rescale, epilogue
+    // TMEM lane 32 * quad + lane: query row `row` of this CTA, half `half` of the tile's keys
+    // in S, and of each 256 latent dims in O
+    const int quad = warp & 3, half = quad >> 1;
+    const int row = 32 * (quad & 1) + lane;
+    const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16);
+    const float c2 = p.scale * 1.4426950408889634f;  // scores in log2 units
+    float* red = (float*)(smem + kS_Red);
+    float* sum = (float*)(smem + kS_Sum);
+    const uint32_t p_row = s_base + kS_P + (uint32_t)(2 * half) * kSlabBytes + (uint32_t)row * 128;
+    const uint32_t box = s_base + kS_P + (uint32_t)(2 * half) * kSlabBytes +
+                         (uint32_t)(quad & 1) * 4096;  // written by this warp alone
+    const uint32_t s_free = peer_addr(bar(kSFree), 0), p_ready = peer_addr(bar(kPReady), 0);
+    int t = 0, seg = 0;
+    float m_ref = 0.f, l = 0.f;
+    while (has) {
+      const int my_row = cur.row0 + kMH * (int)rank + row;  // of the sequence's T * H
+      if (!wait(bar(kSFull + (t & 1)), (t >> 1) & 1, ctl)) break;
+      tc_after();
+      uint32_t v[128];
+      tmem_ld128(tq + 128u * (uint32_t)(t & 1), v);
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_peer(s_free + 8u * (uint32_t)(t & 1));
+      const int hb = cur.half_blocks();
+      const int key0 = half * hb * kRows;  // this thread's first key of the tile
+      const int lim = min(cur.ntok - key0, hb * kRows);
+      const int node0 = cur.chunk * kRows + key0 - (cur.len - p.T);  // drafted node of column 0
+      if (lim < 128 || node0 + 127 >= 0) {
+        const int tok = min(my_row / p.H, p.T - 1);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t seen = seen_word(p, cur.b, tok, node0 + 32 * w);
+          const int left = lim - 32 * w;
+          seen = left <= 0 ? 0u : left < 32 ? seen & ((1u << left) - 1) : seen;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!(seen >> k & 1)) v[32 * w + k] = 0xff800000u;
+        }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 128; k += 8)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mx[c] = fmax3(mx[c], __uint_as_float(v[k + 2 * c]), __uint_as_float(v[k + 2 * c + 1]));
+      float* rt = red + (t & 1) * 2 * kMH;
+      rt[half * kMH + row] = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kRed));
+      if (!wait(bar(kRed), t & 1, ctl)) break;
+      // a row that sees nothing yet keeps a finite reference: all its weights are exp2(-inf) = 0
+      const float mt = fmaxf(fmaxf(rt[row], rt[kMH + row]) * c2, -1e30f);
+      float alpha = 1.f;
+      if (cur.first) {
+        m_ref = mt;
+        l = 0.f;
+      } else if (mt > m_ref + 8.f) {
+        alpha = ex2(m_ref - mt);
+        m_ref = mt;
+      }
+      const float2 c2x2 = make_float2(c2, c2), nm = make_float2(-m_ref, -m_ref);
+      float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 64; ++k) {
+        const float2 x = __ffma2_rn(
+            make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2x2, nm);
+        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+        if (k & 1) s1 = __fadd2_rn(s1, e);
+        else s0 = __fadd2_rn(s0, e);
+        v[k] = pack_bf16(e.x, e.y);
+      }
+      l = l * alpha + ((s0.x + s0.y) + (s1.x + s1.y));
+      // P . V of the previous tile is complete: P may be overwritten and O rescaled
+      if (t > 0 && !wait(bar(kPvDone), (t - 1) & 1, ctl)) break;
+      if (!cur.first && __any_sync(0xffffffffu, alpha != 1.f)) {
+        tc_after();
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(tq + kColO + 32 * ch, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st32(tq + kColO + 32 * ch, o);
+        }
+        tmem_wait_st();
+        tc_before();
+      }
+      // P in the A-operand layout (K-major, 128-byte rows swizzled by row % 8)
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb) {
+        if (cb < hb) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             p_row + cb * kSlabBytes + 16u * (uint32_t)(u ^ (row & 7))),
+                         "r"(v[32 * cb + 4 * u]), "r"(v[32 * cb + 4 * u + 1]),
+                         "r"(v[32 * cb + 4 * u + 2]), "r"(v[32 * cb + 4 * u + 3])
+                         : "memory");
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_peer(p_ready);
+
+      if (cur.last) {
+        // the row's other half of the keys
+        float* st = sum + (seg & 1) * 2 * kMH;
+        st[half * kMH + row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSum));
+        if (!wait(bar(kSum), seg & 1, ctl)) break;
+        const float total = st[row] + st[kMH + row];
+        ++seg;
+        const bool mine = my_row < p.T * p.H;
+        const size_t out_row = (size_t)cur.b * p.T * p.H + my_row;
+        if (half == 0) {
+          const float lse = (m_ref + __log2f(total)) * 0.6931471805599453f;
+          if (cur.slot >= 0) p.part_lse[(size_t)cur.slot * kM + kMH * rank + row] = lse;
+          else if (mine && p.lse) p.lse[out_row] = lse;
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        if (!wait(bar(kPvDone), t & 1, ctl)) break;
+        tc_after();
+        // O / l leaves through this warp's own 4 KB of P's buffer (32 rows x 32 columns, 16-byte
+        // groups swizzled by row % 8), read back four rows per instruction as whole lines
+        const int rsub = lane >> 3, g = (lane & 7) ^ rsub;
+        float* dst = (cur.slot >= 0
+                          ? p.part_o + ((size_t)cur.slot * kM + kMH * rank + 32 * (quad & 1)) * kR
+                          : p.latent + (out_row - lane) * kR) +
+                     (size_t)rsub * kR + 4 * (lane & 7);
+        const int rows = cur.slot >= 0 ? 32 : p.T * p.H - (my_row - lane);  // rows to write
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(tq + kColO + 32 * ch, o);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             box + 128u * (uint32_t)lane + 16u * (uint32_t)(u ^ (lane & 7))),
+                         "f"(__uint_as_float(o[4 * u]) * inv),
+                         "f"(__uint_as_float(o[4 * u + 1]) * inv),
+                         "f"(__uint_as_float(o[4 * u + 2]) * inv),
+                         "f"(__uint_as_float(o[4 * u + 3]) * inv)
+                         : "memory");
+          __syncwarp();
+          // columns 32 ch ..: dims 256 (ch / 4) + 128 half + 32 (ch % 4)
+          float* line = dst + 256 * (ch >> 2) + 128 * half + 32 * (ch & 3);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 x;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                         : "r"(box + 128u * (uint32_t)(4 * i + rsub) +
+                               16u * (uint32_t)((i & 1) ? g ^ 4 : g))
+                         : "memory");
+            if (4 * i + rsub < rows) *(float4*)(line + (size_t)(4 * i) * kR) = x;
+          }
+          __syncwarp();
+        }
+        tc_before();
+      }
+      ++t;
+      has = walk.next(cur);
+    }
+  }
+
+  // ---------------------------------------------------------------------------------- teardown
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 1 && rank == 0) {
+    if (elect_one()) commit_one(bar(kFinal));  // completes once every MMA issued here is done
+    __syncwarp();
+    drain(bar(kFinal), 0, p.err);
+  }
+  cluster_sync();  // no MMA, load or remote arrival of the pair is under way any more
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------------------------------
+// Plan. Items are (sequence, group of `team` tiles of query rows); their 64-row chunks of keys
+// are laid end to end and cut into R ranges of equal size, one per team of clusters. The members
+// of a team walk the same chunks at the same time, each for its own tile of query rows, so the
+// cache rows that several tiles need come from HBM once and from L2 for the others.
+// ------------------------------------------------------------------------------------------
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeParams p) {
+  __shared__ int s_a[32], s_b[32], s_carry[3];
+  const int tid = threadIdx.x;
+  const int items = p.batch * p.groups;
+  wait_prior_grid();
+  if (tid < 3) s_carry[tid] = 0;
+  __syncthreads();
+  for (int base = 0; base < items; base += kPlanThreads) {
+    const int it = base + tid;
+    int nch = 0;
+    if (it < items) {
+      const int b = it / p.groups;
+      const int len = tree_length(p, b, it == b * p.groups);
+      nch = (len + kChunk - 1) / kChunk;
+      p.item_len[it] = len;
+    }
+    int inc = nch, dummy = 0;
+    block_scan2<kPlanThreads>(s_a, s_b, inc, dummy);
+    if (it < items) p.item_chunk0[it] = s_carry[0] + inc - nch;
+    __syncthreads();
+    if (tid == kPlanThreads - 1) s_carry[0] += inc;
+    __syncthreads();
+  }
+  const int C = s_carry[0];
+  const int R = min(C, p.ranges);
+  __syncthreads();
+  if (tid == 0) s_carry[0] = 0;
+  __syncthreads();
+  for (int base = 0; base < items; base += kPlanThreads) {
+    const int it = base + tid;
+    int nseg = 0, x = 0, e = 0;
+    if (it < items) {
+      const int nch = (p.item_len[it] + kChunk - 1) / kChunk;
+      x = p.item_chunk0[it];
+      e = x + nch;
+      if (nch > 0) nseg = 1 + starts_below(e, R, C) - starts_below(x + 1, R, C);
+    }
+    const int nslot = nseg >= 2 ? nseg : 0;
+    int inc_seg = nseg, inc_slot = nslot;
+    block_scan2<kPlanThreads>(s_a, s_b, inc_seg, inc_slot);
+    if (it < items) {
+      const int first = s_carry[0] + inc_seg - nseg;
+      const int slot0 = s_carry[1] + inc_slot - nslot;
+      p.item_slot0[it] = slot0;
+      p.item_nseg[it] = nseg;
+      if (nseg != 1) p.merge_list[atomicAdd(&s_carry[2], 1)] = it;  // in any order
+      int q = starts_below(x + 1, R, C);  // first range starting after x
+      int lo = x;
+      for (int k = 0; k < nseg; ++k) {
+        const int hi = (k == nseg - 1) ? e : range_start(q, R, C);
+        p.segments[first + k] = Segment{it, lo, hi, nseg >= 2 ? slot0 + k : -1};
+        const int qs = starts_below(lo + 1, R, C) - 1;  // range containing chunk lo
+        if (qs >= 0 && range_start(qs, R, C) == lo) p.range_begin[qs] = first + k;
+        lo = hi;
+        ++q;
+      }
+    }
+    __syncthreads();
+    if (tid == kPlanThreads - 1) {
+      s_carry[0] += inc_seg;
+      s_carry[1] += inc_slot;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.header[0] = s_carry[0];  // segments
+    p.header[1] = R;           // ranges in use
+    p.header[2] = s_carry[2];  // items of merge_list
+    p.range_begin[R] = s_carry[0];
+  }
+}
+
+// Merge of the items in merge_list: those cut into several segments, and those without rows
+// (zeros). A warp per query row, dealt round a fixed grid.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_combine_kernel(const TreeParams p) {
+  __shared__ float s_w[kMergeWarps][kRanges];
+  wait_prior_grid();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = p.team * kM;  // query rows of an item
+  const int64_t total = (int64_t)p.header[2] * per;
+  float* w = s_w[warp];
+  for (int64_t i = (int64_t)blockIdx.x * kMergeWarps + warp; i < total;
+       i += (int64_t)gridDim.x * kMergeWarps) {
+    const int it = p.merge_list[i / per], m = (int)(i % per);
+    const int b = it / p.groups, row = (it - b * p.groups) * per + m;
+    if (row >= p.T * p.H) continue;
+    const size_t at = (size_t)b * p.T * p.H + row;
+    const int nseg = p.item_nseg[it];
+    // partial row of segment k: slot (slot0 + k) * team + m / kM, row m % kM
+    const size_t part0 = ((size_t)p.item_slot0[it] * p.team) * kM + m, step = (size_t)p.team * kM;
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int k = lane; k < nseg; k += 32) {
+      const float x = p.part_lse[part0 + k * step];
+      nan |= x != x;
+      mx = fmaxf(mx, x);
+    }
+    mx = warp_max(mx);
+    nan = __any_sync(0xffffffffu, nan);
+    float z = 0.f;
+    for (int k = lane; k < nseg; k += 32) {
+      const float x = p.part_lse[part0 + k * step];
+      const float e = x == -INFINITY ? 0.f : expf(x - mx);
+      w[k] = e;
+      z += e;
+    }
+    z = warp_sum(z);
+    const bool empty = mx == -INFINITY && !nan;
+    const float inv = empty ? 0.f : 1.f / z;
+    __syncwarp();
+    float4 acc[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!empty) {
+#pragma unroll 2
+      for (int k = 0; k < nseg; ++k) {
+        const float e = w[k] * inv;
+        const float4* src = (const float4*)(p.part_o + (part0 + k * step) * kR) + lane;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 v = __ldcs(src + 32 * u);
+          acc[u].x = fmaf(e, v.x, acc[u].x);
+          acc[u].y = fmaf(e, v.y, acc[u].y);
+          acc[u].z = fmaf(e, v.z, acc[u].z);
+          acc[u].w = fmaf(e, v.w, acc[u].w);
+        }
+      }
+    }
+    float4* dst = (float4*)(p.latent + at * kR) + lane;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) dst[32 * u] = acc[u];
+    if (lane == 0 && p.lse) p.lse[at] = empty ? -INFINITY : mx + logf(z);
+    __syncwarp();
+  }
+}
+
+}  // namespace
+
+bool tree_tc_supported(const mla_config& c) {
+  return c.dtype == MLA_BF16 && c.kv_rank == kR && c.rope_dim == kDR && c.block_size % kRows == 0;
+}
+
+// Clusters that work together on one item: as many as there are tiles of query rows, if the teams
+// then leave few of the 74 clusters idle, else a number that does.
+void tree_team(int tiles, int* team, int* ranges) {
+  int best = 1;
+  for (int g = 2; g <= tiles && g <= kRanges; ++g) {
+    const int groups = (tiles + g - 1) / g;
+    // share of the clusters' time that is used: whole teams, and tiles in the last group
+    const double used = (double)(g * (kRanges / g)) / kRanges * tiles / ((double)groups * g);
+    if (used >= 0.94) best = g;
+  }
+  *team = best;
+  *ranges = kRanges / best;
+}
+
+cudaError_t launch_tree_tc(const mla_config& c, const TreeParams& p, cudaStream_t st) {
+  (void)c;
+  CUtensorMap kv, qm;
+  if (!make_bf16_map(&kv, p.pool, kD, (uint64_t)p.num_blocks * p.bs, kD * 2, kRows) ||
+      !make_bf16_map(&qm, p.q, kD, (uint64_t)p.BT * p.H, kD * 2, kMH))
+    return cudaErrorInvalidValue;
+  // the shared-memory attribute applies to the device current when it is set: once per device
+  static std::atomic<unsigned long long> attr_devices{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (!bit || !(attr_devices.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_devices.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  e = launch_pdl(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_tc_kernel, dim3(2 * kRanges), dim3(kThreads), kSmemBytes, st, kv, qm, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_combine_kernel, dim3(2 * 148), dim3(kMergeWarps * 32), 0, st, p);
+  return e;
+}
+
+}  // namespace mla
