@@ -31,9 +31,8 @@
 // row held NaN, so the V stages that hold drafted rows (or rows past the end) pass through the
 // fixer warp, which replaces what is not finite by 0 before the MMA may read it.
 //
-// Warps: 0 TMA, 1 MMA issue (in the pair's first CTA), 2 fixer, 4-7 softmax and epilogue. Every
-// wait is bounded: on timeout the kernel sets MLA_DEV_WAIT_TIMEOUT, drains what it issued, frees
-// TMEM and returns. No TMA multicast is used.
+// Warps: 0 and 3 TMA, 1 MMA issue (in the pair's first CTA), 2 fixer, 4-7 softmax and epilogue. Every wait is bounded: on timeout the kernel sets MLA_DEV_WAIT_TIMEOUT, lets what it
+// issued end, frees TMEM and returns. No TMA multicast is used.
 #include <atomic>
 
 #include "plan_body.cuh"
@@ -61,6 +60,7 @@ constexpr int kThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;           // S buffers at columns 0 and 128
 constexpr unsigned long long kTimeoutNs = 1000000000ull;  // 1 s per wait
+constexpr unsigned long long kSettleNs = 20000000ull;     // 20 ms after an abort
 
 constexpr int kS_Ring = 0;
 constexpr int kS_Q = kS_Ring + kStages * kStageBytes;     // 112 KB
@@ -133,18 +133,11 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
-__device__ __forceinline__ void expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;"
-      "\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
+// Arrival on a barrier of either CTA of the pair. CTA scope on purpose: a release of cluster scope
+// waits for everything the thread has in flight (about 1000 cycles here); what the arrivals
+// order is ordered before them (tcgen05.wait::ld, fence.proxy.async by each writing thread).
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 struct Ctl {
@@ -157,7 +150,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t* 
                                        volatile int* abort) {
   uint64_t t0 = 0;
   for (int it = 0;; ++it) {
-    if (__all_sync(0xffffffffu, try_cluster(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
     if (it == 0) t0 = globaltimer();
     const bool late = (globaltimer() - t0) > kTimeoutNs;
     if (__any_sync(0xffffffffu, *abort != 0 || late)) {
@@ -170,7 +163,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t* 
   }
 }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
-  if (__all_sync(0xffffffffu, try_cluster(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   return wait_slow(bar, parity, c.err, c.abort);
 }
 // Bounded wait for a phase that normally completed long ago (drains at teardown).
@@ -178,7 +171,7 @@ __device__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
   const uint64_t t0 = globaltimer();
   bool done = false;
   while (!done && globaltimer() - t0 < kTimeoutNs)
-    done = __all_sync(0xffffffffu, try_cluster(bar, parity));
+    done = __all_sync(0xffffffffu, mbar_try(bar, parity));
   if (!done && (threadIdx.x & 31) == 0) set_error(err, MLA_DEV_WAIT_TIMEOUT);
 }
 
@@ -255,6 +248,21 @@ struct RowWindow {
       id = 0;
     }
     return id * p.bs + (chunk - at * per) * kRows;
+  }
+};
+
+// A place in the ring: its stage, the parity of the stage's use, and how many places lie before.
+struct Cursor {
+  int stage = 0;
+  uint32_t round = 0;
+  int used = 0;
+  __device__ __forceinline__ void move(int n) {
+    used += n;
+    stage += n;
+    while (stage >= kStages) {
+      stage -= kStages;
+      round ^= 1;
+    }
   }
 };
 
@@ -355,81 +363,91 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   Tile cur, nxt;
   bool has = walk.next(cur);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------------- TMA producer
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------------------- TMA: Q, K and V
+    // Two warps fill the ring, every second place each: one alone took longer for a tile's 17
+    // stages than the products that use them. (A warp for K and one for V would not do: a parity
+    // wait has to be within one phase of the last one, and K runs ahead of V by more.)
     RowWindow wk, wv;
-    int kt = 0, seg = 0;
-    uint32_t fixes = 0, fix_live = 0;  // per stage: parity of its next fix phase; ever used
+    Cursor at;
+    int seg = 0;
     bool ok = true;
-    const uint32_t first_cta = 0;
-    auto acquire = [&](int& stage) {
-      stage = kt % kStages;
-      if (kt >= kStages) ok = wait(bar(kEmpty + stage), ((kt / kStages) - 1) & 1, ctl);
+    const int turn = warp == 0 ? 0 : 1;
+    const uint32_t bars0 = peer_addr(bar(0), 0);
+    // Whether this place is this warp's; if so, once its stage is free.
+    auto mine = [&]() {
+      if ((at.used & 1) != turn) return false;
+      if (at.used >= kStages) ok = wait(bar(kEmpty + at.stage), at.round ^ 1, ctl);
       return ok;
+    };
+    // Loads for a stage are counted on the first CTA's barriers: it expects the bytes of both
+    // CTAs, and gives both arrivals, which the fixers give otherwise.
+    auto arm = [&](int i, uint32_t bytes) {
+      if (rank == 0) {
+        mbar_arrive(bar(i));
+        mbar_expect_tx(bar(i), bytes);
+      }
     };
     auto load_k = [&](const Tile& t) {
       if (t.first) {
-        // the previous segment's S products are done with Q
-        if (seg > 0) ok = wait(bar(kQEmpty), (seg - 1) & 1, ctl);
-        if (!ok) return;
-        if (elect_one()) {
-          const uint32_t full = peer_addr(bar(kQFull), first_cta);
-          expect_tx_cluster(full, kQBytes);
-          const int y = t.b * p.T * p.H + t.row0 + kMH * (int)rank;
+        if (turn == 0) {
+          // the previous segment's S products are done with Q
+          if (seg > 0) ok = wait(bar(kQEmpty), (seg - 1) & 1, ctl);
+          if (!ok) return;
+          if (elect_one()) {
+            arm(kQFull, 2 * kQBytes);
+            const int y = t.b * p.T * p.H + t.row0 + kMH * (int)rank;
 #pragma unroll
-          for (int k = 0; k < kKStages; ++k)
-            tma_load_pair(s_base + kS_Q + k * kSlabBytes, &tm_q, full, 64 * k, y);
+            for (int k = 0; k < kKStages; ++k)
+              tma_load_pair(s_base + kS_Q + k * kSlabBytes, &tm_q, bars0 + 8 * kQFull, 64 * k, y);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         ++seg;
       }
-      // this CTA's blocks of keys; one that the segment does not have is another's again (its
+      // this CTA's blocks of keys; in place of one that the segment does not have, its last (the
       // scores are masked)
-      const int hb = t.half_blocks();
-      int y[2];
-      for (int j = 0; j < hb; ++j) {
-        const int blk = min((int)rank * hb + j, t.nb - 1);
-        y[j] = wk.get(p, t.b, t.chunk + blk, lane);
-      }
-      for (int k = 0; k < kKStages; ++k, ++kt) {
-        int stage;
-        if (!acquire(stage)) return;
-        if (elect_one()) {
-          const uint32_t full = peer_addr(bar(kFull + stage), first_cta);
-          const uint32_t dst = s_base + kS_Ring + stage * kStageBytes;
-          expect_tx_cluster(full, hb * kSlabBytes);
-          tma_load_pair(dst, &tm_kv, full, 64 * k, y[0]);
-          if (hb > 1) tma_load_pair(dst + kSlabBytes, &tm_kv, full, 64 * k, y[1]);
+      const int hb = t.half_blocks(), j0 = (int)rank * hb;
+      const int y0 = wk.get(p, t.b, t.chunk + min(j0, t.nb - 1), lane);
+      const int y1 = wk.get(p, t.b, t.chunk + min(j0 + hb - 1, t.nb - 1), lane);
+#pragma unroll 1
+      for (int k = 0; k < kKStages && ok; ++k) {
+        if (mine()) {
+          if (elect_one()) {
+            const uint32_t full = bars0 + 8u * (uint32_t)(kFull + at.stage);
+            const uint32_t dst = s_base + kS_Ring + at.stage * kStageBytes;
+            arm(kFull + at.stage, 2 * hb * kSlabBytes);
+            tma_load_pair(dst, &tm_kv, full, 64 * k, y0);
+            if (hb > 1) tma_load_pair(dst + kSlabBytes, &tm_kv, full, 64 * k, y1);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        at.move(1);
       }
     };
     auto load_v = [&](const Tile& t) {
-      for (int j = 0; j < t.nb; ++j) {
+      for (int j = 0; j < t.nb && ok; ++j) {
         const int y = wv.get(p, t.b, t.chunk + j, lane);
         const bool fix = needs_fix(t, j, p.T);
-        for (int dh = 0; dh < 2; ++dh, ++kt) {
-          int stage;
-          if (!acquire(stage)) return;
-          if (elect_one()) {
-            const uint32_t dst = s_base + kS_Ring + stage * kStageBytes;
-            const int x = 256 * dh + 128 * (int)rank;
-            if (fix) {
-              mbar_expect_tx(bar(kFix + stage), kStageBytes);
-              tma_load(dst, &tm_kv, bar(kFix + stage), x, y);
-              tma_load(dst + kSlabBytes, &tm_kv, bar(kFix + stage), x + 64, y);
-            } else {
-              const uint32_t full = peer_addr(bar(kFull + stage), first_cta);
-              expect_tx_cluster(full, kStageBytes);
+#pragma unroll 1
+        for (int dh = 0; dh < 2 && ok; ++dh) {
+          if (mine()) {
+            if (elect_one()) {
+              const uint32_t dst = s_base + kS_Ring + at.stage * kStageBytes;
+              const int x = 256 * dh + 128 * (int)rank;
+              uint32_t full = bars0 + 8u * (uint32_t)(kFull + at.stage);
+              if (fix) {
+                full = bar(kFix + at.stage);
+                mbar_expect_tx(full, kStageBytes);
+              } else {
+                arm(kFull + at.stage, 2 * kStageBytes);
+              }
               tma_load_pair(dst, &tm_kv, full, x, y);
               tma_load_pair(dst + kSlabBytes, &tm_kv, full, x + 64, y);
             }
+            __syncwarp();
           }
-          __syncwarp();
-          if (fix) {
-            fixes ^= 1u << stage;
-            fix_live |= 1u << stage;
-          }
+          at.move(1);
         }
       }
     };
@@ -441,19 +459,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       cur = nxt;
       has = more;
     }
-    // what this CTA loaded has landed before it may exit: the fixer's stages here, all others
-    // on the first CTA's barriers (whose bytes are both CTAs'), which the first CTA waits for
-    // while the second waits for it at the cluster barrier
-    for (int i = 0; i < kStages; ++i)
-      if (fix_live >> i & 1) drain(bar(kFix + i), ((fixes >> i) & 1) ^ 1, p.err);
-    if (rank == 0) {
-      for (int k = 1; k <= kStages && k <= kt; ++k)
-        drain(bar(kFull + (kt - k) % kStages), ((kt - k) / kStages) & 1, p.err);
-      if (seg > 0) drain(bar(kQFull), (seg - 1) & 1, p.err);
-    }
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------------------- MMA issue
-    int kt = 0, t = 0, seg = 0;
+    Cursor at;
+    int t = 0, seg = 0;
     bool ok = true;
     const uint32_t q_lo = desc_lo(s_base + kS_Q, 16), p_lo = desc_lo(s_base + kS_P, 16);
     const uint32_t ring_k = desc_lo(s_base + kS_Ring, 16);
@@ -471,20 +480,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       const uint32_t d = tmem + 128u * (uint32_t)(tq & 1);
       const uint32_t id = idesc(128, 128 * tl.half_blocks(), 0);
 #pragma unroll 1
-      for (int k = 0; k < kKStages; ++k, ++kt) {
-        const int stage = kt % kStages;
-        if (!wait(bar(kFull + stage), (kt / kStages) & 1, ctl)) {
+      for (int k = 0; k < kKStages; ++k) {
+        if (!wait(bar(kFull + at.stage), at.round, ctl)) {
           ok = false;
           return;
         }
         tc_after();
         if (elect_one()) {
-          const uint32_t a = q_lo + kSlabLo * k, b = ring_k + kStageLo * stage;
+          const uint32_t a = q_lo + kSlabLo * k, b = ring_k + kStageLo * at.stage;
 #pragma unroll
           for (int i = 0; i < 4; ++i) mma2(d, a + 2 * i, b + 2 * i, id, (k > 0 || i > 0) ? 1u : 0u);
-          commit_both(bar(kEmpty + stage));
+          commit_both(bar(kEmpty + at.stage));
         }
         __syncwarp();
+        at.move(1);
       }
       if (elect_one()) {
         commit_both(bar(kSFull + (tq & 1)));
@@ -506,22 +515,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
 #pragma unroll 1
       for (int j = 0; j < cur.nb && ok; ++j) {
 #pragma unroll 1
-        for (int dh = 0; dh < 2; ++dh, ++kt) {
-          const int stage = kt % kStages;
-          if (!wait(bar(kFull + stage), (kt / kStages) & 1, ctl)) {
+        for (int dh = 0; dh < 2; ++dh) {
+          if (!wait(bar(kFull + at.stage), at.round, ctl)) {
             ok = false;
             break;
           }
           tc_after();
           if (elect_one()) {
-            const uint32_t a = p_lo + slab * j, b = ring_v + kStageLo * stage;
+            const uint32_t a = p_lo + slab * j, b = ring_v + kStageLo * at.stage;
             const uint32_t d = tmem + kColO + 128 * dh;
 #pragma unroll
             for (int i = 0; i < 4; ++i)  // 16 keys per step; V MN-major: 2 KB apart
               mma2(d, a + 2 * i, b + 128 * i, id, (cur.first && j == 0 && i == 0) ? 0u : 1u);
-            commit_both(bar(kEmpty + stage));
+            commit_both(bar(kEmpty + at.stage));
           }
           __syncwarp();
+          at.move(1);
         }
       }
       if (!ok) break;
@@ -533,23 +542,24 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     }
   } else if (warp == 2) {
     // -------------------------------------------------------------------------------- fixer
-    int kt = has ? kKStages : 0;
+    Cursor at;
+    if (has) at.move(kKStages);
     uint32_t fixes = 0;
     bool ok = true;
     const uint32_t full0 = peer_addr(bar(kFull), 0);
     while (ok && has) {
       const bool more = walk.next(nxt);
-      if (more) kt += kKStages;
+      if (more) at.move(kKStages);
       for (int j = 0; j < cur.nb && ok; ++j) {
         if (!needs_fix(cur, j, p.T)) {
-          kt += 2;
+          at.move(2);
           continue;
         }
         // rows of the block: up to `from` are the prefix; from `to` on they lie past the end
         const int from = max(cur.len - p.T - (cur.chunk + j) * kRows, 0);
         const int to = min(cur.len - (cur.chunk + j) * kRows, kRows);
-        for (int dh = 0; dh < 2; ++dh, ++kt) {
-          const int stage = kt % kStages;
+        for (int dh = 0; dh < 2; ++dh) {
+          const int stage = at.stage;
           if (!wait(bar(kFix + stage), fixes >> stage & 1, ctl)) {
             ok = false;
             break;
@@ -572,8 +582,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
           }
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive_peer(full0 + 8u * (uint32_t)stage);
+          if (lane == 0) arrive_pair(full0 + 8u * (uint32_t)stage);
           __syncwarp();
+          at.move(1);
         }
       }
       cur = nxt;
@@ -597,28 +608,34 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     float m_ref = 0.f, l = 0.f;
     while (has) {
       const int my_row = cur.row0 + kMH * (int)rank + row;  // of the sequence's T * H
+      const int hb = cur.half_blocks();
+      const int key0 = half * hb * kRows;  // this thread's first key of the tile
+      const int lim = min(cur.ntok - key0, hb * kRows);
+      const int node0 = cur.chunk * kRows + key0 - (cur.len - p.T);  // drafted node of column 0
+      const bool masked = lim < 128 || node0 + 127 >= 0;
+      uint32_t seen[4];
+      if (masked) {
+        const int tok = min(my_row / p.H, p.T - 1);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int left = lim - 32 * w;
+          const uint32_t bits = left <= 0 ? 0u : seen_word(p, cur.b, tok, node0 + 32 * w);
+          seen[w] = left <= 0 ? 0u : left < 32 ? bits & ((1u << left) - 1) : bits;
+        }
+      }
       if (!wait(bar(kSFull + (t & 1)), (t >> 1) & 1, ctl)) break;
       tc_after();
       uint32_t v[128];
       tmem_ld128(tq + 128u * (uint32_t)(t & 1), v);
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_peer(s_free + 8u * (uint32_t)(t & 1));
-      const int hb = cur.half_blocks();
-      const int key0 = half * hb * kRows;  // this thread's first key of the tile
-      const int lim = min(cur.ntok - key0, hb * kRows);
-      const int node0 = cur.chunk * kRows + key0 - (cur.len - p.T);  // drafted node of column 0
-      if (lim < 128 || node0 + 127 >= 0) {
-        const int tok = min(my_row / p.H, p.T - 1);
+      if (lane == 0) arrive_pair(s_free + 8u * (uint32_t)(t & 1));
+      if (masked) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t seen = seen_word(p, cur.b, tok, node0 + 32 * w);
-          const int left = lim - 32 * w;
-          seen = left <= 0 ? 0u : left < 32 ? seen & ((1u << left) - 1) : seen;
+        for (int w = 0; w < 4; ++w)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (!(seen >> k & 1)) v[32 * w + k] = 0xff800000u;
-        }
+            if (!(seen[w] >> k & 1)) v[32 * w + k] = 0xff800000u;
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -683,7 +700,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive_peer(p_ready);
+      if (lane == 0) arrive_pair(p_ready);
 
       if (cur.last) {
         // the row's other half of the keys
@@ -712,10 +729,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
                           : p.latent + (out_row - lane) * kR) +
                      (size_t)rsub * kR + 4 * (lane & 7);
         const int rows = cur.slot >= 0 ? 32 : p.T * p.H - (my_row - lane);  // rows to write
+        // the next chunk's tensor-memory load is under way while this one is staged and stored
+        uint32_t o[32], on[32];
+        tmem_ld32(tq + kColO, o);
 #pragma unroll 1
         for (int ch = 0; ch < 8; ++ch) {
-          uint32_t o[32];
-          tmem_ld32(tq + kColO + 32 * ch, o);
+          if (ch + 1 < 8) tmem_ld32_async(tq + kColO + 32 * (ch + 1), on);
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
@@ -739,6 +758,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
             if (4 * i + rsub < rows) *(float4*)(line + (size_t)(4 * i) * kR) = x;
           }
           __syncwarp();
+          if (ch + 1 < 8) {
+            tmem_wait_ld(on);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = on[i];
+          }
         }
         tc_before();
       }
@@ -751,6 +775,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   tc_before();
   __syncthreads();
   tc_after();
+  if (*abort_flag != 0) {
+    // some loads may be under way without a wait for them: each has landed long before this
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < kSettleNs) {
+    }
+  }
   if (warp == 1 && rank == 0) {
     if (elect_one()) commit_one(bar(kFinal));  // completes once every MMA issued here is done
     __syncwarp();
