@@ -13,12 +13,14 @@
 // SM that computed it: nothing but MMA operands crosses between the two.
 //
 // Per 256 keys a CTA streams 9 stages of K (128 keys x 64 dims) and 8 of V (64 keys x 128 dims), 16
-// KB each, through one ring in the order the products use them: K(0), K(1), V(0), K(2), V(1) ...
-// so the scores of tile t + 1 run on the tensor core while the softmax of tile t does, and
-// P . V of tile t while the softmax of tile t + 1 reads its scores. Four MMAs (64 cycles each)
-// use a stage. The whole MMA warp runs the issue loop and one elected lane issues: with a single
-// thread in a divergent branch an MMA took 132 cycles to issue whatever its size (measured),
-// with the warp converged 45.
+// KB each, through a ring for each. One warp issues the score products and another P . V, so the
+// scores of tile t + 1 and P . V of tile t share the tensor core while the softmax of tile t + 1
+// waits for the one and that of tile t + 2 ... What bounds the tensor core's use is not the data but
+// the issue: four MMAs of 64 cycles each use a stage, and the wait, the four issues and the commit
+// take a warp about 400 cycles (386 per K stage and 435 per V stage measured with one warp for
+// both, a tile then 7.9k cycles for 4.35k of products). The whole warp runs the issue loop and
+// one elected lane issues: from a single thread in a divergent branch an MMA took 132 cycles to
+// issue whatever its size, with the warp converged and the descriptors' low words at hand 25.
 //
 // Softmax: four warps, a thread holds one query row and half of the tile's keys (TMEM lane), two
 // threads of a row exchange their maxima; base-2 exponents, the running maximum moved only when
@@ -31,7 +33,8 @@
 // row held NaN, so the V stages that hold drafted rows (or rows past the end) pass through the
 // fixer warp, which replaces what is not finite by 0 before the MMA may read it.
 //
-// Warps: 0 and 3 TMA, 1 MMA issue (in the pair's first CTA), 2 fixer, 4-7 softmax and epilogue. Every wait is bounded: on timeout the kernel sets MLA_DEV_WAIT_TIMEOUT, lets what it
+// Warps: 0 TMA of Q and K, 3 of V; 1 issues S, 2 issues P . V (both in the pair's first CTA); 4-7
+// softmax and epilogue; 8 fixer. Every wait is bounded: on timeout the kernel sets MLA_DEV_WAIT_TIMEOUT, lets what it
 // issued end, frees TMEM and returns. No TMA multicast is used.
 #include <atomic>
 
@@ -52,18 +55,25 @@ constexpr int kRows = 64;                 // cache rows per block of keys
 constexpr int kTileBlocks = 4;            // blocks per tile: 256 keys
 constexpr int kSlabBytes = 64 * 64 * 2;   // 64 rows x 64 dims bf16: 8 KB
 constexpr int kStageBytes = 2 * kSlabBytes;
-constexpr int kStages = 7;
+constexpr int kKRing = 4;                 // stages of the K ring
+constexpr int kVRing = 3;                 // stages of the V ring
 constexpr int kKStages = kD / 64;         // stages of a tile's K
 constexpr int kQBytes = kKStages * kSlabBytes;
 constexpr int kPBytes = kTileBlocks * kSlabBytes;
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;             // three warpgroups
+// Registers per thread: 384 threads launch with 168 each (64,512); the softmax warpgroup holds 128
+// scores in registers and takes 240, the two others give 80 each: (88 + 240 + 88) * 128 = 53,248.
+constexpr int kRegsSoftmax = 224, kRegsOther = 88;
+static_assert((kRegsSoftmax + 2 * kRegsOther) * 128 <= 168 * kThreads, "registers of a CTA");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;           // S buffers at columns 0 and 128
+constexpr uint32_t kStageLo = kStageBytes >> 4, kSlabLo = kSlabBytes >> 4;  // in descriptors
 constexpr unsigned long long kTimeoutNs = 1000000000ull;  // 1 s per wait
 constexpr unsigned long long kSettleNs = 20000000ull;     // 20 ms after an abort
 
-constexpr int kS_Ring = 0;
-constexpr int kS_Q = kS_Ring + kStages * kStageBytes;     // 112 KB
+constexpr int kS_K = 0;
+constexpr int kS_V = kS_K + kKRing * kStageBytes;         // 64 KB
+constexpr int kS_Q = kS_V + kVRing * kStageBytes;         // 112 KB
 constexpr int kS_P = kS_Q + kQBytes;                      // 184 KB
 constexpr int kS_Red = kS_P + kPBytes;                    // 216 KB: max[2 tiles][2 halves][64]
 constexpr int kS_Sum = kS_Red + 4 * kMH * 4;              // l[2 segments][2 halves][64]
@@ -72,21 +82,23 @@ constexpr int kSegCache = 32;
 constexpr int kS_Bar = kS_Seg + kSegCache * 32;
 
 enum Bar {
-  // in the first CTA only (the MMA warp waits): arrivals come from both CTAs
-  kFull = 0,                   // kStages: both CTAs' parts of a stage landed (or were fixed)
-  kQFull = kFull + kStages,    // both CTAs' query rows landed
+  // in the first CTA only (the MMA warps wait): bytes and arrivals come from both CTAs
+  kKFull = 0,                  // kKRing: both CTAs' parts of a stage landed
+  kVFull = kKFull + kKRing,    // kVRing: ... or were fixed
+  kQFull = kVFull + kVRing,    // both CTAs' query rows landed
   kSFree,                      // 2: softmax warps of both CTAs copied an S buffer out
   kPReady = kSFree + 2,        // P written and O rescaled in both CTAs
   // in each CTA
-  kEmpty,                      // kStages: the MMAs reading a stage are complete
-  kQEmpty = kEmpty + kStages,  // the segment's last S is complete
+  kKEmpty,                     // kKRing: the MMAs reading a stage are complete
+  kVEmpty = kKEmpty + kKRing,  // kVRing
+  kQEmpty = kVEmpty + kVRing,  // the segment's last S is complete
   kSFull,                      // 2: an S buffer is complete
   kPvDone = kSFull + 2,        // a tile's P . V is complete
   kRed,                        // the four softmax warps posted their maxima
   kSum,                        // ... their sums
-  kFix,                        // kStages: a stage for the fixer landed
-  kFinal = kFix + kStages,
-  kNumBars
+  kFix,                        // kVRing: a stage for the fixer landed
+  kFinal = kFix + kVRing,      // 2: all products of an MMA warp are complete
+  kNumBars = kFinal + 2
 };
 constexpr int kSmemBytes = kS_Bar + kNumBars * 8 + 16 + 1024;  // + alignment to 1 KB
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -145,9 +157,10 @@ struct Ctl {
   volatile int* abort;
 };
 
-// Warp-collective bounded wait; the result is the same in all 32 lanes.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t* err,
-                                       volatile int* abort) {
+// Warp-collective bounded wait; the result is the same in all 32 lanes. Inlined whole: a call
+// would spill the softmax warps' scores.
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t* err,
+                                          volatile int* abort) {
   uint64_t t0 = 0;
   for (int it = 0;; ++it) {
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
@@ -251,16 +264,16 @@ struct RowWindow {
   }
 };
 
-// A place in the ring: its stage, the parity of the stage's use, and how many places lie before.
+// A place in a ring of N stages: the stage, the parity of its use, and how many places lie before.
+template <int N>
 struct Cursor {
   int stage = 0;
   uint32_t round = 0;
   int used = 0;
-  __device__ __forceinline__ void move(int n) {
-    used += n;
-    stage += n;
-    while (stage >= kStages) {
-      stage -= kStages;
+  __device__ __forceinline__ void step() {
+    ++used;
+    if (++stage == N) {
+      stage = 0;
       round ^= 1;
     }
   }
@@ -316,12 +329,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   const Ctl ctl{p.err, abort_flag};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(kFull + i), 2);
-      mbar_init(bar(kEmpty + i), 1);
+    for (int i = 0; i < kKRing; ++i) {
+      mbar_init(bar(kKFull + i), 1);
+      mbar_init(bar(kKEmpty + i), 1);
+    }
+    for (int i = 0; i < kVRing; ++i) {
+      mbar_init(bar(kVFull + i), 2);
+      mbar_init(bar(kVEmpty + i), 1);
       mbar_init(bar(kFix + i), 1);
     }
-    mbar_init(bar(kQFull), 2);
+    mbar_init(bar(kQFull), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kSFree + i), 8);
       mbar_init(bar(kSFull + i), 1);
@@ -331,7 +348,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     mbar_init(bar(kPvDone), 1);
     mbar_init(bar(kRed), 4);
     mbar_init(bar(kSum), 4);
-    mbar_init(bar(kFinal), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(kFinal + i), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -360,237 +377,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   TileWalk walk{&p, seg_cache, sb, sb, se, -1, member, -1, {}};
-  Tile cur, nxt;
+  Tile cur;
   bool has = walk.next(cur);
 
-  if (warp == 0 || warp == 3) {
-    // ------------------------------------------------------------------------- TMA: Q, K and V
-    // Two warps fill the ring, every second place each: one alone took longer for a tile's 17
-    // stages than the products that use them. (A warp for K and one for V would not do: a parity
-    // wait has to be within one phase of the last one, and K runs ahead of V by more.)
-    RowWindow wk, wv;
-    Cursor at;
-    int seg = 0;
-    bool ok = true;
-    const int turn = warp == 0 ? 0 : 1;
-    const uint32_t bars0 = peer_addr(bar(0), 0);
-    // Whether this place is this warp's; if so, once its stage is free.
-    auto mine = [&]() {
-      if ((at.used & 1) != turn) return false;
-      if (at.used >= kStages) ok = wait(bar(kEmpty + at.stage), at.round ^ 1, ctl);
-      return ok;
-    };
-    // Loads for a stage are counted on the first CTA's barriers: it expects the bytes of both
-    // CTAs, and gives both arrivals, which the fixers give otherwise.
-    auto arm = [&](int i, uint32_t bytes) {
-      if (rank == 0) {
-        mbar_arrive(bar(i));
-        mbar_expect_tx(bar(i), bytes);
-      }
-    };
-    auto load_k = [&](const Tile& t) {
-      if (t.first) {
-        if (turn == 0) {
-          // the previous segment's S products are done with Q
-          if (seg > 0) ok = wait(bar(kQEmpty), (seg - 1) & 1, ctl);
-          if (!ok) return;
-          if (elect_one()) {
-            arm(kQFull, 2 * kQBytes);
-            const int y = t.b * p.T * p.H + t.row0 + kMH * (int)rank;
-#pragma unroll
-            for (int k = 0; k < kKStages; ++k)
-              tma_load_pair(s_base + kS_Q + k * kSlabBytes, &tm_q, bars0 + 8 * kQFull, 64 * k, y);
-          }
-          __syncwarp();
-        }
-        ++seg;
-      }
-      // this CTA's blocks of keys; in place of one that the segment does not have, its last (the
-      // scores are masked)
-      const int hb = t.half_blocks(), j0 = (int)rank * hb;
-      const int y0 = wk.get(p, t.b, t.chunk + min(j0, t.nb - 1), lane);
-      const int y1 = wk.get(p, t.b, t.chunk + min(j0 + hb - 1, t.nb - 1), lane);
-#pragma unroll 1
-      for (int k = 0; k < kKStages && ok; ++k) {
-        if (mine()) {
-          if (elect_one()) {
-            const uint32_t full = bars0 + 8u * (uint32_t)(kFull + at.stage);
-            const uint32_t dst = s_base + kS_Ring + at.stage * kStageBytes;
-            arm(kFull + at.stage, 2 * hb * kSlabBytes);
-            tma_load_pair(dst, &tm_kv, full, 64 * k, y0);
-            if (hb > 1) tma_load_pair(dst + kSlabBytes, &tm_kv, full, 64 * k, y1);
-          }
-          __syncwarp();
-        }
-        at.move(1);
-      }
-    };
-    auto load_v = [&](const Tile& t) {
-      for (int j = 0; j < t.nb && ok; ++j) {
-        const int y = wv.get(p, t.b, t.chunk + j, lane);
-        const bool fix = needs_fix(t, j, p.T);
-#pragma unroll 1
-        for (int dh = 0; dh < 2 && ok; ++dh) {
-          if (mine()) {
-            if (elect_one()) {
-              const uint32_t dst = s_base + kS_Ring + at.stage * kStageBytes;
-              const int x = 256 * dh + 128 * (int)rank;
-              uint32_t full = bars0 + 8u * (uint32_t)(kFull + at.stage);
-              if (fix) {
-                full = bar(kFix + at.stage);
-                mbar_expect_tx(full, kStageBytes);
-              } else {
-                arm(kFull + at.stage, 2 * kStageBytes);
-              }
-              tma_load_pair(dst, &tm_kv, full, x, y);
-              tma_load_pair(dst + kSlabBytes, &tm_kv, full, x + 64, y);
-            }
-            __syncwarp();
-          }
-          at.move(1);
-        }
-      }
-    };
-    if (has) load_k(cur);
-    while (ok && has) {
-      const bool more = walk.next(nxt);
-      if (more) load_k(nxt);
-      if (ok) load_v(cur);
-      cur = nxt;
-      has = more;
-    }
-  } else if (warp == 1 && rank == 0) {
-    // ---------------------------------------------------------------------------- MMA issue
-    Cursor at;
-    int t = 0, seg = 0;
-    bool ok = true;
-    const uint32_t q_lo = desc_lo(s_base + kS_Q, 16), p_lo = desc_lo(s_base + kS_P, 16);
-    const uint32_t ring_k = desc_lo(s_base + kS_Ring, 16);
-    const uint32_t ring_v = desc_lo(s_base + kS_Ring, kSlabBytes);
-    constexpr uint32_t kStageLo = kStageBytes >> 4, kSlabLo = kSlabBytes >> 4;
-    int tq = 0;  // tiles whose S was issued
-    auto issue_s = [&](const Tile& tl) {
-      if (tl.first) {
-        ok = wait(bar(kQFull), seg & 1, ctl);
-        ++seg;
-      }
-      // the softmax warps copied out what this buffer held two tiles ago
-      if (ok && tq >= 2) ok = wait(bar(kSFree + (tq & 1)), ((tq >> 1) - 1) & 1, ctl);
-      if (!ok) return;
-      const uint32_t d = tmem + 128u * (uint32_t)(tq & 1);
-      const uint32_t id = idesc(128, 128 * tl.half_blocks(), 0);
-#pragma unroll 1
-      for (int k = 0; k < kKStages; ++k) {
-        if (!wait(bar(kFull + at.stage), at.round, ctl)) {
-          ok = false;
-          return;
-        }
-        tc_after();
-        if (elect_one()) {
-          const uint32_t a = q_lo + kSlabLo * k, b = ring_k + kStageLo * at.stage;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mma2(d, a + 2 * i, b + 2 * i, id, (k > 0 || i > 0) ? 1u : 0u);
-          commit_both(bar(kEmpty + at.stage));
-        }
-        __syncwarp();
-        at.move(1);
-      }
-      if (elect_one()) {
-        commit_both(bar(kSFull + (tq & 1)));
-        if (tl.last) commit_both(bar(kQEmpty));
-      }
-      __syncwarp();
-      ++tq;
-    };
-    if (has) issue_s(cur);
-    while (ok && has) {
-      const bool more = walk.next(nxt);
-      if (more) issue_s(nxt);
-      if (ok) ok = wait(bar(kPReady), t & 1, ctl);
-      if (!ok) break;
-      tc_after();
-      // where P's block of keys j lies: the second half of the keys from slab 2 on
-      const uint32_t slab = cur.half_blocks() > 1 ? kSlabLo : 2 * kSlabLo;
-      constexpr uint32_t id = idesc(128, 256, 1);
-#pragma unroll 1
-      for (int j = 0; j < cur.nb && ok; ++j) {
-#pragma unroll 1
-        for (int dh = 0; dh < 2; ++dh) {
-          if (!wait(bar(kFull + at.stage), at.round, ctl)) {
-            ok = false;
-            break;
-          }
-          tc_after();
-          if (elect_one()) {
-            const uint32_t a = p_lo + slab * j, b = ring_v + kStageLo * at.stage;
-            const uint32_t d = tmem + kColO + 128 * dh;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // 16 keys per step; V MN-major: 2 KB apart
-              mma2(d, a + 2 * i, b + 128 * i, id, (cur.first && j == 0 && i == 0) ? 0u : 1u);
-            commit_both(bar(kEmpty + at.stage));
-          }
-          __syncwarp();
-          at.move(1);
-        }
-      }
-      if (!ok) break;
-      if (elect_one()) commit_both(bar(kPvDone));
-      __syncwarp();
-      ++t;
-      cur = nxt;
-      has = more;
-    }
-  } else if (warp == 2) {
-    // -------------------------------------------------------------------------------- fixer
-    Cursor at;
-    if (has) at.move(kKStages);
-    uint32_t fixes = 0;
-    bool ok = true;
-    const uint32_t full0 = peer_addr(bar(kFull), 0);
-    while (ok && has) {
-      const bool more = walk.next(nxt);
-      if (more) at.move(kKStages);
-      for (int j = 0; j < cur.nb && ok; ++j) {
-        if (!needs_fix(cur, j, p.T)) {
-          at.move(2);
-          continue;
-        }
-        // rows of the block: up to `from` are the prefix; from `to` on they lie past the end
-        const int from = max(cur.len - p.T - (cur.chunk + j) * kRows, 0);
-        const int to = min(cur.len - (cur.chunk + j) * kRows, kRows);
-        for (int dh = 0; dh < 2; ++dh) {
-          const int stage = at.stage;
-          if (!wait(bar(kFix + stage), fixes >> stage & 1, ctl)) {
-            ok = false;
-            break;
-          }
-          fixes ^= 1u << stage;
-          uint8_t* st = smem + kS_Ring + stage * kStageBytes;
-          // 16-byte pieces of rows from .. 63 of both slabs
-          for (int i = 8 * from + lane; i < 8 * kRows; i += 32) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              uint4* v = (uint4*)(st + s * kSlabBytes) + i;
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (i < 8 * to) {
-                const uint4 y = *v;
-                x = make_uint4(finite2(y.x), finite2(y.y), finite2(y.z), finite2(y.w));
-                if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
-              }
-              *v = x;
-            }
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) arrive_pair(full0 + 8u * (uint32_t)stage);
-          __syncwarp();
-          at.move(1);
-        }
-      }
-      cur = nxt;
-      has = more;
-    }
-  } else if (warp >= 4) {
+  if (warp >= 4 && warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------- softmax, rescale, epilogue
     // TMEM lane 32 * quad + lane: query row `row` of this CTA, half `half` of the tile's keys
     // in S, and of each 256 latent dims in O
@@ -769,6 +560,212 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       ++t;
       has = walk.next(cur);
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 0) {
+      // --------------------------------------------------------------------------- TMA: Q and K
+      // Loads are counted on the first CTA's barriers: it expects the bytes of both CTAs.
+      RowWindow win;
+      Cursor<kKRing> at;
+      int seg = 0;
+      bool ok = true;
+      const uint32_t bars0 = peer_addr(bar(0), 0);
+      while (ok && has) {
+        if (cur.first) {
+          // the previous segment's S products are done with Q
+          if (seg > 0 && !wait(bar(kQEmpty), (seg - 1) & 1, ctl)) break;
+          if (elect_one()) {
+            if (rank == 0) mbar_expect_tx(bar(kQFull), 2 * kQBytes);
+            const int y = cur.b * p.T * p.H + cur.row0 + kMH * (int)rank;
+#pragma unroll
+            for (int k = 0; k < kKStages; ++k)
+              tma_load_pair(s_base + kS_Q + k * kSlabBytes, &tm_q, bars0 + 8 * kQFull, 64 * k, y);
+          }
+          __syncwarp();
+          ++seg;
+        }
+        // this CTA's blocks of keys; in place of one that the segment does not have, its last (the
+        // scores are masked)
+        const int hb = cur.half_blocks(), j0 = (int)rank * hb;
+        const int y0 = win.get(p, cur.b, cur.chunk + min(j0, cur.nb - 1), lane);
+        const int y1 = win.get(p, cur.b, cur.chunk + min(j0 + hb - 1, cur.nb - 1), lane);
+#pragma unroll 1
+        for (int k = 0; k < kKStages; ++k) {
+          if (at.used >= kKRing && !wait(bar(kKEmpty + at.stage), at.round ^ 1, ctl)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            const uint32_t full = bars0 + 8u * (uint32_t)(kKFull + at.stage);
+            const uint32_t dst = s_base + kS_K + at.stage * kStageBytes;
+            if (rank == 0) mbar_expect_tx(bar(kKFull + at.stage), 2 * hb * kSlabBytes);
+            tma_load_pair(dst, &tm_kv, full, 64 * k, y0);
+            if (hb > 1) tma_load_pair(dst + kSlabBytes, &tm_kv, full, 64 * k, y1);
+          }
+          __syncwarp();
+          at.step();
+        }
+        has = walk.next(cur);
+      }
+    } else if (warp == 3) {
+      // --------------------------------------------------------------------------------- TMA: V
+      RowWindow win;
+      Cursor<kVRing> at;
+      bool ok = true;
+      const uint32_t bars0 = peer_addr(bar(0), 0);
+      while (ok && has) {
+        for (int j = 0; j < cur.nb && ok; ++j) {
+          const int y = win.get(p, cur.b, cur.chunk + j, lane);
+          const bool fix = needs_fix(cur, j, p.T);
+#pragma unroll 1
+          for (int dh = 0; dh < 2; ++dh) {
+            if (at.used >= kVRing && !wait(bar(kVEmpty + at.stage), at.round ^ 1, ctl)) {
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              const uint32_t dst = s_base + kS_V + at.stage * kStageBytes;
+              const int x = 256 * dh + 128 * (int)rank;
+              uint32_t full = bars0 + 8u * (uint32_t)(kVFull + at.stage);
+              if (fix) {
+                full = bar(kFix + at.stage);
+                mbar_expect_tx(full, kStageBytes);
+              } else if (rank == 0) {
+                // both arrivals, which the fixers give otherwise
+                mbar_arrive(full);
+                mbar_expect_tx(bar(kVFull + at.stage), 2 * kStageBytes);
+              }
+              tma_load_pair(dst, &tm_kv, full, x, y);
+              tma_load_pair(dst + kSlabBytes, &tm_kv, full, x + 64, y);
+            }
+            __syncwarp();
+            at.step();
+          }
+        }
+        has = walk.next(cur);
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ------------------------------------------------------------------------- MMA: S = Q . K^T
+      Cursor<kKRing> at;
+      int t = 0, seg = 0;
+      bool ok = true;
+      const uint32_t q_lo = desc_lo(s_base + kS_Q, 16), ring = desc_lo(s_base + kS_K, 16);
+      while (ok && has) {
+        if (cur.first) {
+          if (!wait(bar(kQFull), seg & 1, ctl)) break;
+          ++seg;
+        }
+        // the softmax warps copied out what this buffer held two tiles ago
+        if (t >= 2 && !wait(bar(kSFree + (t & 1)), ((t >> 1) - 1) & 1, ctl)) break;
+        const uint32_t d = tmem + 128u * (uint32_t)(t & 1);
+        const uint32_t id = idesc(128, 128 * cur.half_blocks(), 0);
+#pragma unroll 1
+        for (int k = 0; k < kKStages; ++k) {
+          if (!wait(bar(kKFull + at.stage), at.round, ctl)) {
+            ok = false;
+            break;
+          }
+          tc_after();
+          if (elect_one()) {
+            const uint32_t a = q_lo + kSlabLo * k, b = ring + kStageLo * at.stage;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma2(d, a + 2 * i, b + 2 * i, id, (k > 0 || i > 0) ? 1u : 0u);
+            commit_both(bar(kKEmpty + at.stage));
+          }
+          __syncwarp();
+          at.step();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          commit_both(bar(kSFull + (t & 1)));
+          if (cur.last) commit_both(bar(kQEmpty));
+        }
+        __syncwarp();
+        ++t;
+        has = walk.next(cur);
+      }
+    } else if (warp == 2 && rank == 0) {
+      // ---------------------------------------------------------------------------- MMA: O += P . V
+      Cursor<kVRing> at;
+      int t = 0;
+      bool ok = true;
+      const uint32_t p_lo = desc_lo(s_base + kS_P, 16), ring = desc_lo(s_base + kS_V, kSlabBytes);
+      while (ok && has) {
+        if (!wait(bar(kPReady), t & 1, ctl)) break;
+        tc_after();
+        // where P's block of keys j lies: the second half of the keys from slab 2 on
+        const uint32_t slab = cur.half_blocks() > 1 ? kSlabLo : 2 * kSlabLo;
+        constexpr uint32_t id = idesc(128, 256, 1);
+#pragma unroll 1
+        for (int j = 0; j < cur.nb && ok; ++j) {
+#pragma unroll 1
+          for (int dh = 0; dh < 2; ++dh) {
+            if (!wait(bar(kVFull + at.stage), at.round, ctl)) {
+              ok = false;
+              break;
+            }
+            tc_after();
+            if (elect_one()) {
+              const uint32_t a = p_lo + slab * j, b = ring + kStageLo * at.stage;
+              const uint32_t d = tmem + kColO + 128 * dh;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)  // 16 keys per step; V MN-major: 2 KB apart
+                mma2(d, a + 2 * i, b + 128 * i, id, (cur.first && j == 0 && i == 0) ? 0u : 1u);
+              commit_both(bar(kVEmpty + at.stage));
+            }
+            __syncwarp();
+            at.step();
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) commit_both(bar(kPvDone));
+        __syncwarp();
+        ++t;
+        has = walk.next(cur);
+      }
+    } else if (warp == 8) {
+      // -------------------------------------------------------------------------------- fixer
+      Cursor<kVRing> at;
+      uint32_t fixes = 0;  // per stage: parity of its next fix
+      bool ok = true;
+      const uint32_t full0 = peer_addr(bar(kVFull), 0);
+      while (ok && has) {
+        for (int j = 0; j < cur.nb && ok; ++j) {
+          const bool fix = needs_fix(cur, j, p.T);
+          // rows of the block: up to `from` are the prefix; from `to` on they lie past the end
+          const int from = max(cur.len - p.T - (cur.chunk + j) * kRows, 0);
+          const int to = min(cur.len - (cur.chunk + j) * kRows, kRows);
+          for (int dh = 0; dh < 2; ++dh, at.step()) {
+            if (!fix) continue;
+            if (!wait(bar(kFix + at.stage), fixes >> at.stage & 1, ctl)) {
+              ok = false;
+              break;
+            }
+            fixes ^= 1u << at.stage;
+            uint8_t* st = smem + kS_V + at.stage * kStageBytes;
+            // 16-byte pieces of rows from .. 63 of both slabs
+            for (int i = 8 * from + lane; i < 8 * kRows; i += 32) {
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                uint4* v = (uint4*)(st + s * kSlabBytes) + i;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (i < 8 * to) {
+                  const uint4 y = *v;
+                  x = make_uint4(finite2(y.x), finite2(y.y), finite2(y.z), finite2(y.w));
+                  if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
+                }
+                *v = x;
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) arrive_pair(full0 + 8u * (uint32_t)at.stage);
+            __syncwarp();
+          }
+        }
+        has = walk.next(cur);
+      }
+    }
   }
 
   // ---------------------------------------------------------------------------------- teardown
@@ -781,10 +778,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     while (globaltimer() - t0 < kSettleNs) {
     }
   }
-  if (warp == 1 && rank == 0) {
-    if (elect_one()) commit_one(bar(kFinal));  // completes once every MMA issued here is done
+  if ((warp == 1 || warp == 2) && rank == 0) {
+    // completes once every MMA that this warp issued is done
+    if (elect_one()) commit_one(bar(kFinal + warp - 1));
     __syncwarp();
-    drain(bar(kFinal), 0, p.err);
+    drain(bar(kFinal + warp - 1), 0, p.err);
   }
   cluster_sync();  // no MMA, load or remote arrival of the pair is under way any more
   if (warp == 1)
