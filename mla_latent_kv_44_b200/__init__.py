@@ -334,37 +334,48 @@ def prefill(cfg: Config, q_nope, q_rope, pos, rows, w_uk, w_uv, cu_seqlens, max_
 # MlaError before anything is launched; they launch on the tensors' device whichever device is
 # current.
 
-def _expect(where: str, name: str, t, dtype, device, *shape):
-    """t is a contiguous tensor of dtype on device; a None in shape stands for any size."""
-    ok = t.dtype is dtype and t.device == device and t.is_contiguous()
-    if ok:
-        got = t.shape
-        ok = len(got) == len(shape)
-        if ok:
-            for n, want in zip(got, shape):
-                if want is not None and n != want:
-                    ok = False
-    if not ok:
+def _expect(where: str, device: int, *tensors):
+    """Every (name, tensor, dtype, shape) is a contiguous tensor of that kind on GPU `device`."""
+    for name, t, dtype, shape in tensors:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device and
+                t.is_contiguous()):
+            continue
         raise MlaError(MLA_ERR_INVALID_ARG,
                        f"{where}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}"
                        f"{'' if t.is_contiguous() else ' (not contiguous)'}, wanted {dtype} "
-                       f"({', '.join('any' if n is None else str(n) for n in shape)}) on {device}")
+                       f"{tuple(shape)} on cuda:{device}")
 
 
-def _launch(where: str, fn, device, stream, *args):
-    """Call fn(*args, stream) with `device` current."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
-        return
-    with torch.cuda.device(device):
-        _check(fn(*args, _stream(stream)), where)
+def _shape(where: str, name: str, t, dims: int):
+    """The shape of a tensor whose sizes the call takes from it."""
+    if t.dim() != dims:
+        raise MlaError(MLA_ERR_INVALID_ARG,
+                       f"{where}: {name} has shape {tuple(t.shape)}, wanted {dims} dimensions")
+    return t.shape
 
 
-def _device_of(where: str, name: str, t):
+def _device_of(where: str, name: str, t) -> int:
     if not t.is_cuda:
         raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is on {t.device}, not on a GPU")
-    return t.device
+    return t.get_device()
+
+
+def _launch(where: str, fn, device: int, stream, *args):
+    """Call fn(*args, stream) with `device` current; None is that device's current stream."""
+    import torch
+    # the raw handle: torch.cuda.current_stream() makes a Stream object, which takes longer
+    # than the rest of a small call
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
+    if st != MLA_OK:
+        raise MlaError(st, where)
 
 
 def build_tables(cfg: Config, seq_lens, new_lens, block_table, blocks_held, free_blocks,
@@ -378,24 +389,22 @@ def build_tables(cfg: Config, seq_lens, new_lens, block_table, blocks_held, free
     import torch
     w, i32 = "mla_build_tables", torch.int32
     dev = _device_of(w, "seq_lens", seq_lens)
-    n, tokens = seq_lens.shape[0], slots.shape[0]
-    _expect(w, "seq_lens", seq_lens, i32, dev, n)
-    _expect(w, "new_lens", new_lens, i32, dev, n)
-    _expect(w, "block_table", block_table, i32, dev, n, None)
-    _expect(w, "blocks_held", blocks_held, i32, dev, n)
-    _expect(w, "free_blocks", free_blocks, i32, dev, None)
-    _expect(w, "free_count", free_count, i32, dev, 1)
-    _expect(w, "blocks_held_out", blocks_held_out, i32, dev, n)
-    _expect(w, "free_count_out", free_count_out, i32, dev, 1)
-    _expect(w, "cu_new", cu_new, i32, dev, n + 1)
-    _expect(w, "seq_idx", seq_idx, i32, dev, tokens)
-    _expect(w, "pos", pos, i32, dev, tokens)
-    _expect(w, "slots", slots, torch.int64, dev, tokens)
-    _expect(w, "dev_err", dev_err, i32, dev, 1)
+    n, = _shape(w, "seq_lens", seq_lens, 1)
+    tokens, = _shape(w, "slots", slots, 1)
+    blocks, = _shape(w, "free_blocks", free_blocks, 1)
+    width = _shape(w, "block_table", block_table, 2)[1]
+    _expect(w, dev, ("seq_lens", seq_lens, i32, (n,)), ("new_lens", new_lens, i32, (n,)),
+            ("block_table", block_table, i32, (n, width)),
+            ("blocks_held", blocks_held, i32, (n,)),
+            ("free_blocks", free_blocks, i32, (blocks,)), ("free_count", free_count, i32, (1,)),
+            ("blocks_held_out", blocks_held_out, i32, (n,)),
+            ("free_count_out", free_count_out, i32, (1,)), ("cu_new", cu_new, i32, (n + 1,)),
+            ("seq_idx", seq_idx, i32, (tokens,)), ("pos", pos, i32, (tokens,)),
+            ("slots", slots, torch.int64, (tokens,)), ("dev_err", dev_err, i32, (1,)))
     _launch(w, lib.mla_build_tables, dev, stream, cfg.ref(), seq_lens.data_ptr(),
-            new_lens.data_ptr(), n, block_table.data_ptr(), block_table.shape[1],
+            new_lens.data_ptr(), n, block_table.data_ptr(), width,
             blocks_held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
-            free_blocks.shape[0], blocks_held_out.data_ptr(), free_count_out.data_ptr(),
+            blocks, blocks_held_out.data_ptr(), free_count_out.data_ptr(),
             cu_new.data_ptr(), seq_idx.data_ptr(), pos.data_ptr(), slots.data_ptr(), tokens,
             dev_err.data_ptr())
 
@@ -406,14 +415,12 @@ def tree_masks(parents, seq_lens, mask, pos, dev_err, stream=None):
     import torch
     w, i32 = "mla_tree_masks", torch.int32
     dev = _device_of(w, "parents", parents)
-    n = seq_lens.shape[0]
-    _expect(w, "parents", parents, i32, dev, None, None)
-    T = parents.shape[1]
-    _expect(w, "seq_lens", seq_lens, i32, dev, n)
-    _expect(w, "mask", mask, i32, dev, n * T, (T + 31) // 32)
-    _expect(w, "pos", pos, i32, dev, n * T)
-    _expect(w, "dev_err", dev_err, i32, dev, 1)
-    _launch(w, lib.mla_tree_masks, dev, stream, parents.data_ptr(), parents.shape[0],
+    n, = _shape(w, "seq_lens", seq_lens, 1)
+    rows, T = _shape(w, "parents", parents, 2)
+    _expect(w, dev, ("parents", parents, i32, (rows, T)), ("seq_lens", seq_lens, i32, (n,)),
+            ("mask", mask, i32, (n * T, (T + 31) // 32)), ("pos", pos, i32, (n * T,)),
+            ("dev_err", dev_err, i32, (1,)))
+    _launch(w, lib.mla_tree_masks, dev, stream, parents.data_ptr(), rows,
             seq_lens.data_ptr(), n, T, mask.data_ptr(), pos.data_ptr(), dev_err.data_ptr())
 
 
@@ -423,17 +430,16 @@ def append_slots(cfg: Config, ckv_raw, krope_raw, gamma, pos, slots, pool, dev_e
     import torch
     w, dt = "mla_append_slots", cfg.torch_dtype
     dev = _device_of(w, "pool", pool)
-    n = slots.shape[0]
-    _expect(w, "ckv_raw", ckv_raw, dt, dev, n, cfg.kv_rank)
-    if cfg.rope_dim:
-        _expect(w, "krope_raw", krope_raw, dt, dev, n, cfg.rope_dim)
-    _expect(w, "gamma", gamma, torch.float32, dev, cfg.kv_rank)
-    _expect(w, "pos", pos, torch.int32, dev, n)
-    _expect(w, "slots", slots, torch.int64, dev, n)
-    _expect(w, "pool", pool, dt, dev, None, cfg.block_size, cfg.kv_rank + cfg.rope_dim)
-    _expect(w, "dev_err", dev_err, torch.int32, dev, 1)
+    n, = _shape(w, "slots", slots, 1)
+    blocks, r, dr = _shape(w, "pool", pool, 3)[0], cfg.kv_rank, cfg.rope_dim
+    _expect(w, dev, ("ckv_raw", ckv_raw, dt, (n, r)), ("gamma", gamma, torch.float32, (r,)),
+            ("pos", pos, torch.int32, (n,)), ("slots", slots, torch.int64, (n,)),
+            ("pool", pool, dt, (blocks, cfg.block_size, r + dr)),
+            ("dev_err", dev_err, torch.int32, (1,)))
+    if dr:
+        _expect(w, dev, ("krope_raw", krope_raw, dt, (n, dr)))
     _launch(w, lib.mla_append_slots, dev, stream, cfg.ref(), ckv_raw.data_ptr(), _ptr(krope_raw),
-            gamma.data_ptr(), pos.data_ptr(), slots.data_ptr(), pool.data_ptr(), pool.shape[0], n,
+            gamma.data_ptr(), pos.data_ptr(), slots.data_ptr(), pool.data_ptr(), blocks, n,
             dev_err.data_ptr())
 
 
@@ -448,24 +454,22 @@ def decode_tree(cfg: Config, q, pool, block_table, seq_lens, q_per_seq: int, tre
     import torch
     w, dt, i32 = "mla_decode_tree", cfg.torch_dtype, torch.int32
     dev = _device_of(w, "pool", pool)
-    n = seq_lens.shape[0]
-    nt, H, D = n * q_per_seq, cfg.num_heads, cfg.kv_rank + cfg.rope_dim
-    dv = cfg.head_dim_v or cfg.head_dim
-    _expect(w, "q", q, dt, dev, nt, H, D)
-    _expect(w, "pool", pool, dt, dev, None, cfg.block_size, D)
-    _expect(w, "block_table", block_table, i32, dev, n, None)
-    _expect(w, "seq_lens", seq_lens, i32, dev, n)
+    n, = _shape(w, "seq_lens", seq_lens, 1)
+    blocks, width = _shape(w, "pool", pool, 3)[0], _shape(w, "block_table", block_table, 2)[1]
+    size, = _shape(w, "workspace", workspace, 1)
+    nt, H, r = n * q_per_seq, cfg.num_heads, cfg.kv_rank
+    D, dv = r + cfg.rope_dim, cfg.head_dim_v or cfg.head_dim
+    _expect(w, dev, ("q", q, dt, (nt, H, D)), ("pool", pool, dt, (blocks, cfg.block_size, D)),
+            ("block_table", block_table, i32, (n, width)), ("seq_lens", seq_lens, i32, (n,)),
+            ("w_uv", w_uv, dt, (H, dv, r)), ("workspace", workspace, torch.uint8, (size,)),
+            ("o", o, dt, (nt, H, dv)), ("dev_err", dev_err, i32, (1,)))
     if tree_mask is not None:
-        _expect(w, "tree_mask", tree_mask, i32, dev, nt, (q_per_seq + 31) // 32)
-    _expect(w, "w_uv", w_uv, dt, dev, H, dv, cfg.kv_rank)
-    _expect(w, "o", o, dt, dev, nt, H, dv)
+        _expect(w, dev, ("tree_mask", tree_mask, i32, (nt, (q_per_seq + 31) // 32)))
     if lse is not None:
-        _expect(w, "lse", lse, torch.float32, dev, nt, H)
-    _expect(w, "workspace", workspace, torch.uint8, dev, None)
-    _expect(w, "dev_err", dev_err, i32, dev, 1)
+        _expect(w, dev, ("lse", lse, torch.float32, (nt, H)))
     _launch(w, lib.mla_decode_tree, dev, stream, cfg.ref(), q.data_ptr(), pool.data_ptr(),
-            block_table.data_ptr(), block_table.shape[1], pool.shape[0], seq_lens.data_ptr(), n,
-            q_per_seq, _ptr(tree_mask), w_uv.data_ptr(), workspace.data_ptr(), workspace.shape[0],
+            block_table.data_ptr(), width, blocks, seq_lens.data_ptr(), n,
+            q_per_seq, _ptr(tree_mask), w_uv.data_ptr(), workspace.data_ptr(), size,
             o.data_ptr(), _ptr(lse), dev_err.data_ptr())
 
 
@@ -476,18 +480,17 @@ def commit_tree(cfg: Config, path, path_len, q_per_seq: int, block_table, pool, 
     import torch
     w, i32 = "mla_commit_tree", torch.int32
     dev = _device_of(w, "pool", pool)
-    n = seq_lens.shape[0]
-    _expect(w, "path", path, i32, dev, n, None)
-    _expect(w, "path_len", path_len, i32, dev, n)
-    _expect(w, "block_table", block_table, i32, dev, n, None)
-    _expect(w, "pool", pool, cfg.torch_dtype, dev, None, cfg.block_size,
-            cfg.kv_rank + cfg.rope_dim)
-    _expect(w, "seq_lens", seq_lens, i32, dev, n)
-    _expect(w, "seq_lens_out", seq_lens_out, i32, dev, n)
-    _expect(w, "dev_err", dev_err, i32, dev, 1)
+    n, = _shape(w, "seq_lens", seq_lens, 1)
+    blocks, width = _shape(w, "pool", pool, 3)[0], _shape(w, "block_table", block_table, 2)[1]
+    steps = _shape(w, "path", path, 2)[1]
+    _expect(w, dev, ("path", path, i32, (n, steps)), ("path_len", path_len, i32, (n,)),
+            ("block_table", block_table, i32, (n, width)),
+            ("pool", pool, cfg.torch_dtype, (blocks, cfg.block_size, cfg.kv_rank + cfg.rope_dim)),
+            ("seq_lens", seq_lens, i32, (n,)), ("seq_lens_out", seq_lens_out, i32, (n,)),
+            ("dev_err", dev_err, i32, (1,)))
     _launch(w, lib.mla_commit_tree, dev, stream, cfg.ref(), path.data_ptr(), path_len.data_ptr(),
-            path.shape[1], q_per_seq, block_table.data_ptr(), block_table.shape[1],
-            pool.data_ptr(), pool.shape[0], seq_lens.data_ptr(), seq_lens_out.data_ptr(), n,
+            steps, q_per_seq, block_table.data_ptr(), width,
+            pool.data_ptr(), blocks, seq_lens.data_ptr(), seq_lens_out.data_ptr(), n,
             dev_err.data_ptr())
 
 
