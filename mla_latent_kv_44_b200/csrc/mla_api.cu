@@ -521,11 +521,11 @@ mla_status mla_decode_step(const mla_config* cfg, const void* q_nope, const void
 // ------------------------------------------------------------------------------------------
 namespace {
 
-// Workspace of mla_decode_tree: the latent sums and the partial results of split key ranges;
-// on the tensor-core path the schedule too.
+// Workspace of mla_decode_tree: the latent sums (two bf16 terms on the tensor-core path, fp32
+// otherwise), the partial results of split key ranges, and (tensor-core path) where they lie.
 struct TreeLayout {
   bool tc;
-  size_t latent, part_lse, part_o, header, range_begin, segments, items[5], total;
+  size_t latent, latent_lo, part_lse, part_o, cuts, total;
   int tile_rows, tiles, splits, team, groups, ranges;
 };
 
@@ -537,17 +537,14 @@ TreeLayout tree_layout(const mla_config& c, int batch, int T) {
   L.tiles = (T * c.num_heads + L.tile_rows - 1) / L.tile_rows;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
-  L.latent = take(n * c.kv_rank * sizeof(float));
+  L.latent = take(n * c.kv_rank * (L.tc ? 2 : 4));
   if (L.tc) {
+    L.latent_lo = take(n * c.kv_rank * 2);
     tree_team(L.tiles, &L.team, &L.ranges);
     L.groups = (L.tiles + L.team - 1) / L.team;
-    const size_t items = (size_t)batch * L.groups;
     L.part_lse = take((size_t)kMaxPartials * kTreeTile * sizeof(float));
     L.part_o = take((size_t)kMaxPartials * kTreeTile * c.kv_rank * sizeof(float));
-    L.header = take(64 * sizeof(int32_t));
-    L.range_begin = take((kRanges + 1) * sizeof(int32_t));
-    L.segments = take((kRanges + items) * sizeof(Segment));
-    for (size_t& it : L.items) it = take(items * sizeof(int32_t));
+    L.cuts = take(kRanges * sizeof(int4));
   } else {
     // enough CTAs for four on each of 148 SMs
     const int64_t ctas = (int64_t)batch * L.tiles;
@@ -652,7 +649,6 @@ mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* poo
   p.table = block_table;
   p.seq_lens = seq_lens;
   p.mask = tree_mask;
-  p.latent = (float*)(ws + L.latent);
   p.lse = lse;
   p.err = dev_err;
   p.part_lse = (float*)(ws + L.part_lse);
@@ -676,21 +672,20 @@ mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* poo
     p.team = L.team;
     p.groups = L.groups;
     p.ranges = L.ranges;
-    p.header = (int32_t*)(ws + L.header);
-    p.range_begin = (int32_t*)(ws + L.range_begin);
-    p.segments = (Segment*)(ws + L.segments);
-    p.item_len = (int32_t*)(ws + L.items[0]);
-    p.item_chunk0 = (int32_t*)(ws + L.items[1]);
-    p.item_slot0 = (int32_t*)(ws + L.items[2]);
-    p.item_nseg = (int32_t*)(ws + L.items[3]);
-    p.merge_list = (int32_t*)(ws + L.items[4]);
-    e = launch_tree_tc(c, p, (cudaStream_t)stream);
-  } else {
-    // no more ranges than 64-row pieces of the longest sequence the table can hold
-    p.splits = (int)std::min<int64_t>(
-        L.splits, std::max<int64_t>(1, ((int64_t)max_blocks * c.block_size + 63) / 64));
-    e = launch_tree_simt(c, p, (cudaStream_t)stream);
+    p.latent_hi = (__nv_bfloat16*)(ws + L.latent);
+    p.latent_lo = (__nv_bfloat16*)(ws + L.latent_lo);
+    p.cuts = (int4*)(ws + L.cuts);
+    e = launch_tree_tc(p, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = launch_tree_merge(p, (cudaStream_t)stream);
+    if (e == cudaSuccess)
+      e = launch_tree_out(p, w_uv, c.head_dim_v, o, (cudaStream_t)stream);
+    return from_cuda(e);
   }
+  p.latent = (float*)(ws + L.latent);
+  // no more ranges than 64-row pieces of the longest sequence the table can hold
+  p.splits = (int)std::min<int64_t>(
+      L.splits, std::max<int64_t>(1, ((int64_t)max_blocks * c.block_size + 63) / 64));
+  e = launch_tree_simt(c, p, (cudaStream_t)stream);
   if (e != cudaSuccess) return from_cuda(e);
   return mla_output(cfg, p.latent, w_uv, o, p.BT, dev_err, stream);
 }

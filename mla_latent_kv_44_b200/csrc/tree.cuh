@@ -24,12 +24,14 @@ struct TreeParams {
   float scale;
   // CUDA-core path: query rows per tile, tiles per sequence, key ranges per sequence
   int32_t tile_rows, tiles, splits;
-  // tensor-core path: the schedule (items are a sequence's groups of `team` tiles)
+  // tensor-core path: items are a sequence's groups of `team` tiles
   int32_t team, groups, ranges;
-  int32_t* header;       // [0] segments, [1] ranges in use, [2] items in merge_list
-  int32_t* range_begin;  // ranges + 1
-  Segment* segments;     // ranges + items; bt is the item
-  int32_t *item_len, *item_chunk0, *item_slot0, *item_nseg, *merge_list;
+  // finished latent sums (BT, H, r) as two bf16 terms, hi = bf16(x) and lo = bf16(x - hi): 16 bits
+  // of x in the operand type of the product with W_UV
+  __nv_bfloat16 *latent_hi, *latent_lo;
+  int4* cuts;  // per range: an item that goes on from the range before into this one (x; -1:
+               // none that begins there), its pieces (y) and the slot of the first (z); piece
+               // k > 0 is in slot 2 * (z / 2 + k)
 };
 
 // Rows of sequence b, its drafted ones included: 0 for an empty place of the batch and for a
@@ -52,7 +54,11 @@ cudaError_t launch_tree_simt(const mla_config& c, const TreeParams& p, cudaStrea
 int tree_simt_tile_rows(const mla_config& c);
 bool tree_tc_supported(const mla_config& c);
 void tree_team(int tiles, int* team, int* ranges);
-cudaError_t launch_tree_tc(const mla_config& c, const TreeParams& p, cudaStream_t st);
+cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t st);
+// tree_out.cu
+cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t st);
+cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void* o,
+                            cudaStream_t st);
 
 // step_tables.cu
 cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens, int batch,

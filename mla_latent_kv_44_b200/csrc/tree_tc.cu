@@ -42,6 +42,7 @@
 #include "tc_ptx.cuh"
 #include "tma_map.h"
 #include "tree.cuh"
+#include "tree_ptx.cuh"
 
 namespace mla {
 namespace {
@@ -77,9 +78,10 @@ constexpr int kS_Q = kS_V + kVRing * kStageBytes;         // 112 KB
 constexpr int kS_P = kS_Q + kQBytes;                      // 184 KB
 constexpr int kS_Red = kS_P + kPBytes;                    // 216 KB: max[2 tiles][2 halves][64]
 constexpr int kS_Sum = kS_Red + 4 * kMH * 4;              // l[2 segments][2 halves][64]
-constexpr int kS_Seg = kS_Sum + 4 * kMH * 4;
-constexpr int kSegCache = 32;
-constexpr int kS_Bar = kS_Seg + kSegCache * 32;
+constexpr int kS_Len = kS_Sum + 4 * kMH * 4;
+constexpr int kLenCache = 256;
+constexpr int kS_Plan = kS_Len + kLenCache * 4;           // 64 ints of the schedule's scans
+constexpr int kS_Bar = kS_Plan + 64 * 4;
 
 enum Bar {
   // in the first CTA only (the MMA warps wait): bytes and arrivals come from both CTAs
@@ -104,18 +106,7 @@ constexpr int kSmemBytes = kS_Bar + kNumBars * 8 + 16 + 1024;  // + alignment to
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 // ------------------------------------------------------------------------------ PTX helpers
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-               : "=r"(p));
-  return p != 0;
-}
-// D[tmem of both CTAs] (+)= A[smem] . B[smem]; descriptors as low words, the high word constant
-// (stride 1024, version 1, 128-byte swizzle)
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
-  return ((addr >> 4) & 0x3FFF) | ((lbo >> 4) << 16);
-}
+// D[tmem of both CTAs] (+)= A[smem] . B[smem], descriptors by their low words
 __device__ __forceinline__ void mma2(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id,
                                      uint32_t acc) {
   asm volatile(
@@ -188,56 +179,52 @@ __device__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
   if (!done && (threadIdx.x & 31) == 0) set_error(err, MLA_DEV_WAIT_TIMEOUT);
 }
 
-// A segment of this team's work range as one member sees it.
-struct SegInfo {
-  int b, row0, chunk_lo, chunk_hi, slot, chunk0, len, pad;
-};
-
-__device__ __forceinline__ SegInfo load_segment(const TreeParams& p, int s, int member) {
-  const Segment sg = p.segments[s];
-  const int b = sg.bt / p.groups, mt = (sg.bt - b * p.groups) * p.team + member;
-  return SegInfo{b, mt * kM, sg.chunk_lo, sg.chunk_hi, sg.slot < 0 ? -1 : sg.slot * p.team + member,
-                 p.item_chunk0[sg.bt], p.item_len[sg.bt], 0};
-}
-
-// One tile: up to four consecutive 64-row chunks of one segment.
+// One tile: up to four consecutive 64-row chunks of one item.
 struct Tile {
   int b, row0, chunk, nb, ntok, len, slot;
   bool first, last;
   __device__ int half_blocks() const { return nb > 2 ? 2 : 1; }  // blocks of keys per CTA
 };
 
-// Walks the tiles of segments [s, se) in order, identically in every warp of both CTAs.
+// Walks the tiles of the chunks [c, end) of the call's list, identically in every warp of both
+// CTAs: the items' chunks lie end to end, so the next item's begin where this one's end.
 struct TileWalk {
   const TreeParams* p;
-  const SegInfo* cache;  // shared memory, segments sb .. sb + kSegCache - 1
-  int sb, s, se, c, member, loaded;
-  SegInfo cur;
+  const int* lens;  // shared memory: rows of items first .. first + kLenCache - 1
+  int first, member, range, begin, end;
+  int it, x, len, c;  // current item, its first chunk and its rows; current chunk
+  __device__ int rows_of(int i) const {
+    return i - first < kLenCache ? lens[i - first] : tree_length(*p, i / p->groups, false);
+  }
   __device__ bool next(Tile& tl) {
-    while (s < se) {
-      if (loaded != s) {
-        cur = (s - sb < kSegCache) ? cache[s - sb] : load_segment(*p, s, member);
-        loaded = s;
+    while (c < end) {
+      const int stop = x + (len + kRows - 1) / kRows;
+      if (c >= stop) {
+        x = stop;
+        len = rows_of(++it);
+        continue;
       }
-      // a member whose tile of query rows lies behind the last one has nothing to do
-      if (cur.row0 < p->T * p->H) {
-        if (c < cur.chunk_lo) c = cur.chunk_lo;
-        if (c < cur.chunk_hi) {
-          tl.b = cur.b;
-          tl.row0 = cur.row0;
-          tl.chunk = c - cur.chunk0;
-          tl.nb = min(kTileBlocks, cur.chunk_hi - c);
-          tl.len = cur.len;
-          tl.ntok = min(tl.nb * kRows, cur.len - tl.chunk * kRows);
-          tl.slot = cur.slot;
-          tl.first = (c == cur.chunk_lo);
-          tl.last = (c + tl.nb == cur.chunk_hi);
-          c += tl.nb;
-          return true;
-        }
+      const int b = it / p->groups;
+      const int mt = (it - b * p->groups) * p->team + member;
+      if (mt >= p->tiles) {  // this member has no query rows in the item
+        c = min(stop, end);
+        continue;
       }
-      ++s;
-      c = -1;
+      tl.b = b;
+      tl.row0 = mt * kM;
+      tl.chunk = c - x;
+      tl.nb = min(kTileBlocks, min(stop, end) - c);
+      tl.len = len;
+      tl.ntok = min(tl.nb * kRows, len - tl.chunk * kRows);
+      // an item cut by the range leaves a partial result: a range has at most two, its first
+      // and its last
+      tl.slot = x >= begin && stop <= end
+                    ? -1
+                    : (2 * range + (x > begin ? 1 : 0)) * p->team + member;
+      tl.first = c == max(x, begin);
+      c += tl.nb;
+      tl.last = c == min(stop, end);
+      return true;
     }
     return false;
   }
@@ -304,6 +291,96 @@ __device__ __forceinline__ uint32_t seen_word(const TreeParams& p, int b, int t,
   return __funnelshift_r(lo, hi, n0 & 31);
 }
 
+// ------------------------------------------------------------------------------------------
+// Schedule. Items are (sequence, group of `team` tiles of query rows); their 64-row chunks of keys
+// are laid end to end and cut into R ranges of equal size, one per team of clusters. The members
+// of a team walk the same chunks at the same time, each for its own tile of query rows, so the
+// cache rows that several tiles need come from HBM once and from L2 for the others. Every CTA
+// finds its own range here: a scan of the items' chunk counts, which costs less than a kernel of
+// its own in front of this one (5-8 us). The cut items go into a list for the merge.
+// ------------------------------------------------------------------------------------------
+struct Range {
+  int begin, end;  // chunks
+  int item, x;     // the item that holds the first chunk, and that item's first chunk
+};
+
+// Chunks of 384 items from `base` on, scanned over the CTA: returns this thread's (inclusive).
+__device__ int scan_chunks(int v, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w)
+    if (w < warp) before += s_warp[w];
+  return v + before;
+}
+
+__device__ Range plan_range(const TreeParams& p, int range, int* s_plan, int* s_len) {
+  const int tid = threadIdx.x, items = p.batch * p.groups;
+  int* s_total = s_plan + 32;  // total, begin of this pass, item, x
+  if (tid < 4) s_total[tid] = 0;
+  __syncthreads();
+  auto chunks = [&](int it) {
+    if (it >= items) return 0;
+    const int b = it / p.groups;
+    return (tree_length(p, b, blockIdx.x == 0 && it == b * p.groups) + kChunk - 1) / kChunk;
+  };
+  // all chunks of the call (with one pass of items, this scan is the one that places them too)
+  const bool one = items <= kThreads;
+  int inc = 0, mine = 0;
+  for (int base = 0; base < items; base += kThreads) {
+    mine = chunks(base + tid);
+    inc = scan_chunks(mine, s_plan);
+    if (tid == kThreads - 1) s_total[0] += inc;
+    __syncthreads();
+  }
+  const int C = s_total[0];
+  const int R = min(C, p.ranges);
+  Range w{0, 0, 0, 0};
+  // one thread block per range says whether an item that began in the range before goes on here
+  const bool writer = range < p.ranges && (blockIdx.x & 1) == 0 && (blockIdx.x >> 1) % p.team == 0;
+  if (writer && tid == 0) p.cuts[range] = make_int4(-1, 0, 0, 0);
+  __syncthreads();
+  if (range < R) {
+    w.begin = range_start(range, R, C);
+    w.end = range_start(range + 1, R, C);
+  }
+  for (int base = 0; base < items; base += kThreads) {
+    const int it = base + tid;
+    if (!one) {
+      mine = chunks(it);
+      inc = scan_chunks(mine, s_plan);
+    }
+    const int x = s_total[1] + inc - mine, e = x + mine;
+    if (mine > 0 && w.begin < w.end && x <= w.begin && w.begin < e) {
+      s_total[2] = it;
+      s_total[3] = x;
+      if (writer && range > 0) {
+        const int before = range_start(range - 1, R, C);
+        if (x < w.begin && x >= before) {
+          const int last = starts_below(e, R, C) - 1;  // the range that holds its last chunk
+          p.cuts[range] = make_int4(it, last - (range - 1) + 1,
+                                    2 * (range - 1) + (x > before ? 1 : 0), 0);
+        }
+      }
+    }
+    __syncthreads();
+    if (tid == kThreads - 1) s_total[1] += inc;
+    __syncthreads();
+  }
+  w.item = s_total[2];
+  w.x = s_total[3];
+  if (tid < kLenCache && w.item + tid < items)
+    s_len[tid] = tree_length(p, (w.item + tid) / p.groups, false);
+  return w;
+}
+
 // the 16-byte piece with every bf16 that is not finite replaced by 0
 __device__ __forceinline__ uint32_t finite2(uint32_t v) {
   if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
@@ -321,7 +398,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   const uint32_t s_base = saddr(smem);
   uint32_t* tmem_slot = (uint32_t*)(smem + kS_Bar + kNumBars * 8);
   volatile int* abort_flag = (volatile int*)(smem + kS_Bar + kNumBars * 8 + 4);
-  SegInfo* seg_cache = (SegInfo*)(smem + kS_Seg);
+  int* s_len = (int*)(smem + kS_Len);
+  int* s_plan = (int*)(smem + kS_Plan);
   auto bar = [&](int i) { return s_base + kS_Bar + 8u * (uint32_t)i; };
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -359,24 +437,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  wait_prior_grid();  // the schedule, Q and the cache rows come from earlier kernels
+  // the output kernel may start on SMs that are done; it waits for this grid before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_prior_grid();  // the lengths, Q and the cache rows come from earlier kernels
 
   const int cluster = blockIdx.x >> 1;
   const int range = cluster / p.team, member = cluster - range * p.team;
-  int sb = 0, se = 0;
-  if (range < p.header[1]) {
-    sb = p.range_begin[range];
-    se = p.range_begin[range + 1];
-  }
-  for (int i = threadIdx.x; i < min(se - sb, kSegCache); i += blockDim.x)
-    seg_cache[i] = load_segment(p, sb + i, member);
+  const Range work = plan_range(p, range, s_plan, s_len);
   tc_before();
   __syncthreads();
   tc_after();
   cluster_sync();  // barriers of both CTAs initialised before any remote traffic
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  TileWalk walk{&p, seg_cache, sb, sb, se, -1, member, -1, {}};
+  TileWalk walk{&p, s_len, work.item, member, range, work.begin, work.end,
+                work.item, work.x, work.begin < work.end ? s_len[0] : 0, work.begin};
   Tile cur;
   bool has = walk.next(cur);
 
@@ -512,47 +587,77 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
         const float inv = total == 0.f ? 0.f : 1.f / total;
         if (!wait(bar(kPvDone), t & 1, ctl)) break;
         tc_after();
-        // O / l leaves through this warp's own 4 KB of P's buffer (32 rows x 32 columns, 16-byte
-        // groups swizzled by row % 8), read back four rows per instruction as whole lines
+        // O / l leaves through this warp's own 4 KB of P's buffer (32 rows of 128 bytes, 16-byte
+        // groups swizzled by row % 8), read back four rows per instruction as whole lines. A
+        // partial result stays in fp32; a finished one becomes two bf16 terms.
         const int rsub = lane >> 3, g = (lane & 7) ^ rsub;
-        float* dst = (cur.slot >= 0
-                          ? p.part_o + ((size_t)cur.slot * kM + kMH * rank + 32 * (quad & 1)) * kR
-                          : p.latent + (out_row - lane) * kR) +
-                     (size_t)rsub * kR + 4 * (lane & 7);
-        const int rows = cur.slot >= 0 ? 32 : p.T * p.H - (my_row - lane);  // rows to write
-        // the next chunk's tensor-memory load is under way while this one is staged and stored
-        uint32_t o[32], on[32];
-        tmem_ld32(tq + kColO, o);
+        const uint32_t w_row = box + 128u * (uint32_t)lane;
+        const bool part = cur.slot >= 0;
+        const int rows = part ? 32 : p.T * p.H - (my_row - lane);  // rows to write
+        char* dst = part ? (char*)(p.part_o +
+                                   ((size_t)cur.slot * kM + kMH * rank + 32 * (quad & 1)) * kR)
+                         : (char*)(p.latent_hi + (out_row - lane) * kR);
+        const int64_t lo = (char*)p.latent_lo - (char*)p.latent_hi;
+        const int pitch = part ? kR * 4 : kR * 2;
+        dst += (size_t)rsub * pitch + 16 * (lane & 7);
+        // columns 64 ch ..: dims 256 (ch / 2) + 128 half + 64 (ch % 2)
 #pragma unroll 1
-        for (int ch = 0; ch < 8; ++ch) {
-          if (ch + 1 < 8) tmem_ld32_async(tq + kColO + 32 * (ch + 1), on);
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t o[64];
+          tmem_ld64(tq + kColO + 64 * ch, o);
+          const int dim = 256 * (ch >> 1) + 128 * half + 64 * (ch & 1);
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             box + 128u * (uint32_t)lane + 16u * (uint32_t)(u ^ (lane & 7))),
-                         "f"(__uint_as_float(o[4 * u]) * inv),
-                         "f"(__uint_as_float(o[4 * u + 1]) * inv),
-                         "f"(__uint_as_float(o[4 * u + 2]) * inv),
-                         "f"(__uint_as_float(o[4 * u + 3]) * inv)
-                         : "memory");
-          __syncwarp();
-          // columns 32 ch ..: dims 256 (ch / 4) + 128 half + 32 (ch % 4)
-          float* line = dst + 256 * (ch >> 2) + 128 * half + 32 * (ch & 3);
+          for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          auto flush = [&](int64_t at) {  // the box's rows, to byte `at` of the output rows
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 x;
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                         : "r"(box + 128u * (uint32_t)(4 * i + rsub) +
-                               16u * (uint32_t)((i & 1) ? g ^ 4 : g))
-                         : "memory");
-            if (4 * i + rsub < rows) *(float4*)(line + (size_t)(4 * i) * kR) = x;
-          }
-          __syncwarp();
-          if (ch + 1 < 8) {
-            tmem_wait_ld(on);
+            for (int i = 0; i < 8; ++i) {
+              uint4 x;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                           : "r"(box + 128u * (uint32_t)(4 * i + rsub) +
+                                 16u * (uint32_t)((i & 1) ? g ^ 4 : g))
+                           : "memory");
+              if (4 * i + rsub < rows) *(uint4*)(dst + (size_t)(4 * i) * pitch + at) = x;
+            }
+            __syncwarp();
+          };
+          if (part) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = on[i];
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 w_row + 16u * (uint32_t)(u ^ (lane & 7))),
+                             "r"(o[32 * h + 4 * u]), "r"(o[32 * h + 4 * u + 1]),
+                             "r"(o[32 * h + 4 * u + 2]), "r"(o[32 * h + 4 * u + 3])
+                             : "memory");
+              flush(4 * (dim + 32 * h));
+            }
+          } else {
+#pragma unroll
+            for (int term = 0; term < 2; ++term) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  float x = __uint_as_float(o[8 * u + 2 * k]);
+                  float y = __uint_as_float(o[8 * u + 2 * k + 1]);
+                  w[k] = pack_bf16(x, y);
+                  if (term == 0) {  // what the first term leaves
+                    o[8 * u + 2 * k] = __float_as_uint(x - __uint_as_float(w[k] << 16));
+                    o[8 * u + 2 * k + 1] =
+                        __float_as_uint(y - __uint_as_float(w[k] & 0xffff0000u));
+                  }
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 w_row + 16u * (uint32_t)(u ^ (lane & 7))),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+              }
+              flush(2 * dim + term * lo);
+            }
           }
         }
         tc_before();
@@ -791,156 +896,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
                  : "memory");
 }
 
-// ------------------------------------------------------------------------------------------
-// Plan. Items are (sequence, group of `team` tiles of query rows); their 64-row chunks of keys
-// are laid end to end and cut into R ranges of equal size, one per team of clusters. The members
-// of a team walk the same chunks at the same time, each for its own tile of query rows, so the
-// cache rows that several tiles need come from HBM once and from L2 for the others.
-// ------------------------------------------------------------------------------------------
-namespace {
-
-constexpr int kPlanThreads = 1024;
-
-__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeParams p) {
-  __shared__ int s_a[32], s_b[32], s_carry[3];
-  const int tid = threadIdx.x;
-  const int items = p.batch * p.groups;
-  wait_prior_grid();
-  if (tid < 3) s_carry[tid] = 0;
-  __syncthreads();
-  for (int base = 0; base < items; base += kPlanThreads) {
-    const int it = base + tid;
-    int nch = 0;
-    if (it < items) {
-      const int b = it / p.groups;
-      const int len = tree_length(p, b, it == b * p.groups);
-      nch = (len + kChunk - 1) / kChunk;
-      p.item_len[it] = len;
-    }
-    int inc = nch, dummy = 0;
-    block_scan2<kPlanThreads>(s_a, s_b, inc, dummy);
-    if (it < items) p.item_chunk0[it] = s_carry[0] + inc - nch;
-    __syncthreads();
-    if (tid == kPlanThreads - 1) s_carry[0] += inc;
-    __syncthreads();
-  }
-  const int C = s_carry[0];
-  const int R = min(C, p.ranges);
-  __syncthreads();
-  if (tid == 0) s_carry[0] = 0;
-  __syncthreads();
-  for (int base = 0; base < items; base += kPlanThreads) {
-    const int it = base + tid;
-    int nseg = 0, x = 0, e = 0;
-    if (it < items) {
-      const int nch = (p.item_len[it] + kChunk - 1) / kChunk;
-      x = p.item_chunk0[it];
-      e = x + nch;
-      if (nch > 0) nseg = 1 + starts_below(e, R, C) - starts_below(x + 1, R, C);
-    }
-    const int nslot = nseg >= 2 ? nseg : 0;
-    int inc_seg = nseg, inc_slot = nslot;
-    block_scan2<kPlanThreads>(s_a, s_b, inc_seg, inc_slot);
-    if (it < items) {
-      const int first = s_carry[0] + inc_seg - nseg;
-      const int slot0 = s_carry[1] + inc_slot - nslot;
-      p.item_slot0[it] = slot0;
-      p.item_nseg[it] = nseg;
-      if (nseg != 1) p.merge_list[atomicAdd(&s_carry[2], 1)] = it;  // in any order
-      int q = starts_below(x + 1, R, C);  // first range starting after x
-      int lo = x;
-      for (int k = 0; k < nseg; ++k) {
-        const int hi = (k == nseg - 1) ? e : range_start(q, R, C);
-        p.segments[first + k] = Segment{it, lo, hi, nseg >= 2 ? slot0 + k : -1};
-        const int qs = starts_below(lo + 1, R, C) - 1;  // range containing chunk lo
-        if (qs >= 0 && range_start(qs, R, C) == lo) p.range_begin[qs] = first + k;
-        lo = hi;
-        ++q;
-      }
-    }
-    __syncthreads();
-    if (tid == kPlanThreads - 1) {
-      s_carry[0] += inc_seg;
-      s_carry[1] += inc_slot;
-    }
-    __syncthreads();
-  }
-  if (tid == 0) {
-    p.header[0] = s_carry[0];  // segments
-    p.header[1] = R;           // ranges in use
-    p.header[2] = s_carry[2];  // items of merge_list
-    p.range_begin[R] = s_carry[0];
-  }
-}
-
-// Merge of the items in merge_list: those cut into several segments, and those without rows
-// (zeros). A warp per query row, dealt round a fixed grid.
-constexpr int kMergeWarps = 8;
-
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_combine_kernel(const TreeParams p) {
-  __shared__ float s_w[kMergeWarps][kRanges];
-  wait_prior_grid();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = p.team * kM;  // query rows of an item
-  const int64_t total = (int64_t)p.header[2] * per;
-  float* w = s_w[warp];
-  for (int64_t i = (int64_t)blockIdx.x * kMergeWarps + warp; i < total;
-       i += (int64_t)gridDim.x * kMergeWarps) {
-    const int it = p.merge_list[i / per], m = (int)(i % per);
-    const int b = it / p.groups, row = (it - b * p.groups) * per + m;
-    if (row >= p.T * p.H) continue;
-    const size_t at = (size_t)b * p.T * p.H + row;
-    const int nseg = p.item_nseg[it];
-    // partial row of segment k: slot (slot0 + k) * team + m / kM, row m % kM
-    const size_t part0 = ((size_t)p.item_slot0[it] * p.team) * kM + m, step = (size_t)p.team * kM;
-    float mx = -INFINITY;
-    bool nan = false;
-    for (int k = lane; k < nseg; k += 32) {
-      const float x = p.part_lse[part0 + k * step];
-      nan |= x != x;
-      mx = fmaxf(mx, x);
-    }
-    mx = warp_max(mx);
-    nan = __any_sync(0xffffffffu, nan);
-    float z = 0.f;
-    for (int k = lane; k < nseg; k += 32) {
-      const float x = p.part_lse[part0 + k * step];
-      const float e = x == -INFINITY ? 0.f : expf(x - mx);
-      w[k] = e;
-      z += e;
-    }
-    z = warp_sum(z);
-    const bool empty = mx == -INFINITY && !nan;
-    const float inv = empty ? 0.f : 1.f / z;
-    __syncwarp();
-    float4 acc[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!empty) {
-#pragma unroll 2
-      for (int k = 0; k < nseg; ++k) {
-        const float e = w[k] * inv;
-        const float4* src = (const float4*)(p.part_o + (part0 + k * step) * kR) + lane;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 v = __ldcs(src + 32 * u);
-          acc[u].x = fmaf(e, v.x, acc[u].x);
-          acc[u].y = fmaf(e, v.y, acc[u].y);
-          acc[u].z = fmaf(e, v.z, acc[u].z);
-          acc[u].w = fmaf(e, v.w, acc[u].w);
-        }
-      }
-    }
-    float4* dst = (float4*)(p.latent + at * kR) + lane;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) dst[32 * u] = acc[u];
-    if (lane == 0 && p.lse) p.lse[at] = empty ? -INFINITY : mx + logf(z);
-    __syncwarp();
-  }
-}
-
-}  // namespace
-
 bool tree_tc_supported(const mla_config& c) {
   return c.dtype == MLA_BF16 && c.kv_rank == kR && c.rope_dim == kDR && c.block_size % kRows == 0;
 }
@@ -959,8 +914,7 @@ void tree_team(int tiles, int* team, int* ranges) {
   *ranges = kRanges / best;
 }
 
-cudaError_t launch_tree_tc(const mla_config& c, const TreeParams& p, cudaStream_t st) {
-  (void)c;
+cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t st) {
   CUtensorMap kv, qm;
   if (!make_bf16_map(&kv, p.pool, kD, (uint64_t)p.num_blocks * p.bs, kD * 2, kRows) ||
       !make_bf16_map(&qm, p.q, kD, (uint64_t)p.BT * p.H, kD * 2, kMH))
@@ -977,12 +931,7 @@ cudaError_t launch_tree_tc(const mla_config& c, const TreeParams& p, cudaStream_
     if (e != cudaSuccess) return e;
     attr_devices.fetch_or(bit, std::memory_order_acq_rel);
   }
-  e = launch_pdl(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p);
-  if (e == cudaSuccess)
-    e = launch_pdl(tree_tc_kernel, dim3(2 * kRanges), dim3(kThreads), kSmemBytes, st, kv, qm, p);
-  if (e == cudaSuccess)
-    e = launch_pdl(tree_combine_kernel, dim3(2 * 148), dim3(kMergeWarps * 32), 0, st, p);
-  return e;
+  return launch_pdl(tree_tc_kernel, dim3(2 * kRanges), dim3(kThreads), kSmemBytes, st, kv, qm, p);
 }
 
 }  // namespace mla
