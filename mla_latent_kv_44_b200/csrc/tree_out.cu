@@ -3,12 +3,12 @@
 //
 // Per head the product is W_UV[h] (d_v x 512) with the call's latent sums of that head (512 x n). A
 // CTA keeps 128 rows of W_UV[h] in shared memory (128 KB, loaded by TMA before it waits for the
-// kernel in front) and streams the latent rows of 32 tokens, 256 dims at a time, through three
-// buffers by cp.async: both bf16 terms of each value (hi = bf16(x), lo = bf16(x - hi); one
-// term alone would add as large an error as the rounding of o). M = 128 (dims), N = 32 (tokens):
-// 32 MMAs per buffer into one of two tensor-memory accumulators; the epilogue of a tile of
-// tokens runs while the next one's products do. What bounds it: the weights' bytes for few
-// tokens, the latent rows' for many.
+// kernel in front) and streams 64 dims of 128 tokens at a time through a ring of three stages,
+// both bf16 terms of each value (hi = bf16(x), lo = bf16(x - hi); one term alone would add as large
+// an error as the rounding of o). M = 128 (dims), N = the tile's tokens: 8 MMAs per stage into
+// one of two tensor-memory accumulators; the epilogue of a tile of tokens runs while the next
+// one's products do. (With 32 tokens per tile the MMAs' issue took 146 us for 1024 tokens.) What
+// bounds it: the weights' bytes for few tokens, the latent rows' for many.
 #include <atomic>
 
 #include "tc_ptx.cuh"
@@ -21,32 +21,50 @@ namespace {
 
 constexpr int kR = 512;
 constexpr int kSlabs = kR / 64;
-constexpr int kHalf = kSlabs / 2;                  // slabs of one buffer, for each term
 constexpr int kDims = 128;                         // rows of W_UV per CTA
-constexpr int kTok = 32;                           // tokens per tile
-constexpr int kBufs = 3;
+constexpr int kTok = 128;                          // tokens per tile
+constexpr int kRing = 3;
 constexpr int kThreads = 256;
-constexpr int kWSlab = kDims * 128, kBSlab = kTok * 128;
+constexpr int kWSlab = kDims * 128, kTerm = kTok * 128;
+constexpr int kStage = 2 * kTerm;                  // hi and lo: 32 KB
 constexpr int kW = 0;
 constexpr int kB = kW + kSlabs * kWSlab;           // 128 KB
-constexpr int kBBytes = kSlabs * kBSlab;           // 32 KB
-constexpr int kBar = kB + kBufs * kBBytes;         // W, products of even and odd buffers
-constexpr int kSmem = kBar + 3 * 8 + 16 + 1024;
+constexpr int kBars = kB + kRing * kStage;         // 224 KB
+enum Bar {
+  kWFull = 0,                  // kSlabs: a slab of W_UV landed
+  kFull = kWFull + kSlabs,     // kRing: a stage landed
+  kEmpty = kFull + kRing,      // kRing: its products are complete
+  kDFull = kEmpty + kRing,     // 2: a tile's products are complete
+  kDEmpty = kDFull + 2,        // 2: the epilogue warps read an accumulator
+  kNumBars = kDEmpty + 2
+};
+constexpr int kSmem = kBars + kNumBars * 8 + 16 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-constexpr unsigned long long kTimeoutNs = 1000000000ull;
+constexpr unsigned long long kTimeoutNs = 1000000000ull, kSettleNs = 20000000ull;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&v)[16]) {
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                          int y, int z) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15])
-      : "r"(ta)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+// Warp-collective bounded wait.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t* err,
+                                     volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    const bool late = globaltimer() - t0 > kTimeoutNs;
+    if (__any_sync(0xffffffffu, *abort != 0 || late)) {
+      if ((threadIdx.x & 31) == 0 && late) {
+        set_error(err, MLA_DEV_WAIT_TIMEOUT);
+        *abort = 1;
+      }
+      return false;
+    }
+  }
 }
 
 // D[tmem] (+)= A[smem] . B[smem], descriptors by their low words
@@ -127,15 +145,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_parts_kernel(cons
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const TreeParams p, int dv, int splits,
+tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_hi,
+                const __grid_constant__ CUtensorMap tm_lo, const TreeParams p, int dv, int splits,
                 __nv_bfloat16* __restrict__ o) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t s_base = saddr(smem);
-  const uint32_t bar_w = s_base + kBar, bar_d = bar_w + 8;  // W; the products of a buffer (by i & 1)
-  uint32_t* tmem_slot = (uint32_t*)(smem + kBar + 24);
-  volatile int* abort_flag = (volatile int*)(smem + kBar + 28);
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  auto bar = [&](int i) { return s_base + kBars + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = (uint32_t*)(smem + kBars + kNumBars * 8);
+  volatile int* abort = (volatile int*)(smem + kBars + kNumBars * 8 + 4);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // this CTA's head, rows of W_UV and tiles of tokens
   const int split = blockIdx.x % splits, h = (blockIdx.x / splits) % p.H;
   const int dim0 = blockIdx.x / (splits * p.H) * kDims;
@@ -143,12 +162,12 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const TreeParams p, in
   const int lo = (int)((int64_t)tiles * split / splits);
   const int hi = (int)((int64_t)tiles * (split + 1) / splits);
 
-  if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(bar_w + 8 * i, 1);
-    *abort_flag = 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i < kDEmpty ? 1 : 4);
+    *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
+  if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      saddr(tmem_slot)),
                  "r"(2 * kTok)
@@ -159,138 +178,142 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const TreeParams p, in
   __syncthreads();
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  if (warp == 0 && elect_one()) {
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------------------------ TMA
     // the weights come from before the attention kernel, which waited for what came before it
     // and is over when the kernel in front of this one writes
-    mbar_expect_tx(bar_w, kSlabs * kWSlab);
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < kSlabs; ++k)
-      tma_load(s_base + kW + k * kWSlab, &tm_w, bar_w, 64 * k, h * dv + dim0);
-  }
-  __syncwarp();
-  wait_prior_grid();
-
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (mbar_try(bar, parity)) return;
-    const uint64_t t0 = globaltimer();
-    while (*abort_flag == 0 && !mbar_try(bar, parity)) {
-      if (globaltimer() - t0 > kTimeoutNs) {
-        set_error(p.err, MLA_DEV_WAIT_TIMEOUT);
-        *abort_flag = 1;
+      for (int k = 0; k < kSlabs; ++k) {
+        mbar_expect_tx(bar(kWFull + k), kWSlab);
+        tma_load(s_base + kW + k * kWSlab, &tm_w, bar(kWFull + k), 64 * k, h * dv + dim0);
       }
     }
-  };
-  // buffer i % 3: 32 tokens, 256 dims (half i & 1) of both terms. A thread takes one 16-byte piece
-  // (32 per row) of four rows in each term. Sequences without rows read as zeros.
-  auto load = [&](int i) {
-    const int piece = tid & 31;
-    const int n0 = (lo + (i >> 1)) * kTok;
-    const uint32_t dst = s_base + kB + (uint32_t)(i % kBufs) * kBBytes + (piece >> 3) * kBSlab;
-    bool live[kTok / 8];
-#pragma unroll
-    for (int u = 0; u < kTok / 8; ++u) {
-      const int n = n0 + (tid >> 5) + 8 * u;
-      live[u] = n < p.BT && tree_length(p, n / p.T, false) > 0;
-      if (n < p.BT && !live[u] && piece == 0 && dim0 == 0 && (i & 1) == 0 && p.lse)
-        p.lse[(size_t)n * p.H + h] = -INFINITY;
-    }
-#pragma unroll
-    for (int u = 0; u < kTok / 8; ++u) {
-      const int t = (tid >> 5) + 8 * u;
-      const uint32_t at = dst + 128u * (uint32_t)t + 16u * (uint32_t)((piece & 7) ^ (t & 7));
-      const size_t src = ((size_t)(n0 + t) * p.H + h) * kR + 256 * (i & 1) + 8 * piece;
-      if (live[u]) {
-        cp_async16(at, p.latent_hi + src);
-        cp_async16(at + kHalf * kBSlab, p.latent_lo + src);
-      } else {
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + term * kHalf * kBSlab),
-                       "r"(0)
-                       : "memory");
-      }
-    }
-  };
-  auto commit_loads = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-  // tile i's accumulator (complete) -> o: a thread holds one dim of 16 tokens; neighbours swap, so that each
-  // stores two dims of every second token
-  auto store = [&](int i) {
-    tc_after();
-    const int quad = warp & 3, half = warp >> 2;
-    uint32_t v[16];
-    tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + kTok * (i & 1) + 16 * half, v);
-    tc_before();
-    const int dim = dim0 + 32 * quad + lane, n0 = (lo + i) * kTok + 16 * half;
-    const bool even = (lane & 1) == 0;
-#pragma unroll
-    for (int c = 0; c < 16; c += 2) {
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, even ? v[c + 1] : v[c], 1);
-      const int n = n0 + c + (even ? 0 : 1);
-      const float x = __uint_as_float(even ? v[c] : got), y = __uint_as_float(even ? got : v[c + 1]);
-      if (n < p.BT) {
-        __nv_bfloat16* dst = o + ((size_t)n * p.H + h) * dv + (dim & ~1);
-        if ((dv & 1) == 0) {
-          if (dim < dv) *(uint32_t*)dst = pack_bf16(x, y);
-        } else {
-          if ((dim & ~1) < dv) dst[0] = __float2bfloat16_rn(x);
-          if ((dim | 1) < dv) dst[1] = __float2bfloat16_rn(y);
+    __syncwarp();
+    wait_prior_grid();
+    int stage = 0, used = 0;
+    uint32_t round = 0;
+    bool ok = true;
+    for (int i = lo; i < hi && ok; ++i) {
+      for (int k = 0; k < kSlabs; ++k, ++used) {
+        if (used >= kRing && !wait(bar(kEmpty + stage), round ^ 1, p.err, abort)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t dst = s_base + kB + stage * kStage;
+          mbar_expect_tx(bar(kFull + stage), kStage);
+          tma_load3(dst, &tm_hi, bar(kFull + stage), 64 * k, h, i * kTok);
+          tma_load3(dst + kTerm, &tm_lo, bar(kFull + stage), 64 * k, h, i * kTok);
+        }
+        __syncwarp();
+        if (++stage == kRing) {
+          stage = 0;
+          round ^= 1;
         }
       }
     }
-  };
-
-  const int count = 2 * (hi - lo);  // buffers: two per tile of tokens
-  if (count > 0) load(0);
-  commit_loads();
-  if (count > 1) load(1);
-  commit_loads();
-  constexpr uint32_t id = idesc(kDims, kTok, 0);
-  const uint32_t w_lo = desc_lo(s_base + kW, 16), b_lo = desc_lo(s_base + kB, 16);
-  for (int i = 0; i < count; ++i) {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    fence_proxy_async();
-    __syncthreads();  // buffer i is in shared memory, and the accumulator it goes to was read
-    if (warp == 0) {
-      if (i == 0) wait(bar_w, 0);
-      __syncwarp();
-      tc_after();
-      if (elect_one()) {
-        const uint32_t b = b_lo + (uint32_t)(i % kBufs) * (kBBytes >> 4);
-        const uint32_t a = w_lo + (i & 1) * kHalf * (kWSlab >> 4);
-        const uint32_t d = tmem + kTok * ((i >> 1) & 1);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------------------------ MMA
+    int stage = 0;
+    uint32_t round = 0;
+    bool ok = true;
+    const uint32_t w_lo = desc_lo(s_base + kW, 16), b_lo = desc_lo(s_base + kB, 16);
+    for (int i = 0; i < hi - lo && ok; ++i) {
+      const int tokens = min(kTok, p.BT - (lo + i) * kTok);
+      const uint32_t id = idesc(kDims, (tokens + 15) / 16 * 16, 0);
+      if (i >= 2) ok = wait(bar(kDEmpty + (i & 1)), ((i >> 1) - 1) & 1, p.err, abort);
+      for (int k = 0; k < kSlabs && ok; ++k) {
+        ok = (i > 0 || wait(bar(kWFull + k), 0, p.err, abort)) &&
+             wait(bar(kFull + stage), round, p.err, abort);
+        if (!ok) break;
+        tc_after();
+        if (elect_one()) {
+          const uint32_t a = w_lo + k * (kWSlab >> 4), b = b_lo + stage * (kStage >> 4);
+          const uint32_t d = tmem + kTok * (i & 1);
 #pragma unroll
-        for (int k = 0; k < 2 * kHalf; ++k)  // hi's slabs, then lo's
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma1(d, a + (k % kHalf) * (kWSlab >> 4) + 2 * s, b + k * (kBSlab >> 4) + 2 * s, id,
-                 ((i & 1) || k > 0 || s > 0) ? 1u : 0u);
-        tc_commit(bar_d + 8 * (i & 1));
+          for (int s = 0; s < 8; ++s)  // the high term, then the low one
+            mma1(d, a + 2 * (s & 3), b + (s >> 2) * (kTerm >> 4) + 2 * (s & 3), id,
+                 (k > 0 || s > 0) ? 1u : 0u);
+          tc_commit(bar(kEmpty + stage));
+          if (k == kSlabs - 1) tc_commit(bar(kDFull + (i & 1)));
+        }
+        __syncwarp();
+        if (++stage == kRing) {
+          stage = 0;
+          round ^= 1;
+        }
       }
-      __syncwarp();
     }
-    // the products of buffer i - 1 are over: it takes i + 2; after a tile's second, its result
-    if (i > 0) {
-      wait(bar_d + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------------------- epilogue
+    // A thread holds one dim of the tile's tokens; neighbours swap, so that each stores two dims
+    // of every second token.
+    wait_prior_grid();
+    const int dim = dim0 + 32 * (warp & 3) + lane;
+    const bool even = (lane & 1) == 0;
+    for (int i = 0; i < hi - lo; ++i) {
+      if (!wait(bar(kDFull + (i & 1)), (i >> 1) & 1, p.err, abort)) break;
+      tc_after();
+      const int n0 = (lo + i) * kTok;
+      for (int c0 = 0; c0 < kTok && n0 + c0 < p.BT; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTok * (i & 1) + c0, v);
+        // tokens of sequences without rows (their latent rows were not written): zeros
+        const int mine = n0 + c0 + lane;
+        const bool none = mine < p.BT && tree_length(p, mine / p.T, false) == 0;
+        const uint32_t empty = __ballot_sync(0xffffffffu, none);
+        if (none && dim0 == 0 && (warp & 3) == 0 && p.lse)
+          p.lse[(size_t)mine * p.H + h] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, even ? v[c + 1] : v[c], 1);
+          const int n = n0 + c0 + c + (even ? 0 : 1);
+          const bool zero = empty >> (c + (even ? 0 : 1)) & 1;
+          const float x = zero ? 0.f : __uint_as_float(even ? v[c] : got);
+          const float y = zero ? 0.f : __uint_as_float(even ? got : v[c + 1]);
+          if (n < p.BT) {
+            __nv_bfloat16* dst = o + ((size_t)n * p.H + h) * dv + (dim & ~1);
+            if ((dv & 1) == 0) {
+              if (dim < dv) *(uint32_t*)dst = pack_bf16(x, y);
+            } else {
+              if ((dim & ~1) < dv) dst[0] = __float2bfloat16_rn(x);
+              if ((dim | 1) < dv) dst[1] = __float2bfloat16_rn(y);
+            }
+          }
+        }
+      }
+      tc_before();
       __syncwarp();
-      if ((i & 1) == 0) store((i >> 1) - 1);
+      if (lane == 0) mbar_arrive(bar(kDEmpty + (i & 1)));
     }
-    if (i + 2 < count) load(i + 2);
-    commit_loads();
   }
-  if (count > 0) {
-    wait(bar_d + 8, ((count - 1) >> 1) & 1);
-    __syncwarp();
-    store((count >> 1) - 1);
-  } else {
-    wait(bar_w, 0);  // the weights have landed before this CTA may exit
-  }
+  __syncwarp();
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 0)
+  if (*abort != 0) {  // loads and products under way without a wait for them end long before this
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < kSettleNs) {
+    }
+  }
+  if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(2 * kTok)
                  : "memory");
+}
+
+// (n, H, 512) bf16 in boxes of 64 dims of one head, 128 tokens
+bool latent_map(CUtensorMap* m, const void* base, int n, int H) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kR, (cuuint64_t)H, (cuuint64_t)n};
+  cuuint64_t strides[2] = {kR * 2, (cuuint64_t)H * kR * 2};
+  cuuint32_t box[3] = {64, 1, kTok}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -303,8 +326,10 @@ cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t st) {
 
 cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void* o,
                             cudaStream_t st) {
-  CUtensorMap w;
-  if (!make_bf16_map(&w, w_uv, kR, (uint64_t)p.H * dv, kR * 2, kDims)) return cudaErrorInvalidValue;
+  CUtensorMap w, hi, lo;
+  if (!make_bf16_map(&w, w_uv, kR, (uint64_t)p.H * dv, kR * 2, kDims) ||
+      !latent_map(&hi, p.latent_hi, p.BT, p.H) || !latent_map(&lo, p.latent_lo, p.BT, p.H))
+    return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> attr_devices{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -319,7 +344,7 @@ cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void*
   const int ctas = p.H * ((dv + kDims - 1) / kDims), tiles = (p.BT + kTok - 1) / kTok;
   const int splits = ctas >= 148 ? 1 : (148 / ctas < tiles ? 148 / ctas : tiles);
   return launch_pdl(tree_out_kernel, dim3((unsigned)(ctas * splits)), dim3(kThreads), kSmem, st,
-                    w, p, dv, splits, (__nv_bfloat16*)o);
+                    w, hi, lo, p, dv, splits, (__nv_bfloat16*)o);
 }
 
 }  // namespace mla

@@ -193,27 +193,33 @@ struct TileWalk {
   const int* lens;  // shared memory: rows of items first .. first + kLenCache - 1
   int first, member, range, begin, end;
   int it, x, len, c;  // current item, its first chunk and its rows; current chunk
-  __device__ int rows_of(int i) const {
-    return i - first < kLenCache ? lens[i - first] : tree_length(*p, i / p->groups, false);
+  int b, row0, stop;  // its sequence, this member's first query row, its end
+  bool idle;          // this member has no query rows in it
+  __device__ __forceinline__ void enter() {
+    b = it / p->groups;
+    const int mt = (it - b * p->groups) * p->team + member;
+    idle = mt >= p->tiles;
+    row0 = mt * kM;
+    stop = x + (len + kRows - 1) / kRows;
   }
-  __device__ bool next(Tile& tl) {
+  __device__ __forceinline__ bool next(Tile& tl) {
     while (c < end) {
-      const int stop = x + (len + kRows - 1) / kRows;
       if (c >= stop) {
         x = stop;
-        len = rows_of(++it);
+        ++it;
+        len = it - first < kLenCache ? lens[it - first] : tree_length(*p, it / p->groups, false);
+        enter();
         continue;
       }
-      const int b = it / p->groups;
-      const int mt = (it - b * p->groups) * p->team + member;
-      if (mt >= p->tiles) {  // this member has no query rows in the item
-        c = min(stop, end);
+      const int to = min(stop, end);
+      if (idle) {
+        c = to;
         continue;
       }
       tl.b = b;
-      tl.row0 = mt * kM;
+      tl.row0 = row0;
       tl.chunk = c - x;
-      tl.nb = min(kTileBlocks, min(stop, end) - c);
+      tl.nb = min(kTileBlocks, to - c);
       tl.len = len;
       tl.ntok = min(tl.nb * kRows, len - tl.chunk * kRows);
       // an item cut by the range leaves a partial result: a range has at most two, its first
@@ -223,7 +229,7 @@ struct TileWalk {
                     : (2 * range + (x > begin ? 1 : 0)) * p->team + member;
       tl.first = c == max(x, begin);
       c += tl.nb;
-      tl.last = c == min(stop, end);
+      tl.last = c == to;
       return true;
     }
     return false;
@@ -452,6 +458,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
 
   TileWalk walk{&p, s_len, work.item, member, range, work.begin, work.end,
                 work.item, work.x, work.begin < work.end ? s_len[0] : 0, work.begin};
+  walk.enter();
   Tile cur;
   bool has = walk.next(cur);
 
