@@ -89,14 +89,15 @@ enum Bar {
   kVFull = kKFull + kKRing,    // kVRing: ... or were fixed
   kQFull = kVFull + kVRing,    // both CTAs' query rows landed
   kSFree,                      // 2: softmax warps of both CTAs copied an S buffer out
-  kPReady = kSFree + 2,        // P written and O rescaled in both CTAs
+  kPReady = kSFree + 2,        // 2: O rescaled and P's first half of the keys written in both
+                               // CTAs; its second half written
   // in each CTA
-  kKEmpty,                     // kKRing: the MMAs reading a stage are complete
+  kKEmpty = kPReady + 2,       // kKRing: the MMAs reading a stage are complete
   kVEmpty = kKEmpty + kKRing,  // kVRing
   kQEmpty = kVEmpty + kVRing,  // the segment's last S is complete
   kSFull,                      // 2: an S buffer is complete
-  kPvDone = kSFull + 2,        // a tile's P . V is complete
-  kRed,                        // the four softmax warps posted their maxima
+  kPvDone = kSFull + 2,        // 2: a tile's P . V is complete over the first half of the keys; all
+  kRed = kPvDone + 2,                      // the four softmax warps posted their maxima
   kSum,                        // ... their sums
   kFix,                        // kVRing: a stage for the fixer landed
   kFinal = kFix + kVRing,      // 2: all products of an MMA warp are complete
@@ -398,7 +399,7 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_q,
-               const TreeParams p) {
+               const __grid_constant__ TreeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t s_base = saddr(smem);
@@ -428,8 +429,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       mbar_init(bar(kSFull + i), 1);
     }
     mbar_init(bar(kPReady), 8);
+    mbar_init(bar(kPReady + 1), 4);
     mbar_init(bar(kQEmpty), 1);
     mbar_init(bar(kPvDone), 1);
+    mbar_init(bar(kPvDone + 1), 1);
     mbar_init(bar(kRed), 4);
     mbar_init(bar(kSum), 4);
     for (int i = 0; i < 2; ++i) mbar_init(bar(kFinal + i), 1);
@@ -543,9 +546,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
         v[k] = pack_bf16(e.x, e.y);
       }
       l = l * alpha + ((s0.x + s0.y) + (s1.x + s1.y));
-      // P . V of the previous tile is complete: P may be overwritten and O rescaled
+      // P's halves change hands one by one, so that the tensor core works on one while the other
+      // is written. The first may be used once O is rescaled in all lanes, which takes all of the
+      // previous tile's P . V: the second half's warps give their part of that before they wait
+      // for their own half. (At a segment's last tile the first half's warps wait for it too:
+      // they come to wait for the last tile's, and phases are waited for one by one.)
+      const bool rescale = !cur.first && __any_sync(0xffffffffu, alpha != 1.f);
       if (t > 0 && !wait(bar(kPvDone), (t - 1) & 1, ctl)) break;
-      if (!cur.first && __any_sync(0xffffffffu, alpha != 1.f)) {
+      if (t > 0 && (rescale || (cur.last && half == 0)) &&
+          !wait(bar(kPvDone + 1), (t - 1) & 1, ctl))
+        break;
+      if (rescale) {
         tc_after();
 #pragma unroll 1
         for (int ch = 0; ch < 8; ++ch) {
@@ -557,6 +568,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
         }
         tmem_wait_st();
         tc_before();
+      }
+      if (half == 1) {
+        __syncwarp();
+        if (lane == 0) arrive_pair(p_ready);
+        if (t > 0 && !wait(bar(kPvDone + 1), (t - 1) & 1, ctl)) break;
       }
       // P in the A-operand layout (K-major, 128-byte rows swizzled by row % 8)
 #pragma unroll
@@ -573,7 +589,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive_pair(p_ready);
+      if (lane == 0) arrive_pair(p_ready + 8u * (uint32_t)half);
 
       if (cur.last) {
         // the row's other half of the keys
@@ -592,7 +608,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
           else if (mine && p.lse) p.lse[out_row] = lse;
         }
         const float inv = total == 0.f ? 0.f : 1.f / total;
-        if (!wait(bar(kPvDone), t & 1, ctl)) break;
+        if (!wait(bar(kPvDone + 1), t & 1, ctl)) break;
         tc_after();
         // O / l leaves through this warp's own 4 KB of P's buffer (32 rows of 128 bytes, 16-byte
         // groups swizzled by row % 8), read back four rows per instruction as whole lines. A
@@ -803,35 +819,39 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       bool ok = true;
       const uint32_t p_lo = desc_lo(s_base + kS_P, 16), ring = desc_lo(s_base + kS_V, kSlabBytes);
       while (ok && has) {
-        if (!wait(bar(kPReady), t & 1, ctl)) break;
-        tc_after();
+        const int hb = cur.half_blocks();
         // where P's block of keys j lies: the second half of the keys from slab 2 on
-        const uint32_t slab = cur.half_blocks() > 1 ? kSlabLo : 2 * kSlabLo;
+        const uint32_t slab = hb > 1 ? kSlabLo : 2 * kSlabLo;
         constexpr uint32_t id = idesc(128, 256, 1);
 #pragma unroll 1
-        for (int j = 0; j < cur.nb && ok; ++j) {
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = wait(bar(kPReady + half), t & 1, ctl);
+          tc_after();
+          const int to = half == 0 ? min(hb, cur.nb) : cur.nb;
 #pragma unroll 1
-          for (int dh = 0; dh < 2; ++dh) {
-            if (!wait(bar(kVFull + at.stage), at.round, ctl)) {
-              ok = false;
-              break;
-            }
-            tc_after();
-            if (elect_one()) {
-              const uint32_t a = p_lo + slab * j, b = ring + kStageLo * at.stage;
-              const uint32_t d = tmem + kColO + 128 * dh;
+          for (int j = half * hb; j < to && ok; ++j) {
+#pragma unroll 1
+            for (int dh = 0; dh < 2; ++dh) {
+              if (!wait(bar(kVFull + at.stage), at.round, ctl)) {
+                ok = false;
+                break;
+              }
+              tc_after();
+              if (elect_one()) {
+                const uint32_t a = p_lo + slab * j, b = ring + kStageLo * at.stage;
+                const uint32_t d = tmem + kColO + 128 * dh;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)  // 16 keys per step; V MN-major: 2 KB apart
-                mma2(d, a + 2 * i, b + 128 * i, id, (cur.first && j == 0 && i == 0) ? 0u : 1u);
-              commit_both(bar(kVEmpty + at.stage));
+                for (int i = 0; i < 4; ++i)  // 16 keys per step; V MN-major: 2 KB apart
+                  mma2(d, a + 2 * i, b + 128 * i, id, (cur.first && j == 0 && i == 0) ? 0u : 1u);
+                commit_both(bar(kVEmpty + at.stage));
+              }
+              __syncwarp();
+              at.step();
             }
-            __syncwarp();
-            at.step();
           }
+          if (ok && elect_one()) commit_both(bar(kPvDone + half));
+          __syncwarp();
         }
-        if (!ok) break;
-        if (elect_one()) commit_both(bar(kPvDone));
-        __syncwarp();
         ++t;
         has = walk.next(cur);
       }

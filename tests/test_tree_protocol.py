@@ -46,15 +46,16 @@ class Model:
         self.tiles, self.planted = tiles, planted
         many = lambda n, c: [Barrier(c) for _ in range(n)]  # noqa: E731
         self.bar = [dict(kfull=many(K_RING, 1), vfull=many(V_RING, 2), qfull=Barrier(1),
-                         sfree=many(2, 8), pready=Barrier(8), kempty=many(K_RING, 1),
+                         sfree=many(2, 8), pready=[Barrier(8), Barrier(4)], kempty=many(K_RING, 1),
                          vempty=many(V_RING, 1), qempty=Barrier(1), sfull=many(2, 1),
-                         pvdone=Barrier(1), red=Barrier(4), fix=many(V_RING, 1))
+                         pvdone=many(2, 1), red=Barrier(4), fix=many(V_RING, 1))
                     for _ in range(2)]
         self.ring = [dict(k=[None] * K_RING, v=[None] * V_RING) for _ in range(2)]
         self.readers = dict(k=[0] * K_RING, v=[0] * V_RING)  # products that may still read
         self.q, self.q_readers = [None, None], 0
         self.s = [[None, None], [None, None]]             # S buffers of each CTA
-        self.p, self.p_readers = [[None] * 4, [None] * 4], 0
+        self.p, self.p_readers = [[None] * 4, [None] * 4], [0, 0]
+        self.rescaled = [[None] * 4, [None] * 4]
         self.events = []                                  # landing loads
         self.mma = [[], []]                               # each MMA warp's products, in order
         self.done_pv = []
@@ -193,18 +194,22 @@ class Model:
     def mma_pv(self):
         used = 0
         for t, tl in enumerate(self.tiles):
-            yield from self.wait(self.bar[0]["pready"], t)
-            assert self.p == [[t] * 4] * 2
-            self.p_readers += 1
-            for j in range(tl["nb"]):
-                for dh in range(2):
-                    yield from self.use(1, "v", used, (t, j, dh))
-                    used += 1
+            hb = 2 if tl["nb"] > 2 else 1
+            for half in range(2):
+                yield from self.wait(self.bar[0]["pready"][half], t)
+                assert [p[2 * half:2 * half + 2] for p in self.p] == [[t] * 2] * 2
+                assert min(map(min, self.rescaled)) >= t, "O used before it was rescaled"
+                self.p_readers[half] += 1
+                for j in range(half * hb, min(hb, tl["nb"]) if half == 0 else tl["nb"]):
+                    for dh in range(2):
+                        yield from self.use(1, "v", used, (t, j, dh))
+                        used += 1
 
-            def pv_done(t=t):
-                self.p_readers -= 1
-                self.done_pv.append(t)
-            self.commit(1, "pvdone", after=pv_done)
+                def pv_done(t=t, half=half):
+                    self.p_readers[half] -= 1
+                    if half:
+                        self.done_pv.append(t)
+                self.commit(1, "pvdone", half, pv_done)
 
     # -- a softmax warp
     def softmax(self, rank, w):
@@ -218,17 +223,27 @@ class Model:
             self.bar[0]["sfree"][t & 1].arrive()
             yield
             self.bar[rank]["red"].arrive()
-            while not self.bar[rank]["red"].passes(t & 1, t):
-                yield
+            yield from self.wait(self.bar[rank]["red"], t)
+            half = w // 2
+            rescale = not tl["first"] and tl["rescale"]
             if t > 0 and self.planted != "p":
-                yield from self.wait(self.bar[rank]["pvdone"], t - 1)
-            assert self.p_readers == 0, "P overwritten while a product may read it"
+                yield from self.wait(self.bar[rank]["pvdone"][0], t - 1)
+                if rescale or (tl["last"] and half == 0):
+                    yield from self.wait(self.bar[rank]["pvdone"][1], t - 1)
+            if rescale and self.planted != "p":
+                assert self.done_pv[-1] == t - 1 and self.p_readers == [0, 0]
+            self.rescaled[rank][w] = t
+            if half == 1:
+                self.bar[0]["pready"][0].arrive()
+                yield
+                if t > 0 and self.planted != "p":
+                    yield from self.wait(self.bar[rank]["pvdone"][1], t - 1)
+            assert self.p_readers[half] == 0, "P overwritten while a product may read it"
             self.p[rank][w] = t
             yield
-            self.bar[0]["pready"].arrive()
+            self.bar[0]["pready"][half].arrive()
             if tl["last"]:
-                while not self.bar[rank]["pvdone"].passes(t & 1, t):
-                    yield
+                yield from self.wait(self.bar[rank]["pvdone"][1], t)
                 assert self.done_pv[-1] == t, "O read while the next segment's products run"
 
     def run(self):
@@ -236,12 +251,17 @@ class Model:
         for r in range(2):
             procs += [self.load_k(r), self.load_v(r), self.fixer(r)]
             procs += [self.softmax(r, w) for w in range(4)]
+        # some warps, and the loads, may be much slower than others
+        pace = {id(x): self.rng.choice([1.0, 1.0, 0.3, 0.03]) for x in procs}
+        engines = self.rng.choice([0.5, 0.9, 0.05])
         idle = 0
         while procs:
-            if self.rng.random() < 0.5 and self.step_async():
+            if self.rng.random() < engines and self.step_async():
                 idle = 0
                 continue
             i = self.rng.randrange(len(procs))
+            if self.rng.random() > pace[id(procs[i])]:
+                continue
             try:
                 next(procs[i])
             except StopIteration:
@@ -249,10 +269,10 @@ class Model:
                 idle = 0
                 continue
             idle += 1
-            if idle > 4000 and not self.events and not any(self.mma):
+            if idle > 60000 and not self.events and not any(self.mma):
                 state = [(x.__name__, x.gi_frame.f_lineno) for x in procs]
                 raise AssertionError(f"no progress: {state}")
-            if idle > 200000:
+            if idle > 2000000:
                 raise AssertionError("no progress")
 
 
@@ -263,7 +283,7 @@ def draw_tiles(rng):
         while left:
             nb = min(4, left)
             left -= nb
-            tiles.append(dict(seg=s, first=first, last=left == 0, nb=nb,
+            tiles.append(dict(seg=s, first=first, rescale=rng.random() < 0.3, last=left == 0, nb=nb,
                               fix=[left == 0 and j >= nb - 2 and rng.random() < 0.7
                                    for j in range(nb)]))
             first = False
