@@ -16,6 +16,17 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Waits for a phase up to about 0.1 ms in hardware, which takes no issue slots from the warps that
+// share the scheduler (a warp that polls does).
+__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity), "r"(100000u) : "memory");
+  return ok != 0;
+}
+
 // Shared-memory matrix descriptors of 128-byte swizzled slabs, 8-row groups 1024 bytes apart
 // (as sdesc builds them): the high word is constant, the low word holds the start and the
 // leading offset, and moves by bytes / 16.

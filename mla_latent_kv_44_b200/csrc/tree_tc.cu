@@ -25,17 +25,18 @@
 // Softmax: four warps, a thread holds one query row and half of the tile's keys (TMEM lane), two
 // threads of a row exchange their maxima; base-2 exponents, the running maximum moved only when
 // a tile exceeds it by 2^8, the sum l of the fp32 weights. The same warps rescale O when the
-// maximum moves and write O / l at a segment's end.
+// maximum moves. At a segment's end four other warps write O / l, so that the softmax of the next
+// segment goes on meanwhile.
 //
 // Rows that a token does not see: the prefix (rows before the drafted ones) is seen by all; for
 // the drafted rows a thread builds the 32-bit words of its keys from its token's mask, and a
 // masked score becomes -inf by selection. P = 0 times a masked row's V would still be NaN if the
 // row held NaN, so the V stages that hold drafted rows (or rows past the end) pass through the
-// fixer warp, which replaces what is not finite by 0 before the MMA may read it.
+// finishing warps, which replace what is not finite by 0 before the MMA may read it.
 //
 // Warps: 0 TMA of Q and K, 3 of V; 1 issues S, 2 issues P . V (both in the pair's first CTA); 4-7
-// softmax and epilogue; 8 fixer. Every wait is bounded: on timeout the kernel sets MLA_DEV_WAIT_TIMEOUT, lets what it
-// issued end, frees TMEM and returns. No TMA multicast is used.
+// softmax; 8-11 fix V and write O. Every wait is bounded: on timeout the kernel sets
+// MLA_DEV_WAIT_TIMEOUT, lets what it issued end, frees TMEM and returns. No TMA multicast is used.
 #include <atomic>
 
 #include "plan_body.cuh"
@@ -61,11 +62,10 @@ constexpr int kVRing = 3;                 // stages of the V ring
 constexpr int kKStages = kD / 64;         // stages of a tile's K
 constexpr int kQBytes = kKStages * kSlabBytes;
 constexpr int kPBytes = kTileBlocks * kSlabBytes;
-constexpr int kThreads = 384;             // three warpgroups
-// Registers per thread: 384 threads launch with 168 each (64,512); the softmax warpgroup holds 128
-// scores in registers and takes 240, the two others give 80 each: (88 + 240 + 88) * 128 = 53,248.
-constexpr int kRegsSoftmax = 224, kRegsOther = 88;
-static_assert((kRegsSoftmax + 2 * kRegsOther) * 128 <= 168 * kThreads, "registers of a CTA");
+constexpr int kThreads = 384;             // three warpgroups: issue, softmax, finish
+constexpr int kFinishWarps = 4;
+// 168 registers a thread. (Moving registers to the softmax warps, which hold 128 scores, made the
+// compiler spill more in all roles: 540 against 490 us for 32 x 16384 rows x 4 tokens.)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;           // S buffers at columns 0 and 128
 constexpr uint32_t kStageLo = kStageBytes >> 4, kSlabLo = kSlabBytes >> 4;  // in descriptors
@@ -78,7 +78,8 @@ constexpr int kS_Q = kS_V + kVRing * kStageBytes;         // 112 KB
 constexpr int kS_P = kS_Q + kQBytes;                      // 184 KB
 constexpr int kS_Red = kS_P + kPBytes;                    // 216 KB: max[2 tiles][2 halves][64]
 constexpr int kS_Sum = kS_Red + 4 * kMH * 4;              // l[2 segments][2 halves][64]
-constexpr int kS_Len = kS_Sum + 4 * kMH * 4;
+constexpr int kS_Inv = kS_Sum + 4 * kMH * 4;              // 1 / l[2 segments][64]
+constexpr int kS_Len = kS_Inv + 2 * kMH * 4;
 constexpr int kLenCache = 256;
 constexpr int kS_Plan = kS_Len + kLenCache * 4;           // 64 ints of the schedule's scans
 constexpr int kS_Bar = kS_Plan + 64 * 4;
@@ -91,15 +92,18 @@ enum Bar {
   kSFree,                      // 2: softmax warps of both CTAs copied an S buffer out
   kPReady = kSFree + 2,        // 2: O rescaled and P's first half of the keys written in both
                                // CTAs; its second half written
+  kOFree = kPReady + 2,        // O of the segment was read out in both CTAs
   // in each CTA
-  kKEmpty = kPReady + 2,       // kKRing: the MMAs reading a stage are complete
+  kKEmpty,                     // kKRing: the MMAs reading a stage are complete
   kVEmpty = kKEmpty + kKRing,  // kVRing
   kQEmpty = kVEmpty + kVRing,  // the segment's last S is complete
-  kSFull,                      // 2: an S buffer is complete
+  kSegDone,                    // the segment's last P . V is complete
+  kLReady,                     // 2: 1 / l of an even / odd segment's rows is in shared memory
+  kSFull = kLReady + 2,        // 2: an S buffer is complete
   kPvDone = kSFull + 2,        // 2: a tile's P . V is complete over the first half of the keys; all
-  kRed = kPvDone + 2,                      // the four softmax warps posted their maxima
+  kRed = kPvDone + 2,          // the four softmax warps posted their maxima
   kSum,                        // ... their sums
-  kFix,                        // kVRing: a stage for the fixer landed
+  kFix,                        // kVRing: a stage to be fixed landed
   kFinal = kFix + kVRing,      // 2: all products of an MMA warp are complete
   kNumBars = kFinal + 2
 };
@@ -144,6 +148,10 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
 struct Ctl {
   uint32_t* err;
   volatile int* abort;
@@ -155,7 +163,7 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_
                                           volatile int* abort) {
   uint64_t t0 = 0;
   for (int it = 0;; ++it) {
-    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_try_long(bar, parity))) return true;
     if (it == 0) t0 = globaltimer();
     const bool late = (globaltimer() - t0) > kTimeoutNs;
     if (__any_sync(0xffffffffu, *abort != 0 || late)) {
@@ -168,7 +176,7 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_
   }
 }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
-  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, mbar_try_long(bar, parity))) return true;
   return wait_slow(bar, parity, c.err, c.abort);
 }
 // Bounded wait for a phase that normally completed long ago (drains at teardown).
@@ -348,7 +356,10 @@ __device__ Range plan_range(const TreeParams& p, int range, int* s_plan, int* s_
     __syncthreads();
   }
   const int C = s_total[0];
-  const int R = min(C, p.ranges);
+  // A range holds two chunks at least, four where more would mean many partial results (each is
+  // 256 KB): 8 tokens x 1000 rows took 32.4 us cut into single chunks, 32.0 into twos, 29.6 into
+  // fours; 3 x 5 tokens of 16 heads x up to 1000 rows 28.9, 26.1 and 30.4.
+  const int R = min(p.ranges, max((C + 3) / 4, min((C + 1) / 2, 32 / p.team)));
   Range w{0, 0, 0, 0};
   // one thread block per range says whether an item that began in the range before goes on here
   const bool writer = range < p.ranges && (blockIdx.x & 1) == 0 && (blockIdx.x >> 1) % p.team == 0;
@@ -388,6 +399,34 @@ __device__ Range plan_range(const TreeParams& p, int range, int* s_plan, int* s_
   return w;
 }
 
+// Four lanes with 64 bytes each of a row of their own (w: four 16-byte pieces) change them round,
+// so that lane i holds piece i of the group's rows, and write them: a store instruction then
+// covers 64 bytes of eight rows. dst: the warp's row 0; only rows below `rows` are written.
+__device__ __forceinline__ void put_rows(uint32_t (&w)[16], char* dst, int pitch, int rows,
+                                         int lane) {
+#pragma unroll
+  for (int step = 1; step < 4; step <<= 1) {
+    const bool up = lane & step;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q & step) continue;  // pieces q and q + step change places across the pair
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t &a = w[4 * q + i], &b = w[4 * (q + step) + i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, step);
+        if (up) a = got;
+        else b = got;
+      }
+    }
+  }
+  const int r0 = lane & ~3;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (r0 + k < rows)
+      *(uint4*)(dst + (size_t)(r0 + k) * pitch + 16 * (lane & 3)) =
+          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+}
+
 // the 16-byte piece with every bf16 that is not finite replaced by 0
 __device__ __forceinline__ uint32_t finite2(uint32_t v) {
   if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
@@ -405,6 +444,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   const uint32_t s_base = saddr(smem);
   uint32_t* tmem_slot = (uint32_t*)(smem + kS_Bar + kNumBars * 8);
   volatile int* abort_flag = (volatile int*)(smem + kS_Bar + kNumBars * 8 + 4);
+  float* s_inv = (float*)(smem + kS_Inv);
   int* s_len = (int*)(smem + kS_Len);
   int* s_plan = (int*)(smem + kS_Plan);
   auto bar = [&](int i) { return s_base + kS_Bar + 8u * (uint32_t)i; };
@@ -419,7 +459,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       mbar_init(bar(kKEmpty + i), 1);
     }
     for (int i = 0; i < kVRing; ++i) {
-      mbar_init(bar(kVFull + i), 2);
+      mbar_init(bar(kVFull + i), 2 * kFinishWarps);
       mbar_init(bar(kVEmpty + i), 1);
       mbar_init(bar(kFix + i), 1);
     }
@@ -431,6 +471,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     mbar_init(bar(kPReady), 8);
     mbar_init(bar(kPReady + 1), 4);
     mbar_init(bar(kQEmpty), 1);
+    mbar_init(bar(kSegDone), 1);
+    mbar_init(bar(kLReady), 2);
+    mbar_init(bar(kLReady + 1), 2);
+    mbar_init(bar(kOFree), 2 * kFinishWarps);
     mbar_init(bar(kPvDone), 1);
     mbar_init(bar(kPvDone + 1), 1);
     mbar_init(bar(kRed), 4);
@@ -466,8 +510,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   bool has = walk.next(cur);
 
   if (warp >= 4 && warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    // -------------------------------------------------------------- softmax, rescale, epilogue
+    // ------------------------------------------------------------------------ softmax, rescale
     // TMEM lane 32 * quad + lane: query row `row` of this CTA, half `half` of the tile's keys
     // in S, and of each 256 latent dims in O
     const int quad = warp & 3, half = quad >> 1;
@@ -477,8 +520,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     float* red = (float*)(smem + kS_Red);
     float* sum = (float*)(smem + kS_Sum);
     const uint32_t p_row = s_base + kS_P + (uint32_t)(2 * half) * kSlabBytes + (uint32_t)row * 128;
-    const uint32_t box = s_base + kS_P + (uint32_t)(2 * half) * kSlabBytes +
-                         (uint32_t)(quad & 1) * 4096;  // written by this warp alone
     const uint32_t s_free = peer_addr(bar(kSFree), 0), p_ready = peer_addr(bar(kPReady), 0);
     int t = 0, seg = 0;
     float m_ref = 0.f, l = 0.f;
@@ -549,14 +590,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       // P's halves change hands one by one, so that the tensor core works on one while the other
       // is written. The first may be used once O is rescaled in all lanes, which takes all of the
       // previous tile's P . V: the second half's warps give their part of that before they wait
-      // for their own half. (At a segment's last tile the first half's warps wait for it too:
-      // they come to wait for the last tile's, and phases are waited for one by one.)
+      // for their own half.
       const bool rescale = !cur.first && __any_sync(0xffffffffu, alpha != 1.f);
       if (t > 0 && !wait(bar(kPvDone), (t - 1) & 1, ctl)) break;
-      if (t > 0 && (rescale || (cur.last && half == 0)) &&
-          !wait(bar(kPvDone + 1), (t - 1) & 1, ctl))
-        break;
       if (rescale) {
+        if (t > 0 && !wait(bar(kPvDone + 1), (t - 1) & 1, ctl)) break;
         tc_after();
 #pragma unroll 1
         for (int ch = 0; ch < 8; ++ch) {
@@ -592,104 +630,130 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
       if (lane == 0) arrive_pair(p_ready + 8u * (uint32_t)half);
 
       if (cur.last) {
-        // the row's other half of the keys
+        // l with the row's other half of the keys; the finishing warps take over from here
         float* st = sum + (seg & 1) * 2 * kMH;
         st[half * kMH + row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kSum));
         if (!wait(bar(kSum), seg & 1, ctl)) break;
-        const float total = st[row] + st[kMH + row];
-        ++seg;
-        const bool mine = my_row < p.T * p.H;
-        const size_t out_row = (size_t)cur.b * p.T * p.H + my_row;
         if (half == 0) {
+          const float total = st[row] + st[kMH + row];
+          s_inv[(seg & 1) * kMH + row] = total == 0.f ? 0.f : 1.f / total;
           const float lse = (m_ref + __log2f(total)) * 0.6931471805599453f;
           if (cur.slot >= 0) p.part_lse[(size_t)cur.slot * kM + kMH * rank + row] = lse;
-          else if (mine && p.lse) p.lse[out_row] = lse;
+          else if (my_row < p.T * p.H && p.lse) p.lse[(size_t)cur.b * p.T * p.H + my_row] = lse;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kLReady + (seg & 1)));
         }
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        if (!wait(bar(kPvDone + 1), t & 1, ctl)) break;
-        tc_after();
-        // O / l leaves through this warp's own 4 KB of P's buffer (32 rows of 128 bytes, 16-byte
-        // groups swizzled by row % 8), read back four rows per instruction as whole lines. A
-        // partial result stays in fp32; a finished one becomes two bf16 terms.
-        const int rsub = lane >> 3, g = (lane & 7) ^ rsub;
-        const uint32_t w_row = box + 128u * (uint32_t)lane;
-        const bool part = cur.slot >= 0;
-        const int rows = part ? 32 : p.T * p.H - (my_row - lane);  // rows to write
-        char* dst = part ? (char*)(p.part_o +
-                                   ((size_t)cur.slot * kM + kMH * rank + 32 * (quad & 1)) * kR)
-                         : (char*)(p.latent_hi + (out_row - lane) * kR);
-        const int64_t lo = (char*)p.latent_lo - (char*)p.latent_hi;
-        const int pitch = part ? kR * 4 : kR * 2;
-        dst += (size_t)rsub * pitch + 16 * (lane & 7);
-        // columns 64 ch ..: dims 256 (ch / 2) + 128 half + 64 (ch % 2)
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t o[64];
-          tmem_ld64(tq + kColO + 64 * ch, o);
-          const int dim = 256 * (ch >> 1) + 128 * half + 64 * (ch & 1);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-          auto flush = [&](int64_t at) {  // the box's rows, to byte `at` of the output rows
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint4 x;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                           : "r"(box + 128u * (uint32_t)(4 * i + rsub) +
-                                 16u * (uint32_t)((i & 1) ? g ^ 4 : g))
-                           : "memory");
-              if (4 * i + rsub < rows) *(uint4*)(dst + (size_t)(4 * i) * pitch + at) = x;
-            }
-            __syncwarp();
-          };
-          if (part) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 w_row + 16u * (uint32_t)(u ^ (lane & 7))),
-                             "r"(o[32 * h + 4 * u]), "r"(o[32 * h + 4 * u + 1]),
-                             "r"(o[32 * h + 4 * u + 2]), "r"(o[32 * h + 4 * u + 3])
-                             : "memory");
-              flush(4 * (dim + 32 * h));
-            }
-          } else {
-#pragma unroll
-            for (int term = 0; term < 2; ++term) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  float x = __uint_as_float(o[8 * u + 2 * k]);
-                  float y = __uint_as_float(o[8 * u + 2 * k + 1]);
-                  w[k] = pack_bf16(x, y);
-                  if (term == 0) {  // what the first term leaves
-                    o[8 * u + 2 * k] = __float_as_uint(x - __uint_as_float(w[k] << 16));
-                    o[8 * u + 2 * k + 1] =
-                        __float_as_uint(y - __uint_as_float(w[k] & 0xffff0000u));
-                  }
-                }
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 w_row + 16u * (uint32_t)(u ^ (lane & 7))),
-                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                             : "memory");
-              }
-              flush(2 * dim + term * lo);
-            }
-          }
-        }
-        tc_before();
+        ++seg;
       }
       ++t;
       has = walk.next(cur);
     }
+  } else if (warp >= 8) {
+    // --------------------------------------------- fixes of V; O / l out at a segment's end
+    Cursor<kVRing> at;
+    uint32_t fixes = 0;  // per stage: parity of its next fix
+    int seg = 0;
+    bool ok = true;
+    const uint32_t full0 = peer_addr(bar(kVFull), 0), o_free = peer_addr(bar(kOFree), 0);
+    const int quad = warp & 3, half = quad >> 1, tid = threadIdx.x - 256;
+    const uint32_t to_ = tmem + ((uint32_t)(32 * quad) << 16) + kColO;
+    while (ok && has) {
+      for (int j = 0; j < cur.nb && ok; ++j) {
+        const bool fix = needs_fix(cur, j, p.T);
+        // rows of the block: up to `from` are the prefix; from `to` on they lie past the end
+        const int from = max(cur.len - p.T - (cur.chunk + j) * kRows, 0);
+        const int to = min(cur.len - (cur.chunk + j) * kRows, kRows);
+#pragma unroll 1
+        for (int dh = 0; dh < 2; ++dh, at.step()) {
+          if (!fix) continue;
+          if (!wait(bar(kFix + at.stage), fixes >> at.stage & 1, ctl)) {
+            ok = false;
+            break;
+          }
+          fixes ^= 1u << at.stage;
+          // 16-byte pieces of rows from .. 63 of both slabs, all reads before the writes
+          uint4* st = (uint4*)(smem + kS_V + at.stage * kStageBytes);
+          uint4 x[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = 8 * from + tid + 128 * (u >> 1);
+            if (i < 8 * to) x[u] = st[(u & 1) * (kSlabBytes / 16) + i];
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = 8 * from + tid + 128 * (u >> 1);
+            uint4* at_ = st + (u & 1) * (kSlabBytes / 16) + i;
+            if (i < 8 * to) {
+              const uint4 y = make_uint4(finite2(x[u].x), finite2(x[u].y), finite2(x[u].z),
+                                         finite2(x[u].w));
+              if (x[u].x != y.x || x[u].y != y.y || x[u].z != y.z || x[u].w != y.w) *at_ = y;
+            } else if (i < 8 * kRows) {
+              *at_ = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) arrive_pair(full0 + 8u * (uint32_t)at.stage);
+        }
+      }
+      if (ok && cur.last) {
+        // (the softmax may be one segment ahead, not two: it needs that one's P . V)
+        if (!wait(bar(kLReady + (seg & 1)), (seg >> 1) & 1, ctl) ||
+            !wait(bar(kSegDone), seg & 1, ctl))
+          break;
+        tc_after();
+        const float inv = s_inv[(seg & 1) * kMH + 32 * (quad & 1) + lane];
+        // A partial result stays in fp32; a finished one becomes two bf16 terms. Lane i of a
+        // group of four ends up with piece i of the group's four rows (put_rows), so that 64
+        // bytes of a row are written at a time.
+        const bool cut = cur.slot >= 0;
+        const int r0 = cur.row0 + kMH * (int)rank + 32 * (quad & 1);  // the warp's first row
+        const int rows = cut ? 32 : p.T * p.H - r0;                   // rows to write
+        const size_t row = cut ? (size_t)cur.slot * kM + kMH * rank + 32 * (quad & 1)
+                               : (size_t)cur.b * p.T * p.H + r0;
+        char* dst = cut ? (char*)(p.part_o + row * kR) : (char*)(p.latent_hi + row * kR);
+        const int64_t lo = (char*)p.latent_lo - (char*)p.latent_hi;
+        const int pitch = cut ? kR * 4 : kR * 2;
+        // columns 32 ch ..: dims 256 (ch / 4) + 128 half + 32 (ch % 4)
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(to_ + 32 * ch, o);
+          const int dim = 256 * (ch >> 2) + 128 * half + 32 * (ch & 3);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          uint32_t w[16];
+          if (cut) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = o[16 * u + i];
+              put_rows(w, dst + 4 * dim + 64 * u, pitch, rows, lane);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = __uint_as_float(o[2 * i]), y = __uint_as_float(o[2 * i + 1]);
+              w[i] = pack_bf16(x, y);
+              o[i] = pack_bf16(x - __uint_as_float(w[i] << 16),
+                               y - __uint_as_float(w[i] & 0xffff0000u));
+            }
+            put_rows(w, dst + 2 * dim, pitch, rows, lane);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = o[i];
+            put_rows(w, dst + 2 * dim + lo, pitch, rows, lane);
+          }
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(o_free);
+        ++seg;
+      }
+      has = walk.next(cur);
+    }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 0) {
       // --------------------------------------------------------------------------- TMA: Q and K
       // Loads are counted on the first CTA's barriers: it expects the bytes of both CTAs.
@@ -759,8 +823,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
                 full = bar(kFix + at.stage);
                 mbar_expect_tx(full, kStageBytes);
               } else if (rank == 0) {
-                // both arrivals, which the fixers give otherwise
-                mbar_arrive(full);
+                // all arrivals, which the finishing warps give otherwise
+                mbar_arrive_n(bar(kVFull + at.stage), 2 * kFinishWarps - 1);
                 mbar_expect_tx(bar(kVFull + at.stage), 2 * kStageBytes);
               }
               tma_load_pair(dst, &tm_kv, full, x, y);
@@ -815,10 +879,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     } else if (warp == 2 && rank == 0) {
       // ---------------------------------------------------------------------------- MMA: O += P . V
       Cursor<kVRing> at;
-      int t = 0;
+      int t = 0, seg = 0;
       bool ok = true;
       const uint32_t p_lo = desc_lo(s_base + kS_P, 16), ring = desc_lo(s_base + kS_V, kSlabBytes);
       while (ok && has) {
+        if (cur.first) {
+          // the segment before was read out of O
+          if (seg > 0 && !wait(bar(kOFree), (seg - 1) & 1, ctl)) break;
+          ++seg;
+        }
         const int hb = cur.half_blocks();
         // where P's block of keys j lies: the second half of the keys from slab 2 on
         const uint32_t slab = hb > 1 ? kSlabLo : 2 * kSlabLo;
@@ -849,52 +918,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
               at.step();
             }
           }
-          if (ok && elect_one()) commit_both(bar(kPvDone + half));
+          if (ok && elect_one()) {
+            commit_both(bar(kPvDone + half));
+            if (half == 1 && cur.last) commit_both(bar(kSegDone));
+          }
           __syncwarp();
         }
         ++t;
-        has = walk.next(cur);
-      }
-    } else if (warp == 8) {
-      // -------------------------------------------------------------------------------- fixer
-      Cursor<kVRing> at;
-      uint32_t fixes = 0;  // per stage: parity of its next fix
-      bool ok = true;
-      const uint32_t full0 = peer_addr(bar(kVFull), 0);
-      while (ok && has) {
-        for (int j = 0; j < cur.nb && ok; ++j) {
-          const bool fix = needs_fix(cur, j, p.T);
-          // rows of the block: up to `from` are the prefix; from `to` on they lie past the end
-          const int from = max(cur.len - p.T - (cur.chunk + j) * kRows, 0);
-          const int to = min(cur.len - (cur.chunk + j) * kRows, kRows);
-          for (int dh = 0; dh < 2; ++dh, at.step()) {
-            if (!fix) continue;
-            if (!wait(bar(kFix + at.stage), fixes >> at.stage & 1, ctl)) {
-              ok = false;
-              break;
-            }
-            fixes ^= 1u << at.stage;
-            uint8_t* st = smem + kS_V + at.stage * kStageBytes;
-            // 16-byte pieces of rows from .. 63 of both slabs
-            for (int i = 8 * from + lane; i < 8 * kRows; i += 32) {
-#pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                uint4* v = (uint4*)(st + s * kSlabBytes) + i;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (i < 8 * to) {
-                  const uint4 y = *v;
-                  x = make_uint4(finite2(y.x), finite2(y.y), finite2(y.z), finite2(y.w));
-                  if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
-                }
-                *v = x;
-              }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) arrive_pair(full0 + 8u * (uint32_t)at.stage);
-            __syncwarp();
-          }
-        }
         has = walk.next(cur);
       }
     }

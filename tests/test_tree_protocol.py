@@ -1,6 +1,6 @@
 """A model of the tree-attention kernel's barrier protocol (csrc/tree_tc.cu) under random
-interleavings: two CTAs, each with a loading warp for Q and K, one for V, a fixer and four softmax
-warps, and the first CTA's two MMA warps (scores; P . V). Loads land and MMAs complete after random delays. Checked:
+interleavings: two CTAs, each with a loading warp for Q and K, one for V, four softmax and four
+finishing warps, and the first CTA's two MMA warps (scores; P . V). Loads land and MMAs complete after random delays. Checked:
 no deadlock, no parity wait that passes on the wrong phase, no stage refilled or buffer
 overwritten while a product may still read it, and every product reads what it should."""
 import random
@@ -45,10 +45,11 @@ class Model:
         self.rng = random.Random(seed)
         self.tiles, self.planted = tiles, planted
         many = lambda n, c: [Barrier(c) for _ in range(n)]  # noqa: E731
-        self.bar = [dict(kfull=many(K_RING, 1), vfull=many(V_RING, 2), qfull=Barrier(1),
+        self.bar = [dict(kfull=many(K_RING, 1), vfull=many(V_RING, 8), qfull=Barrier(1),
                          sfree=many(2, 8), pready=[Barrier(8), Barrier(4)], kempty=many(K_RING, 1),
                          vempty=many(V_RING, 1), qempty=Barrier(1), sfull=many(2, 1),
-                         pvdone=many(2, 1), red=Barrier(4), fix=many(V_RING, 1))
+                         pvdone=many(2, 1), red=Barrier(4), sum=Barrier(4), fix=many(V_RING, 1),
+                         ofree=Barrier(8), lready=many(2, 2), segdone=Barrier(1))
                     for _ in range(2)]
         self.ring = [dict(k=[None] * K_RING, v=[None] * V_RING) for _ in range(2)]
         self.readers = dict(k=[0] * K_RING, v=[0] * V_RING)  # products that may still read
@@ -56,6 +57,7 @@ class Model:
         self.s = [[None, None], [None, None]]             # S buffers of each CTA
         self.p, self.p_readers = [[None] * 4, [None] * 4], [0, 0]
         self.rescaled = [[None] * 4, [None] * 4]
+        self.inv, self.o_readers = [[None, None], [None, None]], 0
         self.events = []                                  # landing loads
         self.mma = [[], []]                               # each MMA warp's products, in order
         self.done_pv = []
@@ -125,26 +127,37 @@ class Model:
                         bar.arrive(1)
                         key = ("raw",) + key
                     elif rank == 0:
-                        bar.arrive()
+                        for _ in range(7):
+                            bar.arrive()
                         bar.arrive(2)
                     self.load(self.put(rank, "v", st, key), key, bar)
                     used += 1
                     yield
 
-    def fixer(self, rank):
+    def finisher(self, rank, w):
         used, n_fix = 0, [0] * V_RING
         for t, tl in enumerate(self.tiles):
             for j in range(tl["nb"]):
                 for dh in range(2):
-                    st = used % V_RING
+                    st, key = used % V_RING, (t, j, dh)
                     if tl["fix"][j]:
                         yield from self.wait(self.bar[rank]["fix"][st], n_fix[st])
                         n_fix[st] += 1
-                        assert self.ring[rank]["v"][st] == ("raw", t, j, dh)
-                        self.ring[rank]["v"][st] = (t, j, dh)
+                        held = self.ring[rank]["v"][st]
+                        part = 1 if held == ("raw",) + key else held[1] + 1
+                        assert part == 1 or held == ("fixed", part - 1) + key
+                        self.ring[rank]["v"][st] = key if part == 4 else ("fixed", part) + key
                         self.bar[0]["vfull"][st].arrive()
                         yield
                     used += 1
+            if tl["last"]:
+                yield from self.wait(self.bar[rank]["lready"][tl["seg"] & 1], tl["seg"] >> 1)
+                yield from self.wait(self.bar[rank]["segdone"], tl["seg"])
+                assert self.done_pv[-1] == t, "O read while the next segment's products run"
+                assert self.inv[rank][tl["seg"] & 1] == tl["seg"]
+                yield
+                assert self.done_pv[-1] == t and self.o_readers == 0
+                self.bar[0]["ofree"].arrive()
 
     # -- the MMA warps
     def commit(self, w, name, i=None, after=None):
@@ -195,11 +208,14 @@ class Model:
         used = 0
         for t, tl in enumerate(self.tiles):
             hb = 2 if tl["nb"] > 2 else 1
+            if tl["first"] and tl["seg"] > 0 and self.planted != "o":
+                yield from self.wait(self.bar[0]["ofree"], tl["seg"] - 1)
             for half in range(2):
                 yield from self.wait(self.bar[0]["pready"][half], t)
                 assert [p[2 * half:2 * half + 2] for p in self.p] == [[t] * 2] * 2
                 assert min(map(min, self.rescaled)) >= t, "O used before it was rescaled"
                 self.p_readers[half] += 1
+                self.o_readers += 1
                 for j in range(half * hb, min(hb, tl["nb"]) if half == 0 else tl["nb"]):
                     for dh in range(2):
                         yield from self.use(1, "v", used, (t, j, dh))
@@ -207,9 +223,12 @@ class Model:
 
                 def pv_done(t=t, half=half):
                     self.p_readers[half] -= 1
+                    self.o_readers -= 1
                     if half:
                         self.done_pv.append(t)
                 self.commit(1, "pvdone", half, pv_done)
+                if half and tl["last"]:
+                    self.commit(1, "segdone")
 
     # -- a softmax warp
     def softmax(self, rank, w):
@@ -228,7 +247,7 @@ class Model:
             rescale = not tl["first"] and tl["rescale"]
             if t > 0 and self.planted != "p":
                 yield from self.wait(self.bar[rank]["pvdone"][0], t - 1)
-                if rescale or (tl["last"] and half == 0):
+                if rescale:
                     yield from self.wait(self.bar[rank]["pvdone"][1], t - 1)
             if rescale and self.planted != "p":
                 assert self.done_pv[-1] == t - 1 and self.p_readers == [0, 0]
@@ -243,13 +262,17 @@ class Model:
             yield
             self.bar[0]["pready"][half].arrive()
             if tl["last"]:
-                yield from self.wait(self.bar[rank]["pvdone"][1], t)
-                assert self.done_pv[-1] == t, "O read while the next segment's products run"
+                self.bar[rank]["sum"].arrive()
+                yield from self.wait(self.bar[rank]["sum"], tl["seg"])
+                if half == 0:
+                    self.inv[rank][tl["seg"] & 1] = tl["seg"]
+                    self.bar[rank]["lready"][tl["seg"] & 1].arrive()
 
     def run(self):
         procs = [self.mma_s(), self.mma_pv()]
         for r in range(2):
-            procs += [self.load_k(r), self.load_v(r), self.fixer(r)]
+            procs += [self.load_k(r), self.load_v(r)]
+            procs += [self.finisher(r, w) for w in range(4)]
             procs += [self.softmax(r, w) for w in range(4)]
         # some warps, and the loads, may be much slower than others
         pace = {id(x): self.rng.choice([1.0, 1.0, 0.3, 0.03]) for x in procs}
@@ -296,9 +319,9 @@ def test_protocol_under_random_interleavings(seed):
     Model(draw_tiles(rng), seed).run()
 
 
-@pytest.mark.parametrize("planted", ["q", "p"])
+@pytest.mark.parametrize("planted", ["q", "p", "o"])
 def test_a_missing_wait_is_found(planted):
-    """Negative controls: Q replaced without its wait, P written without its wait."""
+    """Negative controls: Q replaced, P written and O begun anew without their waits."""
     found = 0
     for seed in range(40):
         try:
