@@ -109,7 +109,9 @@ class _Lib:
     def __getattr__(self, name):
         if _Lib._handle is None:
             _Lib._handle = _load()
-        return getattr(_Lib._handle, name)
+        fn = getattr(_Lib._handle, name)
+        self.__dict__[name] = fn  # found without this call from now on
+        return fn
 
 
 lib = _Lib()
@@ -332,11 +334,24 @@ def prefill(cfg: Config, q_nope, q_rope, pos, rows, w_uk, w_uv, cu_seqlens, max_
 # ---- speculative decoding with a drafted tree ------------------------------------------------
 # These calls check what a raw pointer cannot carry (device, dtype, shape, contiguity) and raise
 # MlaError before anything is launched; they launch on the tensors' device whichever device is
-# current.
+# current. The checks are written out in each call, and only a failed one asks _refuse which it
+# was: a call of a few microseconds on the GPU should not take longer on the host.
 
-def _expect(where: str, device: int, *tensors):
-    """Every (name, tensor, dtype, shape) is a contiguous tensor of that kind on GPU `device`."""
+torch = None  # imported by the first of these calls
+
+
+def _import_torch():
+    global torch
+    import torch as module
+    torch = module
+
+
+def _refuse(where: str, device: int, *tensors):
+    """Raise for the first (name, tensor, dtype, shape) that is not a contiguous tensor of that
+    kind on GPU `device`."""
     for name, t, dtype, shape in tensors:
+        if not t.is_cuda:
+            raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is on {t.device}, not on a GPU")
         if (t.dtype is dtype and t.shape == shape and t.get_device() == device and
                 t.is_contiguous()):
             continue
@@ -346,36 +361,27 @@ def _expect(where: str, device: int, *tensors):
                        f"{tuple(shape)} on cuda:{device}")
 
 
-def _shape(where: str, name: str, t, dims: int):
+def _sizes(where: str, name: str, t, dims: int):
     """The shape of a tensor whose sizes the call takes from it."""
-    if t.dim() != dims:
+    shape = t.shape
+    if len(shape) != dims:
         raise MlaError(MLA_ERR_INVALID_ARG,
-                       f"{where}: {name} has shape {tuple(t.shape)}, wanted {dims} dimensions")
-    return t.shape
+                       f"{where}: {name} has shape {tuple(shape)}, wanted {dims} dimensions")
+    return shape
 
 
-def _device_of(where: str, name: str, t) -> int:
-    if not t.is_cuda:
-        raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is on {t.device}, not on a GPU")
-    return t.get_device()
-
-
-def _launch(where: str, fn, device: int, stream, *args):
-    """Call fn(*args, stream) with `device` current; None is that device's current stream."""
-    import torch
-    # the raw handle: torch.cuda.current_stream() makes a Stream object, which takes longer
-    # than the rest of a small call
+def _on(device: int, stream) -> int:
+    """The raw handle of `stream`; None is the device's current one. (torch.cuda.current_stream()
+    makes a Stream object, which takes longer than the rest of a small call.)"""
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if device == torch.cuda.current_device():
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream)
-    if st != MLA_OK:
-        raise MlaError(st, where)
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _elsewhere(where: str, device: int, fn, *args):
+    """fn(*args) with `device` current, which it was not."""
+    with torch.cuda.device(device):
+        _check(fn(*args), where)
 
 
 def build_tables(cfg: Config, seq_lens, new_lens, block_table, blocks_held, free_blocks,
@@ -386,61 +392,120 @@ def build_tables(cfg: Config, seq_lens, new_lens, block_table, blocks_held, free
     The pool has free_blocks.shape[0] blocks; blocks_held_out and free_count_out may be
     blocks_held and free_count.
     """
-    import torch
+    if torch is None:
+        _import_torch()
     w, i32 = "mla_build_tables", torch.int32
-    dev = _device_of(w, "seq_lens", seq_lens)
-    n, = _shape(w, "seq_lens", seq_lens, 1)
-    tokens, = _shape(w, "slots", slots, 1)
-    blocks, = _shape(w, "free_blocks", free_blocks, 1)
-    width = _shape(w, "block_table", block_table, 2)[1]
-    _expect(w, dev, ("seq_lens", seq_lens, i32, (n,)), ("new_lens", new_lens, i32, (n,)),
-            ("block_table", block_table, i32, (n, width)),
-            ("blocks_held", blocks_held, i32, (n,)),
-            ("free_blocks", free_blocks, i32, (blocks,)), ("free_count", free_count, i32, (1,)),
-            ("blocks_held_out", blocks_held_out, i32, (n,)),
-            ("free_count_out", free_count_out, i32, (1,)), ("cu_new", cu_new, i32, (n + 1,)),
-            ("seq_idx", seq_idx, i32, (tokens,)), ("pos", pos, i32, (tokens,)),
-            ("slots", slots, torch.int64, (tokens,)), ("dev_err", dev_err, i32, (1,)))
-    _launch(w, lib.mla_build_tables, dev, stream, cfg.ref(), seq_lens.data_ptr(),
-            new_lens.data_ptr(), n, block_table.data_ptr(), width,
-            blocks_held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
-            blocks, blocks_held_out.data_ptr(), free_count_out.data_ptr(),
-            cu_new.data_ptr(), seq_idx.data_ptr(), pos.data_ptr(), slots.data_ptr(), tokens,
-            dev_err.data_ptr())
+    dev = seq_lens.get_device()
+    per, rows = _sizes(w, "seq_lens", seq_lens, 1), _sizes(w, "slots", slots, 1)
+    blocks, width = _sizes(w, "free_blocks", free_blocks, 1)[0], _sizes(
+        w, "block_table", block_table, 2)[1]
+    n, tokens = per[0], rows[0]
+    if not (seq_lens.is_cuda and seq_lens.dtype is i32 and seq_lens.is_contiguous() and
+            new_lens.dtype is i32 and new_lens.shape == per and new_lens.get_device() == dev and
+            new_lens.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape[0] == n and
+            block_table.get_device() == dev and block_table.is_contiguous() and
+            blocks_held.dtype is i32 and blocks_held.shape == per and
+            blocks_held.get_device() == dev and blocks_held.is_contiguous() and
+            free_blocks.dtype is i32 and free_blocks.get_device() == dev and
+            free_blocks.is_contiguous() and
+            free_count.dtype is i32 and free_count.shape == (1,) and
+            free_count.get_device() == dev and
+            blocks_held_out.dtype is i32 and blocks_held_out.shape == per and
+            blocks_held_out.get_device() == dev and blocks_held_out.is_contiguous() and
+            free_count_out.dtype is i32 and free_count_out.shape == (1,) and
+            free_count_out.get_device() == dev and
+            cu_new.dtype is i32 and cu_new.shape == (n + 1,) and cu_new.get_device() == dev and
+            cu_new.is_contiguous() and
+            seq_idx.dtype is i32 and seq_idx.shape == rows and seq_idx.get_device() == dev and
+            seq_idx.is_contiguous() and
+            pos.dtype is i32 and pos.shape == rows and pos.get_device() == dev and
+            pos.is_contiguous() and
+            slots.dtype is torch.int64 and slots.get_device() == dev and slots.is_contiguous() and
+            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev):
+        _refuse(w, dev, ("seq_lens", seq_lens, i32, (n,)), ("new_lens", new_lens, i32, (n,)),
+                ("block_table", block_table, i32, (n, width)),
+                ("blocks_held", blocks_held, i32, (n,)),
+                ("free_blocks", free_blocks, i32, (blocks,)),
+                ("free_count", free_count, i32, (1,)),
+                ("blocks_held_out", blocks_held_out, i32, (n,)),
+                ("free_count_out", free_count_out, i32, (1,)), ("cu_new", cu_new, i32, (n + 1,)),
+                ("seq_idx", seq_idx, i32, (tokens,)), ("pos", pos, i32, (tokens,)),
+                ("slots", slots, torch.int64, (tokens,)), ("dev_err", dev_err, i32, (1,)))
+    args = (cfg.ref(), seq_lens.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(), width,
+            blocks_held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(), blocks,
+            blocks_held_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(),
+            seq_idx.data_ptr(), pos.data_ptr(), slots.data_ptr(), tokens, dev_err.data_ptr(),
+            _on(dev, stream))
+    if dev != torch._C._cuda_getDevice():
+        return _elsewhere(w, dev, lib.mla_build_tables, *args)
+    st = lib.mla_build_tables(*args)
+    if st:
+        raise MlaError(st, w)
 
 
 def tree_masks(parents, seq_lens, mask, pos, dev_err, stream=None):
     """mla_tree_masks: ancestor masks (int32 words) and RoPE positions of drafted trees given by
     their parent indices, (batch, T), or (1, T) for one tree that all sequences share."""
-    import torch
+    if torch is None:
+        _import_torch()
     w, i32 = "mla_tree_masks", torch.int32
-    dev = _device_of(w, "parents", parents)
-    n, = _shape(w, "seq_lens", seq_lens, 1)
-    rows, T = _shape(w, "parents", parents, 2)
-    _expect(w, dev, ("parents", parents, i32, (rows, T)), ("seq_lens", seq_lens, i32, (n,)),
-            ("mask", mask, i32, (n * T, (T + 31) // 32)), ("pos", pos, i32, (n * T,)),
-            ("dev_err", dev_err, i32, (1,)))
-    _launch(w, lib.mla_tree_masks, dev, stream, parents.data_ptr(), rows,
-            seq_lens.data_ptr(), n, T, mask.data_ptr(), pos.data_ptr(), dev_err.data_ptr())
+    dev = parents.get_device()
+    n = _sizes(w, "seq_lens", seq_lens, 1)[0]
+    rows, T = _sizes(w, "parents", parents, 2)
+    if not (parents.is_cuda and parents.dtype is i32 and parents.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous() and
+            mask.dtype is i32 and mask.shape == (n * T, (T + 31) // 32) and
+            mask.get_device() == dev and mask.is_contiguous() and
+            pos.dtype is i32 and pos.shape == (n * T,) and pos.get_device() == dev and
+            pos.is_contiguous() and
+            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev):
+        _refuse(w, dev, ("parents", parents, i32, (rows, T)), ("seq_lens", seq_lens, i32, (n,)),
+                ("mask", mask, i32, (n * T, (T + 31) // 32)), ("pos", pos, i32, (n * T,)),
+                ("dev_err", dev_err, i32, (1,)))
+    args = (parents.data_ptr(), rows, seq_lens.data_ptr(), n, T, mask.data_ptr(), pos.data_ptr(),
+            dev_err.data_ptr(), _on(dev, stream))
+    if dev != torch._C._cuda_getDevice():
+        return _elsewhere(w, dev, lib.mla_tree_masks, *args)
+    st = lib.mla_tree_masks(*args)
+    if st:
+        raise MlaError(st, w)
 
 
 def append_slots(cfg: Config, ckv_raw, krope_raw, gamma, pos, slots, pool, dev_err, stream=None):
     """mla_append_slots: mla_append_latent's rows written to the pool rows `slots` (a negative
     slot is skipped), RoPE positions given apart. krope_raw may be None when rope_dim is 0."""
-    import torch
-    w, dt = "mla_append_slots", cfg.torch_dtype
-    dev = _device_of(w, "pool", pool)
-    n, = _shape(w, "slots", slots, 1)
-    blocks, r, dr = _shape(w, "pool", pool, 3)[0], cfg.kv_rank, cfg.rope_dim
-    _expect(w, dev, ("ckv_raw", ckv_raw, dt, (n, r)), ("gamma", gamma, torch.float32, (r,)),
-            ("pos", pos, torch.int32, (n,)), ("slots", slots, torch.int64, (n,)),
-            ("pool", pool, dt, (blocks, cfg.block_size, r + dr)),
-            ("dev_err", dev_err, torch.int32, (1,)))
-    if dr:
-        _expect(w, dev, ("krope_raw", krope_raw, dt, (n, dr)))
-    _launch(w, lib.mla_append_slots, dev, stream, cfg.ref(), ckv_raw.data_ptr(), _ptr(krope_raw),
-            gamma.data_ptr(), pos.data_ptr(), slots.data_ptr(), pool.data_ptr(), blocks, n,
-            dev_err.data_ptr())
+    if torch is None:
+        _import_torch()
+    w, dt, i32 = "mla_append_slots", cfg.torch_dtype, torch.int32
+    dev = pool.get_device()
+    per = _sizes(w, "slots", slots, 1)
+    n, blocks, r, dr = per[0], _sizes(w, "pool", pool, 3)[0], cfg.kv_rank, cfg.rope_dim
+    if not (pool.is_cuda and pool.dtype is dt and pool.is_contiguous() and
+            pool.shape == (blocks, cfg.block_size, r + dr) and
+            ckv_raw.dtype is dt and ckv_raw.shape == (n, r) and ckv_raw.get_device() == dev and
+            ckv_raw.is_contiguous() and
+            gamma.dtype is torch.float32 and gamma.shape == (r,) and gamma.get_device() == dev and
+            gamma.is_contiguous() and
+            pos.dtype is i32 and pos.shape == per and pos.get_device() == dev and
+            pos.is_contiguous() and
+            slots.dtype is torch.int64 and slots.get_device() == dev and slots.is_contiguous() and
+            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev and
+            (dr == 0 or (krope_raw.dtype is dt and krope_raw.shape == (n, dr) and
+                         krope_raw.get_device() == dev and krope_raw.is_contiguous()))):
+        _refuse(w, dev, ("pool", pool, dt, (blocks, cfg.block_size, r + dr)),
+                ("ckv_raw", ckv_raw, dt, (n, r)), ("gamma", gamma, torch.float32, (r,)),
+                ("pos", pos, i32, (n,)), ("slots", slots, torch.int64, (n,)),
+                ("dev_err", dev_err, i32, (1,)),
+                *([("krope_raw", krope_raw, dt, (n, dr))] if dr else []))
+    args = (cfg.ref(), ckv_raw.data_ptr(), krope_raw.data_ptr() if dr else None, gamma.data_ptr(),
+            pos.data_ptr(), slots.data_ptr(), pool.data_ptr(), blocks, n, dev_err.data_ptr(),
+            _on(dev, stream))
+    if dev != torch._C._cuda_getDevice():
+        return _elsewhere(w, dev, lib.mla_append_slots, *args)
+    st = lib.mla_append_slots(*args)
+    if st:
+        raise MlaError(st, w)
 
 
 def decode_tree_workspace_size(cfg: Config, batch: int, q_per_seq: int) -> int:
@@ -451,47 +516,89 @@ def decode_tree(cfg: Config, q, pool, block_table, seq_lens, q_per_seq: int, tre
                 workspace, o, lse, dev_err, stream=None):
     """mla_decode_tree: attention of every drafted token over its sequence's cache and the drafted
     rows its mask names (None: a chain), then W_UV. lse may be None."""
-    import torch
+    if torch is None:
+        _import_torch()
     w, dt, i32 = "mla_decode_tree", cfg.torch_dtype, torch.int32
-    dev = _device_of(w, "pool", pool)
-    n, = _shape(w, "seq_lens", seq_lens, 1)
-    blocks, width = _shape(w, "pool", pool, 3)[0], _shape(w, "block_table", block_table, 2)[1]
-    size, = _shape(w, "workspace", workspace, 1)
-    nt, H, r = n * q_per_seq, cfg.num_heads, cfg.kv_rank
+    dev = pool.get_device()
+    n = _sizes(w, "seq_lens", seq_lens, 1)[0]
+    blocks, width = _sizes(w, "pool", pool, 3)[0], _sizes(w, "block_table", block_table, 2)[1]
+    size = _sizes(w, "workspace", workspace, 1)[0]
+    nt, H, r, bs = n * q_per_seq, cfg.num_heads, cfg.kv_rank, cfg.block_size
     D, dv = r + cfg.rope_dim, cfg.head_dim_v or cfg.head_dim
-    _expect(w, dev, ("q", q, dt, (nt, H, D)), ("pool", pool, dt, (blocks, cfg.block_size, D)),
-            ("block_table", block_table, i32, (n, width)), ("seq_lens", seq_lens, i32, (n,)),
-            ("w_uv", w_uv, dt, (H, dv, r)), ("workspace", workspace, torch.uint8, (size,)),
-            ("o", o, dt, (nt, H, dv)), ("dev_err", dev_err, i32, (1,)))
-    if tree_mask is not None:
-        _expect(w, dev, ("tree_mask", tree_mask, i32, (nt, (q_per_seq + 31) // 32)))
-    if lse is not None:
-        _expect(w, dev, ("lse", lse, torch.float32, (nt, H)))
-    _launch(w, lib.mla_decode_tree, dev, stream, cfg.ref(), q.data_ptr(), pool.data_ptr(),
-            block_table.data_ptr(), width, blocks, seq_lens.data_ptr(), n,
-            q_per_seq, _ptr(tree_mask), w_uv.data_ptr(), workspace.data_ptr(), size,
-            o.data_ptr(), _ptr(lse), dev_err.data_ptr())
+    if not (pool.is_cuda and pool.dtype is dt and pool.shape == (blocks, bs, D) and
+            pool.is_contiguous() and
+            q.dtype is dt and q.shape == (nt, H, D) and q.get_device() == dev and
+            q.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape[0] == n and
+            block_table.get_device() == dev and block_table.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous() and
+            w_uv.dtype is dt and w_uv.shape == (H, dv, r) and w_uv.get_device() == dev and
+            w_uv.is_contiguous() and
+            workspace.dtype is torch.uint8 and workspace.get_device() == dev and
+            workspace.is_contiguous() and
+            o.dtype is dt and o.shape == (nt, H, dv) and o.get_device() == dev and
+            o.is_contiguous() and
+            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev and
+            (tree_mask is None or
+             (tree_mask.dtype is i32 and tree_mask.shape == (nt, (q_per_seq + 31) // 32) and
+              tree_mask.get_device() == dev and tree_mask.is_contiguous())) and
+            (lse is None or
+             (lse.dtype is torch.float32 and lse.shape == (nt, H) and lse.get_device() == dev and
+              lse.is_contiguous()))):
+        _refuse(w, dev, ("pool", pool, dt, (blocks, bs, D)), ("q", q, dt, (nt, H, D)),
+                ("block_table", block_table, i32, (n, width)), ("seq_lens", seq_lens, i32, (n,)),
+                ("w_uv", w_uv, dt, (H, dv, r)), ("workspace", workspace, torch.uint8, (size,)),
+                ("o", o, dt, (nt, H, dv)), ("dev_err", dev_err, i32, (1,)),
+                *([] if tree_mask is None else
+                  [("tree_mask", tree_mask, i32, (nt, (q_per_seq + 31) // 32))]),
+                *([] if lse is None else [("lse", lse, torch.float32, (nt, H))]))
+    args = (cfg.ref(), q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), width, blocks,
+            seq_lens.data_ptr(), n, q_per_seq, None if tree_mask is None else tree_mask.data_ptr(),
+            w_uv.data_ptr(), workspace.data_ptr(), size, o.data_ptr(),
+            None if lse is None else lse.data_ptr(), dev_err.data_ptr(), _on(dev, stream))
+    if dev != torch._C._cuda_getDevice():
+        return _elsewhere(w, dev, lib.mla_decode_tree, *args)
+    st = lib.mla_decode_tree(*args)
+    if st:
+        raise MlaError(st, w)
 
 
 def commit_tree(cfg: Config, path, path_len, q_per_seq: int, block_table, pool, seq_lens,
                 seq_lens_out, dev_err, stream=None):
     """mla_commit_tree: the accepted path's rows moved together, seq_lens_out the lengths with it
     (may be seq_lens). path: (batch, width) node numbers, path_len of them count."""
-    import torch
-    w, i32 = "mla_commit_tree", torch.int32
-    dev = _device_of(w, "pool", pool)
-    n, = _shape(w, "seq_lens", seq_lens, 1)
-    blocks, width = _shape(w, "pool", pool, 3)[0], _shape(w, "block_table", block_table, 2)[1]
-    steps = _shape(w, "path", path, 2)[1]
-    _expect(w, dev, ("path", path, i32, (n, steps)), ("path_len", path_len, i32, (n,)),
-            ("block_table", block_table, i32, (n, width)),
-            ("pool", pool, cfg.torch_dtype, (blocks, cfg.block_size, cfg.kv_rank + cfg.rope_dim)),
-            ("seq_lens", seq_lens, i32, (n,)), ("seq_lens_out", seq_lens_out, i32, (n,)),
-            ("dev_err", dev_err, i32, (1,)))
-    _launch(w, lib.mla_commit_tree, dev, stream, cfg.ref(), path.data_ptr(), path_len.data_ptr(),
-            steps, q_per_seq, block_table.data_ptr(), width,
-            pool.data_ptr(), blocks, seq_lens.data_ptr(), seq_lens_out.data_ptr(), n,
-            dev_err.data_ptr())
+    if torch is None:
+        _import_torch()
+    w, dt, i32 = "mla_commit_tree", cfg.torch_dtype, torch.int32
+    dev = pool.get_device()
+    per = _sizes(w, "seq_lens", seq_lens, 1)
+    n, blocks, width = per[0], _sizes(w, "pool", pool, 3)[0], _sizes(
+        w, "block_table", block_table, 2)[1]
+    steps, D = _sizes(w, "path", path, 2)[1], cfg.kv_rank + cfg.rope_dim
+    if not (pool.is_cuda and pool.dtype is dt and pool.shape == (blocks, cfg.block_size, D) and
+            pool.is_contiguous() and
+            path.dtype is i32 and path.shape[0] == n and path.get_device() == dev and
+            path.is_contiguous() and
+            path_len.dtype is i32 and path_len.shape == per and path_len.get_device() == dev and
+            path_len.is_contiguous() and
+            block_table.dtype is i32 and block_table.shape[0] == n and
+            block_table.get_device() == dev and block_table.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous() and
+            seq_lens_out.dtype is i32 and seq_lens_out.shape == per and
+            seq_lens_out.get_device() == dev and seq_lens_out.is_contiguous() and
+            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev):
+        _refuse(w, dev, ("pool", pool, dt, (blocks, cfg.block_size, D)),
+                ("path", path, i32, (n, steps)), ("path_len", path_len, i32, (n,)),
+                ("block_table", block_table, i32, (n, width)), ("seq_lens", seq_lens, i32, (n,)),
+                ("seq_lens_out", seq_lens_out, i32, (n,)), ("dev_err", dev_err, i32, (1,)))
+    args = (cfg.ref(), path.data_ptr(), path_len.data_ptr(), steps, q_per_seq,
+            block_table.data_ptr(), width, pool.data_ptr(), blocks, seq_lens.data_ptr(),
+            seq_lens_out.data_ptr(), n, dev_err.data_ptr(), _on(dev, stream))
+    if dev != torch._C._cuda_getDevice():
+        return _elsewhere(w, dev, lib.mla_commit_tree, *args)
+    st = lib.mla_commit_tree(*args)
+    if st:
+        raise MlaError(st, w)
 
 
 def abi_version() -> int:
