@@ -521,8 +521,8 @@ mla_status mla_decode_step(const mla_config* cfg, const void* q_nope, const void
 // ------------------------------------------------------------------------------------------
 namespace {
 
-// Workspace of mla_decode_tree: the latent sums (two bf16 terms on the tensor-core path, fp32
-// otherwise), the partial results of split key ranges, and (tensor-core path) where they lie.
+// Workspace of mla_decode_tree: the results of the key ranges, and on the tensor-core path where
+// those of cut items lie and the finished latent sums in two bf16 terms.
 struct TreeLayout {
   bool tc;
   size_t latent, latent_lo, part_lse, part_o, cuts, total;
@@ -537,8 +537,8 @@ TreeLayout tree_layout(const mla_config& c, int batch, int T) {
   L.tiles = (T * c.num_heads + L.tile_rows - 1) / L.tile_rows;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
-  L.latent = take(n * c.kv_rank * (L.tc ? 2 : 4));
   if (L.tc) {
+    L.latent = take(n * c.kv_rank * 2);
     L.latent_lo = take(n * c.kv_rank * 2);
     tree_team(L.tiles, &L.team, &L.ranges);
     L.groups = (L.tiles + L.team - 1) / L.team;
@@ -549,8 +549,8 @@ TreeLayout tree_layout(const mla_config& c, int batch, int T) {
     // enough CTAs for four on each of 148 SMs
     const int64_t ctas = (int64_t)batch * L.tiles;
     L.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTreeMaxSplits, 4 * 148 / ctas));
-    L.part_lse = take(L.splits > 1 ? L.splits * n * sizeof(float) : 0);
-    L.part_o = take(L.splits > 1 ? L.splits * n * c.kv_rank * sizeof(float) : 0);
+    L.part_lse = take(L.splits * n * sizeof(float));
+    L.part_o = take(L.splits * n * c.kv_rank * sizeof(float));
   }
   L.total = off;
   return L;
@@ -667,7 +667,6 @@ mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* poo
   p.scale = c.softmax_scale;
   p.tile_rows = L.tile_rows;
   p.tiles = L.tiles;
-  cudaError_t e;
   if (L.tc) {
     p.team = L.team;
     p.groups = L.groups;
@@ -675,19 +674,16 @@ mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* poo
     p.latent_hi = (__nv_bfloat16*)(ws + L.latent);
     p.latent_lo = (__nv_bfloat16*)(ws + L.latent_lo);
     p.cuts = (int4*)(ws + L.cuts);
-    e = launch_tree_tc(p, (cudaStream_t)stream);
+    cudaError_t e = launch_tree_tc(p, (cudaStream_t)stream);
     if (e == cudaSuccess) e = launch_tree_merge(p, (cudaStream_t)stream);
     if (e == cudaSuccess)
       e = launch_tree_out(p, w_uv, c.head_dim_v, o, (cudaStream_t)stream);
     return from_cuda(e);
   }
-  p.latent = (float*)(ws + L.latent);
   // no more ranges than 64-row pieces of the longest sequence the table can hold
   p.splits = (int)std::min<int64_t>(
       L.splits, std::max<int64_t>(1, ((int64_t)max_blocks * c.block_size + 63) / 64));
-  e = launch_tree_simt(c, p, (cudaStream_t)stream);
-  if (e != cudaSuccess) return from_cuda(e);
-  return mla_output(cfg, p.latent, w_uv, o, p.BT, dev_err, stream);
+  return from_cuda(launch_tree_simt(c, p, w_uv, o, (cudaStream_t)stream));
 }
 
 mla_status mla_commit_tree(const mla_config* cfg, const int32_t* path, const int32_t* path_len,

@@ -15,7 +15,6 @@ struct TreeParams {
   const int32_t* table;
   const int32_t* seq_lens;
   const uint32_t* mask;  // null: a chain
-  float* latent;         // (BT, H, r), workspace
   float* lse;            // may be null
   uint32_t* err;
   float* part_o;    // partial results of split key ranges
@@ -50,7 +49,8 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int
   return (p.mask[((size_t)b * p.T + t) * p.words + (node >> 5)] >> (node & 31)) & 1u;
 }
 
-cudaError_t launch_tree_simt(const mla_config& c, const TreeParams& p, cudaStream_t st);
+cudaError_t launch_tree_simt(const mla_config& c, const TreeParams& p, const void* w_uv, void* o,
+                             cudaStream_t st);
 int tree_simt_tile_rows(const mla_config& c);
 bool tree_tc_supported(const mla_config& c);
 void tree_team(int tiles, int* team, int* ranges);

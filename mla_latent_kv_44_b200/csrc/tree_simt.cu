@@ -3,17 +3,18 @@
 //
 // A sequence's T drafted tokens and H heads are T * H query rows over the same cache rows, so
 // they are tiled together: one CTA takes 8 * RPW of them (8 warps, RPW rows per warp) against a
-// range of cache rows, staged 32 at a time in shared memory as fp32. Scores: lane j of a warp
-// takes cache row j for the warp's RPW query rows (one conflict-free 16-byte read of the row,
+// range of cache rows, staged 32 * KPL at a time in shared memory as fp32. Scores: lane j of a
+// warp takes cache rows j (and j + 32) for the warp's RPW query rows (one conflict-free 16-byte read of the row,
 // its pitch D + 4 words, per RPW broadcast reads of the queries). Softmax: running maximum and
 // sum in fp32. Values: lane owns r / 32 columns; the weights go through shared memory four cache
 // rows at a time. Rows of the cache that precede the drafted ones are seen by every token; for
 // the drafted ones the token's mask word decides, and a masked score is replaced, never added to,
 // so that nothing of a masked row (NaN included) reaches the result.
-// The keys of a sequence are cut into `splits` equal ranges when there are too few query tiles
-// to fill the GPU; the merge weighs the ranges by their log-sum-exp, in range order.
-#include <cuda_fp8.h>
-
+// The keys of a sequence are cut into `splits` equal ranges when there are too few query tiles to
+// fill the GPU. The second kernel weighs the ranges by their log-sum-exp, in range order, and
+// applies W_UV to the merged rows where it has them, in shared memory.
+// What bounds it: latency at the sizes that it is for (fp32 models, small heads): a CTA's chain of
+// block id, cache rows, scores, softmax, values. So 64 cache rows go in one tile where they fit.
 #include <algorithm>
 
 #include "tree.cuh"
@@ -22,7 +23,6 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kKeys = 32;  // cache rows per staged tile (one per lane)
 
 template <typename T> __device__ __forceinline__ float4 load4(const T* p);
 template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
@@ -34,15 +34,14 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
                      __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
 
-template <typename T, int RPW, int RW>  // RW: latent columns per lane (r <= 32 * RW)
+template <typename T, int RPW, int KPL, int RW>  // RW: latent columns per lane (r <= 32 * RW)
 __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams p) {
-  constexpr int M = kWarps * RPW;
+  constexpr int M = kWarps * RPW, kKeys = 32 * KPL;
   extern __shared__ __align__(16) float smem[];
   const int D = p.D, ld = D + 4, r = p.r, quads = D / 4;
   float* s_q = smem;                  // M x D
   float* s_k = s_q + M * D;           // kKeys x ld
   float* s_p = s_k + kKeys * ld;      // M x kKeys
-  int* s_blk = (int*)(s_p + M * kKeys);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % p.splits, tile = blockIdx.x / p.splits;
   const int b = tile / p.tiles, m0 = (tile - b * p.tiles) * M;
@@ -74,61 +73,80 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
   const float* qw = s_q + warp * RPW * D;
   float* pw = s_p + warp * RPW * kKeys;
 
-  for (int t0 = lo; t0 < hi; t0 += kKeys) {
-    __syncthreads();  // previous tile consumed (s_q written, the first time)
-    if (threadIdx.x < kKeys) {
-      const int row = t0 + threadIdx.x;
-      int blk = -1;
-      if (row < hi) {
-        blk = p.table[(size_t)b * p.max_blocks + row / p.bs];
-        if (blk < 0 || blk >= p.num_blocks) {
-          set_error(p.err, MLA_DEV_OOB_BLOCK);
-          blk = -1;
-        }
-      }
-      s_blk[threadIdx.x] = blk;
+  // the pool row of a cache row, or -1 (past the range, or a block outside the pool)
+  auto place = [&](int row, bool report) -> int64_t {
+    if (row >= hi) return -1;
+    const int at = row / p.bs, blk = p.table[(size_t)b * p.max_blocks + at];
+    if (blk < 0 || blk >= p.num_blocks) {
+      if (report) set_error(p.err, MLA_DEV_OOB_BLOCK);
+      return -1;
     }
-    __syncthreads();
+    return (int64_t)blk * p.bs + (row - at * p.bs);
+  };
+
+  for (int t0 = lo; t0 < hi; t0 += kKeys) {
+    __syncthreads();  // previous tile consumed
     for (int i = threadIdx.x; i < kKeys * quads; i += blockDim.x) {
-      const int t = i / quads, qd = i - t * quads, blk = s_blk[t];
+      const int t = i / quads, qd = i - t * quads;
+      const int64_t at = place(t0 + t, true);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (blk >= 0)
-        v = load4((const T*)p.pool + ((size_t)blk * p.bs + (t0 + t) % p.bs) * D + 4 * qd);
+      if (at >= 0) v = load4((const T*)p.pool + at * D + 4 * qd);
       *(float4*)(s_k + t * ld + 4 * qd) = v;
     }
+    bool there[KPL];
+#pragma unroll
+    for (int c = 0; c < KPL; ++c) there[c] = place(t0 + lane + 32 * c, false) >= 0;
     __syncthreads();
 
-    // scores of cache row t0 + lane
-    float s[RPW];
+    // scores of cache rows t0 + lane + 32 c
+    float s[RPW][KPL];
 #pragma unroll
-    for (int a = 0; a < RPW; ++a) s[a] = 0.f;
+    for (int a = 0; a < RPW; ++a)
+#pragma unroll
+      for (int c = 0; c < KPL; ++c) s[a][c] = 0.f;
     const float* krow = s_k + lane * ld;
     for (int d = 0; d < D; d += 4) {
-      const float4 k = *(const float4*)(krow + d);
+      float4 k[KPL];
+#pragma unroll
+      for (int c = 0; c < KPL; ++c) k[c] = *(const float4*)(krow + 32 * c * ld + d);
 #pragma unroll
       for (int a = 0; a < RPW; ++a) {
         const float4 q = *(const float4*)(qw + a * D + d);
-        s[a] = fmaf(q.x, k.x, s[a]);
-        s[a] = fmaf(q.y, k.y, s[a]);
-        s[a] = fmaf(q.z, k.z, s[a]);
-        s[a] = fmaf(q.w, k.w, s[a]);
+#pragma unroll
+        for (int c = 0; c < KPL; ++c) {
+          s[a][c] = fmaf(q.x, k[c].x, s[a][c]);
+          s[a][c] = fmaf(q.y, k[c].y, s[a][c]);
+          s[a][c] = fmaf(q.z, k[c].z, s[a][c]);
+          s[a][c] = fmaf(q.w, k[c].w, s[a][c]);
+        }
       }
     }
     const bool drafted = t0 + kKeys > first;  // the tile holds drafted rows
-    const int node = t0 + lane - first;
 #pragma unroll
     for (int a = 0; a < RPW; ++a) {
-      bool seen = s_blk[lane] >= 0;
-      if (node >= 0 && seen) seen = tree_sees(p, b, tok[a], node);
-      s[a] = seen ? s[a] * p.scale : -INFINITY;
-      const float m = fmaxf(mx[a], warp_max(s[a]));
+      float top = -INFINITY;
+      bool seen[KPL];
+#pragma unroll
+      for (int c = 0; c < KPL; ++c) {
+        const int node = t0 + lane + 32 * c - first;
+        seen[c] = there[c];
+        if (drafted && node >= 0 && seen[c]) seen[c] = tree_sees(p, b, tok[a], node);
+        s[a][c] = seen[c] ? s[a][c] * p.scale : -INFINITY;
+        top = fmaxf(top, s[a][c]);
+      }
+      const float m = fmaxf(mx[a], warp_max(top));
       const float alpha = mx[a] == -INFINITY ? 0.f : expf(mx[a] - m);
-      const float e = seen && s[a] != -INFINITY ? expf(s[a] - m) : 0.f;
-      l[a] = l[a] * alpha + warp_sum(e);
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < KPL; ++c) {
+        const float e = seen[c] && s[a][c] != -INFINITY ? expf(s[a][c] - m) : 0.f;
+        sum += e;
+        pw[a * kKeys + lane + 32 * c] = e;
+      }
+      l[a] = l[a] * alpha + warp_sum(sum);
       mx[a] = m;
 #pragma unroll
       for (int k = 0; k < RW; ++k) o[a][k] *= alpha;
-      pw[a * kKeys + lane] = e;
     }
     __syncwarp();
     if (drafted) {  // a masked row's values are left out, whatever they are
@@ -166,83 +184,105 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
         }
       }
     }
+    __syncwarp();  // the warp's weights are read
   }
 
 #pragma unroll
   for (int a = 0; a < RPW; ++a) {
     const int m = warp * RPW + a;
     if (m0 + m >= rows) continue;
-    const size_t at = (size_t)b * rows + m0 + m;  // (token, head) of the call
+    // row (token, head) of the call, in this range's part
+    const size_t at = (size_t)split * p.BT * p.H + (size_t)b * rows + m0 + m;
     const bool empty = l[a] == 0.f;
     const float inv = empty ? 0.f : 1.f / l[a];
-    const float lse = empty ? -INFINITY : mx[a] + logf(l[a]);
-    float* dst;
-    if (p.splits == 1) {
-      dst = p.latent + at * r;
-      if (lane == 0 && p.lse) p.lse[at] = lse;
-    } else {
-      const size_t part = (size_t)split * p.BT * p.H + at;
-      dst = p.part_o + part * r;
-      if (lane == 0) p.part_lse[part] = lse;
-    }
+    if (lane == 0) p.part_lse[at] = empty ? -INFINITY : mx[a] + logf(l[a]);
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       const int d = lane + 32 * k;
-      if (d < r) dst[d] = empty ? 0.f : o[a][k] * inv;
+      if (d < r) p.part_o[at * r + d] = empty ? 0.f : o[a][k] * inv;
     }
   }
 }
 
-// ---- merge of `splits` ranges: one warp per (token, head) --------------------------------
-__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
-  __shared__ float s_w[4][kTreeMaxSplits];
+// ---- merge of the ranges and W_UV: one CTA per head and NT tokens -------------------------
+template <typename T, int NT>
+__global__ void __launch_bounds__(128)
+tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restrict__ o, int dv) {
+  extern __shared__ __align__(16) float s_lat[];  // NT x r
+  __shared__ float s_w[NT][kTreeMaxSplits];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = p.r;
+  const int h = blockIdx.x % p.H, n0 = blockIdx.x / p.H * NT;
+  const size_t part = (size_t)p.BT * p.H;
   wait_prior_grid();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t n = (size_t)p.BT * p.H, at = (size_t)blockIdx.x * 4 + warp;
-  if (at >= n) return;
-  float* w = s_w[warp];
-  float mx = -INFINITY;
-  bool nan = false;
-  for (int k = lane; k < p.splits; k += 32) {
-    const float x = p.part_lse[k * n + at];
-    nan |= x != x;
-    mx = fmaxf(mx, x);
-  }
-  mx = warp_max(mx);
-  float z = 0.f;
-  for (int k = lane; k < p.splits; k += 32) {
-    const float x = p.part_lse[k * n + at];
-    const float e = x == -INFINITY ? 0.f : expf(x - mx);
-    w[k] = e;
-    z += e;
-  }
-  z = warp_sum(z);
-  nan = __any_sync(0xffffffffu, nan);
-  const bool empty = mx == -INFINITY && !nan;
-  const float inv = empty ? 0.f : 1.f / z;
-  __syncwarp();
-  for (int d = 4 * lane; d < p.r; d += 128) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < p.splits; ++k) {
-      const float e = w[k] * inv;
-      if (e == 0.f) continue;  // a range without rows
-      const float4 v = __ldcs((const float4*)(p.part_o + (k * n + at) * p.r + d));
-      acc.x = fmaf(e, v.x, acc.x);
-      acc.y = fmaf(e, v.y, acc.y);
-      acc.z = fmaf(e, v.z, acc.z);
-      acc.w = fmaf(e, v.w, acc.w);
+  for (int t = warp; t < NT; t += 4) {  // a warp per token: weights, then the merged row
+    const int n = n0 + t;
+    if (n >= p.BT) break;
+    const size_t at = (size_t)n * p.H + h;
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int k = lane; k < p.splits; k += 32) {
+      const float x = p.part_lse[k * part + at];
+      nan |= x != x;
+      mx = fmaxf(mx, x);
     }
-    *(float4*)(p.latent + at * p.r + d) = acc;
+    mx = warp_max(mx);
+    nan = __any_sync(0xffffffffu, nan);
+    float z = 0.f;
+    for (int k = lane; k < p.splits; k += 32) {
+      const float x = p.part_lse[k * part + at];
+      const float e = x == -INFINITY ? 0.f : expf(x - mx);
+      s_w[t][k] = e;
+      z += e;
+    }
+    z = warp_sum(z);
+    const bool empty = mx == -INFINITY && !nan;
+    const float inv = empty ? 0.f : 1.f / z;
+    __syncwarp();
+    for (int d = 4 * lane; d < r; d += 128) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < p.splits; ++k) {
+        const float e = s_w[t][k] * inv;
+        // a range without rows holds zeros
+        const float4 v = __ldcs((const float4*)(p.part_o + (k * part + at) * r + d));
+        a.x = fmaf(e, v.x, a.x);
+        a.y = fmaf(e, v.y, a.y);
+        a.z = fmaf(e, v.z, a.z);
+        a.w = fmaf(e, v.w, a.w);
+      }
+      *(float4*)(s_lat + t * r + d) = a;
+    }
+    if (lane == 0 && p.lse) p.lse[at] = empty ? -INFINITY : mx + logf(z);
   }
-  if (lane == 0 && p.lse) p.lse[at] = empty ? -INFINITY : mx + logf(z);
+  __syncthreads();
+  for (int i = threadIdx.x; i < dv; i += blockDim.x) {
+    const T* w = w_uv + ((size_t)h * dv + i) * r;
+    float acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < r; d += 4) {
+      const float4 u = load4(w + d);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float4 v = *(const float4*)(s_lat + t * r + d);
+        acc[t] = fmaf(u.x, v.x, acc[t]);
+        acc[t] = fmaf(u.y, v.y, acc[t]);
+        acc[t] = fmaf(u.z, v.z, acc[t]);
+        acc[t] = fmaf(u.w, v.w, acc[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (n0 + t < p.BT) o[((size_t)(n0 + t) * p.H + h) * dv + i] = from_f32<T>(acc[t]);
+  }
 }
 
-template <typename T, int RPW, int RW>
+template <typename T, int RPW, int KPL, int RW>
 cudaError_t simt_go(const TreeParams& p, cudaStream_t st) {
-  const int M = kWarps * RPW;
-  const size_t smem = sizeof(float) * ((size_t)M * p.D + kKeys * (p.D + 4) + M * kKeys) +
-                      sizeof(int) * kKeys;
-  auto k = tree_simt_kernel<T, RPW, RW>;
+  const int M = kWarps * RPW, keys = 32 * KPL;
+  const size_t smem = sizeof(float) * ((size_t)M * p.D + keys * (p.D + 4) + M * keys);
+  auto k = tree_simt_kernel<T, RPW, KPL, RW>;
   const cudaError_t e =
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -250,28 +290,47 @@ cudaError_t simt_go(const TreeParams& p, cudaStream_t st) {
                     st, p);
 }
 
-template <typename T>
-cudaError_t simt_dispatch(const TreeParams& p, cudaStream_t st) {
-  if (p.tile_rows == kWarps * 4) {
-    if (p.r <= 64) return simt_go<T, 4, 2>(p, st);
-    if (p.r <= 128) return simt_go<T, 4, 4>(p, st);
-    if (p.r <= 256) return simt_go<T, 4, 8>(p, st);
-    return simt_go<T, 4, 16>(p, st);
+template <typename T, int NT>
+cudaError_t simt_out(const TreeParams& p, const void* w_uv, int dv, void* o, cudaStream_t st) {
+  const size_t smem = sizeof(float) * NT * p.r;
+  auto k = tree_simt_out_kernel<T, NT>;
+  if (smem > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
   }
-  if (p.r <= 512) return simt_go<T, 1, 16>(p, st);
-  return simt_go<T, 1, 32>(p, st);
+  return launch_pdl(k, dim3((unsigned)(p.H * ((p.BT + NT - 1) / NT))), dim3(128), smem, st, p,
+                    (const T*)w_uv, (T*)o, dv);
+}
+
+template <typename T>
+cudaError_t simt_dispatch(const TreeParams& p, const void* w_uv, int dv, void* o,
+                          cudaStream_t st) {
+  cudaError_t e;
+  if (p.tile_rows == kWarps * 4) {
+    // 64 cache rows per tile where two CTAs fit an SM, else 32
+    if (p.r <= 64 && p.D <= 192) e = simt_go<T, 4, 2, 2>(p, st);
+    else if (p.r <= 128 && p.D <= 192) e = simt_go<T, 4, 2, 4>(p, st);
+    else if (p.r <= 256) e = simt_go<T, 4, 1, 8>(p, st);
+    else e = simt_go<T, 4, 1, 16>(p, st);
+  } else if (p.r <= 512) {
+    e = simt_go<T, 1, 1, 16>(p, st);
+  } else {
+    e = simt_go<T, 1, 1, 32>(p, st);
+  }
+  if (e != cudaSuccess) return e;
+  // four tokens a CTA while those fill the GPU no more than twice over, else sixteen (W_UV[h] is
+  // read once per CTA)
+  if ((int64_t)p.H * p.BT <= 4 * 2 * 148 * 4) return simt_out<T, 4>(p, w_uv, dv, o, st);
+  return simt_out<T, 16>(p, w_uv, dv, o, st);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_simt(const mla_config& c, const TreeParams& p, cudaStream_t st) {
-  cudaError_t e = c.dtype == MLA_BF16 ? simt_dispatch<__nv_bfloat16>(p, st)
-                                      : simt_dispatch<float>(p, st);
-  if (e == cudaSuccess && p.splits > 1) {
-    const size_t n = (size_t)p.BT * p.H;
-    e = launch_pdl(tree_merge_kernel, dim3((unsigned)((n + 3) / 4)), dim3(128), 0, st, p);
-  }
-  return e;
+cudaError_t launch_tree_simt(const mla_config& c, const TreeParams& p, const void* w_uv, void* o,
+                             cudaStream_t st) {
+  return c.dtype == MLA_BF16 ? simt_dispatch<__nv_bfloat16>(p, w_uv, c.head_dim_v, o, st)
+                             : simt_dispatch<float>(p, w_uv, c.head_dim_v, o, st);
 }
 
 // Query rows per tile: 32 (four per warp) where r <= 512 and the tile and 32 cache rows fit
