@@ -546,9 +546,9 @@ TreeLayout tree_layout(const mla_config& c, int batch, int T) {
     L.part_o = take((size_t)kMaxPartials * kTreeTile * c.kv_rank * sizeof(float));
     L.cuts = take(kRanges * sizeof(int4));
   } else {
-    // enough CTAs for four on each of 148 SMs
+    // about two CTAs on each of 148 SMs
     const int64_t ctas = (int64_t)batch * L.tiles;
-    L.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTreeMaxSplits, 4 * 148 / ctas));
+    L.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTreeMaxSplits, 2 * 148 / ctas));
     L.part_lse = take(L.splits * n * sizeof(float));
     L.part_o = take(L.splits * n * c.kv_rank * sizeof(float));
   }

@@ -24,6 +24,13 @@ namespace {
 
 constexpr int kWarps = 8;
 
+// 2^x, off by 2 ulp at most
+__device__ __forceinline__ float ex2_(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <typename T> __device__ __forceinline__ float4 load4(const T* p);
 template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
   return *(const float4*)p;
@@ -42,6 +49,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
   float* s_q = smem;                  // M x D
   float* s_k = s_q + M * D;           // kKeys x ld
   float* s_p = s_k + kKeys * ld;      // M x kKeys
+  __shared__ int s_there[kKeys];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % p.splits, tile = blockIdx.x / p.splits;
   const int b = tile / p.tiles, m0 = (tile - b * p.tiles) * M;
@@ -54,10 +62,20 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
   const int tiles = (len + kKeys - 1) / kKeys, per = (tiles + p.splits - 1) / p.splits;
   const int lo = min(split * per, tiles) * kKeys, hi = min((split + 1) * per * kKeys, len);
 
+  // queries, times softmax_scale / ln 2: scores come out in base-2 units
+  const float c2 = p.scale * 1.4426950408889634f;
   const T* Q = (const T*)p.q + ((size_t)b * rows + m0) * D;
-  for (int i = threadIdx.x; i < M * quads; i += blockDim.x) {
-    const int m = i / quads;
-    ((float4*)s_q)[i] = m0 + m < rows ? load4(Q + 4 * (size_t)i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int qd = lane; qd < quads; qd += 32) {
+    float4 v[RPW];
+#pragma unroll
+    for (int a = 0; a < RPW; ++a) {
+      const int m = warp * RPW + a;
+      v[a] = m0 + m < rows ? load4(Q + (size_t)m * D + 4 * qd) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int a = 0; a < RPW; ++a)
+      *(float4*)(s_q + (warp * RPW + a) * D + 4 * qd) =
+          make_float4(v[a].x * c2, v[a].y * c2, v[a].z * c2, v[a].w * c2);
   }
   float o[RPW][RW], mx[RPW], l[RPW];
 #pragma unroll
@@ -74,11 +92,11 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
   float* pw = s_p + warp * RPW * kKeys;
 
   // the pool row of a cache row, or -1 (past the range, or a block outside the pool)
-  auto place = [&](int row, bool report) -> int64_t {
+  auto place = [&](int row) -> int64_t {
     if (row >= hi) return -1;
     const int at = row / p.bs, blk = p.table[(size_t)b * p.max_blocks + at];
     if (blk < 0 || blk >= p.num_blocks) {
-      if (report) set_error(p.err, MLA_DEV_OOB_BLOCK);
+      set_error(p.err, MLA_DEV_OOB_BLOCK);
       return -1;
     }
     return (int64_t)blk * p.bs + (row - at * p.bs);
@@ -86,17 +104,27 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
 
   for (int t0 = lo; t0 < hi; t0 += kKeys) {
     __syncthreads();  // previous tile consumed
-    for (int i = threadIdx.x; i < kKeys * quads; i += blockDim.x) {
-      const int t = i / quads, qd = i - t * quads;
-      const int64_t at = place(t0 + t, true);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (at >= 0) v = load4((const T*)p.pool + at * D + 4 * qd);
-      *(float4*)(s_k + t * ld + 4 * qd) = v;
+    // a warp takes every eighth row; lane j finds where row j of its rows lies
+    constexpr int kPer = kKeys / kWarps;
+    const int64_t my_at = place(t0 + warp + kWarps * (lane % kPer));
+    int64_t at[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) at[j] = __shfl_sync(0xffffffffu, my_at, j) * D;
+    for (int qd = lane; qd < quads; qd += 32) {  // all rows' loads, then their stores
+      float4 v[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        v[j] = at[j] >= 0 ? load4((const T*)p.pool + at[j] + 4 * qd)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) *(float4*)(s_k + (warp + kWarps * j) * ld + 4 * qd) = v[j];
     }
+    if (lane < kPer) s_there[warp + kWarps * lane] = my_at >= 0;
+    __syncthreads();
+    if (m0 + warp * RPW >= rows) continue;  // this warp has no query rows
     bool there[KPL];
 #pragma unroll
-    for (int c = 0; c < KPL; ++c) there[c] = place(t0 + lane + 32 * c, false) >= 0;
-    __syncthreads();
+    for (int c = 0; c < KPL; ++c) there[c] = s_there[lane + 32 * c];
 
     // scores of cache rows t0 + lane + 32 c
     float s[RPW][KPL];
@@ -105,6 +133,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
 #pragma unroll
       for (int c = 0; c < KPL; ++c) s[a][c] = 0.f;
     const float* krow = s_k + lane * ld;
+#pragma unroll 4
     for (int d = 0; d < D; d += 4) {
       float4 k[KPL];
 #pragma unroll
@@ -131,15 +160,15 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
         const int node = t0 + lane + 32 * c - first;
         seen[c] = there[c];
         if (drafted && node >= 0 && seen[c]) seen[c] = tree_sees(p, b, tok[a], node);
-        s[a][c] = seen[c] ? s[a][c] * p.scale : -INFINITY;
+        s[a][c] = seen[c] ? s[a][c] : -INFINITY;
         top = fmaxf(top, s[a][c]);
       }
       const float m = fmaxf(mx[a], warp_max(top));
-      const float alpha = mx[a] == -INFINITY ? 0.f : expf(mx[a] - m);
+      const float alpha = mx[a] == -INFINITY ? 0.f : ex2_(mx[a] - m);
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < KPL; ++c) {
-        const float e = seen[c] && s[a][c] != -INFINITY ? expf(s[a][c] - m) : 0.f;
+        const float e = seen[c] && s[a][c] != -INFINITY ? ex2_(s[a][c] - m) : 0.f;
         sum += e;
         pw[a * kKeys + lane + 32 * c] = e;
       }
@@ -149,36 +178,45 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
       for (int k = 0; k < RW; ++k) o[a][k] *= alpha;
     }
     __syncwarp();
+    // a lane's columns: 64 k + 2 lane and the next
     if (drafted) {  // a masked row's values are left out, whatever they are
       for (int j = 0; j < kKeys; ++j) {
 #pragma unroll
-        for (int k = 0; k < RW; ++k) {
-          const int d = lane + 32 * k;
-          const float v = d < r ? s_k[j * ld + d] : 0.f;
+        for (int k = 0; k < RW / 2; ++k) {
+          const int d = 64 * k + 2 * lane;
+          const float2 v = d < r ? *(const float2*)(s_k + j * ld + d) : make_float2(0.f, 0.f);
 #pragma unroll
           for (int a = 0; a < RPW; ++a) {
             const float e = pw[a * kKeys + j];
-            o[a][k] = e == 0.f ? o[a][k] : fmaf(e, v, o[a][k]);
+            o[a][2 * k] = e == 0.f ? o[a][2 * k] : fmaf(e, v.x, o[a][2 * k]);
+            o[a][2 * k + 1] = e == 0.f ? o[a][2 * k + 1] : fmaf(e, v.y, o[a][2 * k + 1]);
           }
         }
       }
     } else {
+#pragma unroll 4
       for (int j = 0; j < kKeys; j += 4) {
         float4 e[RPW];
 #pragma unroll
         for (int a = 0; a < RPW; ++a) e[a] = *(const float4*)(pw + a * kKeys + j);
 #pragma unroll
-        for (int k = 0; k < RW; ++k) {
-          const int d = lane + 32 * k;
+        for (int k = 0; k < RW / 2; ++k) {
+          const int d = 64 * k + 2 * lane;
           if (d < r) {
-            const float v0 = s_k[j * ld + d], v1 = s_k[(j + 1) * ld + d],
-                        v2 = s_k[(j + 2) * ld + d], v3 = s_k[(j + 3) * ld + d];
+            const float* at = s_k + j * ld + d;
+            const float2 v0 = *(const float2*)at, v1 = *(const float2*)(at + ld),
+                         v2 = *(const float2*)(at + 2 * ld), v3 = *(const float2*)(at + 3 * ld);
 #pragma unroll
             for (int a = 0; a < RPW; ++a) {
-              o[a][k] = fmaf(e[a].x, v0, o[a][k]);
-              o[a][k] = fmaf(e[a].y, v1, o[a][k]);
-              o[a][k] = fmaf(e[a].z, v2, o[a][k]);
-              o[a][k] = fmaf(e[a].w, v3, o[a][k]);
+              float &x = o[a][2 * k], &y = o[a][2 * k + 1];
+              x = fmaf(e[a].x, v0.x, x);
+              y = fmaf(e[a].x, v0.y, y);
+              x = fmaf(e[a].y, v1.x, x);
+              y = fmaf(e[a].y, v1.y, y);
+              x = fmaf(e[a].z, v2.x, x);
+              y = fmaf(e[a].z, v2.y, y);
+              x = fmaf(e[a].w, v3.x, x);
+              y = fmaf(e[a].w, v3.y, y);
             }
           }
         }
@@ -195,24 +233,44 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
     const size_t at = (size_t)split * p.BT * p.H + (size_t)b * rows + m0 + m;
     const bool empty = l[a] == 0.f;
     const float inv = empty ? 0.f : 1.f / l[a];
-    if (lane == 0) p.part_lse[at] = empty ? -INFINITY : mx[a] + logf(l[a]);
+    if (lane == 0)
+      p.part_lse[at] = empty ? -INFINITY : (mx[a] + log2f(l[a])) * 0.6931471805599453f;
 #pragma unroll
-    for (int k = 0; k < RW; ++k) {
-      const int d = lane + 32 * k;
-      if (d < r) p.part_o[at * r + d] = empty ? 0.f : o[a][k] * inv;
+    for (int k = 0; k < RW / 2; ++k) {
+      const int d = 64 * k + 2 * lane;
+      if (d < r)
+        *(float2*)(p.part_o + at * r + d) =
+            empty ? make_float2(0.f, 0.f) : make_float2(o[a][2 * k] * inv, o[a][2 * k + 1] * inv);
     }
   }
 }
 
 // ---- merge of the ranges and W_UV: one CTA per head and NT tokens -------------------------
+// stage: W_UV[h] fits shared memory; it is fetched before the wait for the attention (it is no
+// result of it) and read from there.
 template <typename T, int NT>
 __global__ void __launch_bounds__(128)
-tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restrict__ o, int dv) {
-  extern __shared__ __align__(16) float s_lat[];  // NT x r
+tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restrict__ o, int dv,
+                     int stage) {
+  extern __shared__ __align__(16) float s_lat[];  // NT x r, then dv rows of W_UV[h]
   __shared__ float s_w[NT][kTreeMaxSplits];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = p.r;
   const int h = blockIdx.x % p.H, n0 = blockIdx.x / p.H * NT;
   const size_t part = (size_t)p.BT * p.H;
+  constexpr int kPiece = 16 / sizeof(T);
+  const int pitch = r + kPiece;  // values per row of the copy
+  T* s_wuv = (T*)(s_lat + NT * r);
+  if (stage) {
+    const T* w = w_uv + (size_t)h * dv * r;
+    for (int i = threadIdx.x; i < dv * (r / kPiece); i += blockDim.x) {
+      const int row = i / (r / kPiece), c = i - row * (r / kPiece);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(s_wuv + row * pitch + c * kPiece)),
+                   "l"(w + (size_t)i * kPiece)
+                   : "memory");
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
   wait_prior_grid();
   for (int t = warp; t < NT; t += 4) {  // a warp per token: weights, then the merged row
     const int n = n0 + t;
@@ -240,7 +298,7 @@ tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restri
     __syncwarp();
     for (int d = 4 * lane; d < r; d += 128) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
       for (int k = 0; k < p.splits; ++k) {
         const float e = s_w[t][k] * inv;
         // a range without rows holds zeros
@@ -254,9 +312,10 @@ tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restri
     }
     if (lane == 0 && p.lse) p.lse[at] = empty ? -INFINITY : mx + logf(z);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   for (int i = threadIdx.x; i < dv; i += blockDim.x) {
-    const T* w = w_uv + ((size_t)h * dv + i) * r;
+    const T* w = stage ? s_wuv + i * pitch : w_uv + ((size_t)h * dv + i) * r;
     float acc[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = 0.f;
@@ -292,7 +351,9 @@ cudaError_t simt_go(const TreeParams& p, cudaStream_t st) {
 
 template <typename T, int NT>
 cudaError_t simt_out(const TreeParams& p, const void* w_uv, int dv, void* o, cudaStream_t st) {
-  const size_t smem = sizeof(float) * NT * p.r;
+  const size_t w_bytes = (size_t)dv * (p.r * sizeof(T) + 16);
+  const int stage = w_bytes <= 64 * 1024;
+  const size_t smem = sizeof(float) * NT * p.r + (stage ? w_bytes : 0);
   auto k = tree_simt_out_kernel<T, NT>;
   if (smem > 40 * 1024) {
     const cudaError_t e =
@@ -300,7 +361,7 @@ cudaError_t simt_out(const TreeParams& p, const void* w_uv, int dv, void* o, cud
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(k, dim3((unsigned)(p.H * ((p.BT + NT - 1) / NT))), dim3(128), smem, st, p,
-                    (const T*)w_uv, (T*)o, dv);
+                    (const T*)w_uv, (T*)o, dv, stage);
 }
 
 template <typename T>
