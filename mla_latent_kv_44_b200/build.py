@@ -6,8 +6,8 @@ Each csrc/*.cu compiles to an object under _build/ (recompiled when it or a head
 then the objects link into mla_latent_kv_44_b200/libmla.so with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU (calls then fail with
 MLA_ERR_CUDA) and needs nothing at run time but the NVIDIA driver. A second library,
-libmla_testhook.so, differs only in a test define of the attention kernel (one K-slab load of
-the first work range is left out); only the tests load it.
+libmla_testhook.so, differs only in a test define of the attention kernels (one K load of the first
+work range is left out in each); only the tests load it.
 """
 from __future__ import annotations
 
@@ -29,7 +29,7 @@ LIB = os.path.join(PKG, "libmla.so")
 # (MLA_TEST_DROP_ARRIVE), so that the tests can watch a bounded wait run out.
 TEST_LIB = os.path.join(PKG, "libmla_testhook.so")
 TEST_DEFINE = "-DMLA_TEST_DROP_ARRIVE"
-TEST_SOURCES = ("decode_tc.cu",)
+TEST_SOURCES = ("decode_tc.cu", "tree_tc.cu")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
