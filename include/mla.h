@@ -415,7 +415,7 @@ MLA_API mla_status mla_combine_partials(const mla_config* cfg, const float* part
  * and has no tokens), for more than max_tokens tokens (those behind are dropped, cu_new stops
  * there) and for a free_count outside [0, num_blocks] or more blocks given back than the list
  * has room for (no block moves); MLA_DEV_OOB_BLOCK for a block id outside the pool (slot -1).
- * One launch; deterministic. batch <= MLA_MAX_TABLE_BATCH, max_tokens <= 2^26 and
+ * One launch (two for more than 32,768 tokens); deterministic. batch <= MLA_MAX_TABLE_BATCH, max_tokens <= 2^26 and
  * batch * max_blocks <= 2^30 (MLA_ERR_UNSUPPORTED). max_tokens may be 0.
  */
 MLA_API mla_status mla_build_tables(const mla_config* cfg, const int32_t* seq_lens,
@@ -450,7 +450,8 @@ MLA_API mla_status mla_tree_masks(const int32_t* parents, int32_t parents_batch,
  * step's padding); one outside the pool sets MLA_DEV_OOB_BLOCK and is skipped. Slots must differ:
  * of two tokens with one slot either's values may stay. ckv_raw (n_tokens, r), krope_raw
  * (n_tokens, d_r), pool (num_blocks, block_size, r + d_r) dtype; gamma (r) float32; pos
- * (n_tokens) int32; slots (n_tokens) int64. ckv_raw, gamma and pool must be 16-byte aligned.
+ * (n_tokens) int32; slots (n_tokens) int64. ckv_raw, gamma and pool must be 16-byte aligned,
+ * krope_raw 8-byte.
  * fp32 statistics, angles in double; the sum of squares is taken in another order than
  * mla_append_latent's, so a value may round the other way.
  */

@@ -608,7 +608,8 @@ mla_status mla_append_slots(const mla_config* cfg, const void* ckv_raw, const vo
   if (!ckv_raw || (cfg->rope_dim > 0 && !krope_raw) || !gamma || !pos || !slots || !pool ||
       !dev_err || num_blocks < 1)
     return MLA_ERR_INVALID_ARG;
-  if (!aligned(ckv_raw, 16) || !aligned(gamma, 16) || !aligned(pool, 16))
+  if (!aligned(ckv_raw, 16) || !aligned(gamma, 16) || !aligned(pool, 16) ||
+      (cfg->rope_dim > 0 && !aligned(krope_raw, 8)))
     return MLA_ERR_INVALID_ARG;
   if (n_tokens > (1 << 26)) return MLA_ERR_UNSUPPORTED;
   return from_cuda(launch_append_slots(*cfg, ckv_raw, krope_raw, gamma, pos, slots, pool,

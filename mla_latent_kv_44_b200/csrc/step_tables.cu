@@ -2,7 +2,8 @@
 // lengths (and a drafted tree's parent indices) to the block tables, slot maps, masks and
 // positions that the other calls read.
 //
-// build_tables. One thread-block cluster does the whole call in one launch. Every CTA scans the
+// build_tables. One thread-block cluster does the whole call in one launch, but for the slot map of
+// long token lists (a second kernel's). Every CTA scans the
 // requests (new tokens, blocks given back, blocks taken: three prefix sums) into its own shared
 // memory, so that no offsets travel between CTAs; the CTAs then share the moves and the slot
 // map. Three phases are separated by cluster barriers, because each reads what the one before
@@ -31,6 +32,7 @@ struct TableParams {
   int batch, max_blocks, num_blocks, bs, max_tokens;
   int per_thread;  // tokens per thread and pass: 1 or 4
   bool vec;        // four at a time, 16-byte stores
+  bool map_apart;  // the slot map is the second kernel's
 };
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -95,6 +97,108 @@ __device__ __forceinline__ Request load_request(const TableParams& p, int b) {
   q.want = q.ok ? (int)(((int64_t)q.len + p.bs - 1) / p.bs) : q.held;
   if (!q.ok) q.fresh = 0;
   return q;
+}
+
+// Tokens i0 .. i0 + per - 1: one search and one division for all of them while they stay in a
+// request. cu: offsets of the requests; start_of(b): its first new row, or -1 - row when it was not
+// served; `real` tokens in all.
+template <typename F>
+__device__ __forceinline__ void map_tokens(const TableParams& p, const int* cu, F start_of,
+                                           int64_t i0, int per, int real) {
+  int seq[4], row[4];
+  int64_t slot[4];
+  int b = -1, left = 0, r = 0, at = 0, in = 0, blk = -1;
+  bool served = false;
+  if (p.vec && i0 + 4 <= real) {
+    // four tokens of one request, as most are: everything follows from the first (a warp whose
+    // lanes part here runs both ways, so a block's end inside the four stays on this one)
+    int lo = 0, hi = p.batch - 1;
+    const int i = (int)i0;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    const int start = start_of(lo);
+    if (cu[lo + 1] - i >= 4 && start >= 0 && p.bs >= 4) {
+      const int row0 = start + i - cu[lo], at0 = row0 / p.bs, in0 = row0 - at0 * p.bs;
+      const int32_t* ids = p.table + (size_t)lo * p.max_blocks + at0;
+      const bool ends = in0 + 4 > p.bs;
+      const int id = __ldcg(ids), next = ends ? __ldcg(ids + 1) : id;
+      if (id >= 0 && id < p.num_blocks && next >= 0 && next < p.num_blocks) {
+        const int64_t a = (int64_t)id * p.bs + in0, b4 = (int64_t)next * p.bs + in0 - p.bs;
+        int64_t at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) at[u] = (in0 + u < p.bs ? a : b4) + u;
+        *(int4*)(p.seq_idx + i0) = make_int4(lo, lo, lo, lo);
+        *(int4*)(p.pos + i0) = make_int4(row0, row0 + 1, row0 + 2, row0 + 3);
+        *(longlong2*)(p.slots + i0) = make_longlong2(at[0], at[1]);
+        *(longlong2*)(p.slots + i0 + 2) = make_longlong2(at[2], at[3]);
+        return;
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = (int)i0 + u;
+    seq[u] = -1;
+    row[u] = 0;
+    slot[u] = -1;
+    if (u >= per || i >= real) continue;
+    bool look = false;
+    if (left == 0) {  // the request that holds token i
+      int lo = 0, hi = p.batch - 1;  // the last one with cu <= i
+      if (b >= 0) {
+        lo = b + 1;
+        while (cu[lo + 1] <= i) ++lo;
+      } else {
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (cu[mid] <= i) lo = mid;
+          else hi = mid - 1;
+        }
+      }
+      b = lo;
+      left = cu[b + 1] - i;
+      const int from = start_of(b);
+      served = from >= 0;
+      r = (served ? from : -1 - from) + i - cu[b];
+      at = r / p.bs;
+      in = r - at * p.bs;
+      look = true;
+    } else if (in == p.bs) {
+      in = 0;
+      ++at;
+      look = true;
+    }
+    if (look && served) {
+      blk = __ldcg(p.table + (size_t)b * p.max_blocks + at);
+      if (blk < 0 || blk >= p.num_blocks) {
+        set_error(p.err, MLA_DEV_OOB_BLOCK);
+        blk = -1;
+      }
+    }
+    seq[u] = b;
+    row[u] = r;
+    if (served && blk >= 0) slot[u] = (int64_t)blk * p.bs + in;
+    ++r;
+    ++in;
+    --left;
+  }
+  if (p.vec && i0 + 4 <= p.max_tokens) {
+    *(int4*)(p.seq_idx + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+    *(int4*)(p.pos + i0) = make_int4(row[0], row[1], row[2], row[3]);
+    *(longlong2*)(p.slots + i0) = make_longlong2(slot[0], slot[1]);
+    *(longlong2*)(p.slots + i0 + 2) = make_longlong2(slot[2], slot[3]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (u < per && i0 + u < p.max_tokens) {
+        p.seq_idx[i0 + u] = seq[u];
+        p.pos[i0 + u] = row[u];
+        p.slots[i0 + u] = slot[u];
+      }
+  }
 }
 
 __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TableParams p) {
@@ -204,76 +308,32 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablePa
     }
   }
 
-  // tokens: `per` consecutive ones per thread and pass (one search and one division for all of
-  // them while they stay in a request)
+  // tokens
+  if (p.map_apart) return;
   const int per = p.per_thread, real = min(tokens, p.max_tokens);
   for (int64_t i0 = (int64_t)(cta * kTabThreads + tid) * per; i0 < p.max_tokens;
-       i0 += (int64_t)ctas * kTabThreads * per) {
-    int seq[4], row[4];
-    int64_t slot[4];
-    int b = -1, left = 0, r = 0, at = 0, in = 0, blk = -1;
-    bool served = false;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = (int)i0 + u;
-      seq[u] = -1;
-      row[u] = 0;
-      slot[u] = -1;
-      if (u >= per || i >= real) continue;
-      bool look = false;
-      if (left == 0) {  // the request that holds token i
-        int lo = 0, hi = p.batch - 1;  // the last one with s_cu <= i
-        if (b >= 0) {
-          lo = b + 1;
-          while (s_cu[lo + 1] <= i) ++lo;
-        } else {
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_cu[mid] <= i) lo = mid;
-            else hi = mid - 1;
-          }
-        }
-        b = lo;
-        left = s_cu[b + 1] - i;
-        served = s_start[b] >= 0;
-        r = (served ? s_start[b] : -1 - s_start[b]) + i - s_cu[b];
-        at = r / p.bs;
-        in = r - at * p.bs;
-        look = true;
-      } else if (in == p.bs) {
-        in = 0;
-        ++at;
-        look = true;
-      }
-      if (look && served) {
-        blk = __ldcg(p.table + (size_t)b * p.max_blocks + at);
-        if (blk < 0 || blk >= p.num_blocks) {
-          set_error(p.err, MLA_DEV_OOB_BLOCK);
-          blk = -1;
-        }
-      }
-      seq[u] = b;
-      row[u] = r;
-      if (served && blk >= 0) slot[u] = (int64_t)blk * p.bs + in;
-      ++r;
-      ++in;
-      --left;
-    }
-    if (p.vec && i0 + 4 <= p.max_tokens) {
-      *(int4*)(p.seq_idx + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
-      *(int4*)(p.pos + i0) = make_int4(row[0], row[1], row[2], row[3]);
-      *(longlong2*)(p.slots + i0) = make_longlong2(slot[0], slot[1]);
-      *(longlong2*)(p.slots + i0 + 2) = make_longlong2(slot[2], slot[3]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u < per && i0 + u < p.max_tokens) {
-          p.seq_idx[i0 + u] = seq[u];
-          p.pos[i0 + u] = row[u];
-          p.slots[i0 + u] = slot[u];
-        }
-    }
-  }
+       i0 += (int64_t)ctas * kTabThreads * per)
+    map_tokens(p, s_cu, [&](int b) { return s_start[b]; }, i0, per, real);
+}
+
+// The slot map of long token lists, over the whole GPU: what a request was given follows from the
+// first kernel's results (served: as many blocks held as its rows need).
+constexpr int kMapThreads = 256;
+
+__global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const TableParams p) {
+  extern __shared__ int s_cu[];
+  wait_prior_grid();
+  for (int b = threadIdx.x; b <= p.batch; b += kMapThreads) s_cu[b] = p.cu[b];
+  __syncthreads();
+  const int64_t i0 = ((int64_t)blockIdx.x * kMapThreads + threadIdx.x) * p.per_thread;
+  if (i0 >= p.max_tokens) return;
+  map_tokens(
+      p, s_cu,
+      [&](int b) {
+        const int len = p.seq_lens[b], start = len - p.new_lens[b];
+        return (int64_t)p.held_out[b] * p.bs >= len ? start : -1 - start;
+      },
+      i0, p.per_thread, s_cu[p.batch]);
 }
 
 }  // namespace
@@ -284,13 +344,15 @@ cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens
                                 int32_t* held_out, int32_t* free_count_out, int32_t* cu,
                                 int32_t* seq_idx, int32_t* pos, int64_t* slots, int max_tokens,
                                 uint32_t* err, cudaStream_t st) {
-  // one token per thread while that takes one pass of one CTA (64 tokens: 7 us either way), else
-  // four (131,072 tokens: 24.6 us with one search per token)
+  // one token per thread while that takes one pass of one CTA, else four; and lists that take
+  // the cluster more than one pass go to a kernel of their own (131,072 tokens: 17.0 us in the
+  // cluster alone)
   const int per = max_tokens <= kTabThreads ? 1 : 4;
   const bool vec = per == 4 && (((uintptr_t)seq_idx | (uintptr_t)pos | (uintptr_t)slots) & 15) == 0;
+  const bool apart = max_tokens > kTabMaxCtas * kTabThreads * 4;
   TableParams p{seq_lens, new_lens, held,  table, free_blocks, free_count, held_out,
                 free_count_out, cu, seq_idx, pos, slots, err, batch, max_blocks, num_blocks, bs,
-                max_tokens, per, vec};
+                max_tokens, per, vec, apart};
   const size_t smem = sizeof(int) * (4 * (size_t)batch + 1);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -298,7 +360,8 @@ cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens
     if (e != cudaSuccess) return e;
   }
   // one CTA while a pass of it covers the tokens and the requests, else a full cluster
-  const int ctas = max_tokens <= kTabThreads && batch <= kTabThreads ? 1 : kTabMaxCtas;
+  const int ctas =
+      (apart || max_tokens <= kTabThreads) && batch <= kTabThreads ? 1 : kTabMaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kTabThreads);
@@ -313,7 +376,11 @@ cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
+  if (e == cudaSuccess && apart)
+    e = launch_pdl(slot_map_kernel, dim3((max_tokens + 4 * kMapThreads - 1) / (4 * kMapThreads)),
+                   dim3(kMapThreads), sizeof(int) * ((size_t)batch + 1), st, p);
+  return e;
 }
 
 // ------------------------------------------------------------------------------------------

@@ -60,8 +60,25 @@ struct RopeTheta {
   double t[128];  // d_r <= 256
 };
 
+// two neighbouring values
+__device__ __forceinline__ float2 load2(const float* p) { return *(const float2*)p; }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  const uint32_t u = *(const uint32_t*)p;
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ void store2(float* p, float x, float y) {
+  *(float2*)p = make_float2(x, y);
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
+  *(__nv_bfloat162*)p = __floats2bfloat162_rn(x, y);
+}
+
+// four CTAs per SM: with more the registers no longer hold what a row has in flight (16,384 rows:
+// 10.5 us at four, 11.3 at three and five, 14.8 at six; two rows per warp 14.0)
+constexpr int kAppendCtas = 4;
+
 template <typename T, int NP>
-__global__ void __launch_bounds__(kAppendWarps * 32)
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas)
 append_slots_kernel(const T* __restrict__ ckv, const T* __restrict__ kr,
                     const float* __restrict__ gamma, const int32_t* __restrict__ pos,
                     const int64_t* __restrict__ slots, T* pool, int64_t pool_rows, int n, int r,
@@ -73,37 +90,39 @@ append_slots_kernel(const T* __restrict__ ckv, const T* __restrict__ kr,
   const double theta0 = lane < half ? theta.t[lane] : 0.0;
   wait_prior_grid();
   for (int row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5); row < n; row += warps) {
+    // everything that the row reads, before anything is done with it
     const int64_t slot = slots[row];
+    const double p = (double)pos[row];
+    float v[NP][E];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int at = (lane + 32 * k) * E;
+      if (at < r) Piece<T>::load(ckv + (size_t)row * r + at, v[k]);
+    }
+    float2 k0;
+    if (lane < half) k0 = load2(kr + (size_t)row * dr + 2 * lane);
     if (slot < 0) continue;  // a step's padding
     if (slot >= pool_rows) {
       if (lane == 0) set_error(err, MLA_DEV_OOB_BLOCK);
       continue;
     }
-    const T* x = ckv + (size_t)row * r;
-    float v[NP][E];
-    float ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int at = (lane + 32 * k) * E;
-      if (at < r) {
-        Piece<T>::load(x + at, v[k]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(v[k][e], v[k][e], ss);
-      }
-    }
     T* dst = pool + (size_t)slot * D;
-    const double p = (double)pos[row];
-    const T* kx = kr + (size_t)row * dr;
     for (int i = lane; i < half; i += 32) {
+      const float2 x = i < 32 ? k0 : load2(kr + (size_t)row * dr + 2 * i);
       const double a = p * (i < 32 ? theta0 : theta.t[i]);
       const double turns = rint(a * 0.15915494309189535);  // 1 / (2 pi)
       const double red = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, a));
       float c, s;
       sincosf((float)red, &s, &c);
-      const float x0 = to_f32(kx[2 * i]), x1 = to_f32(kx[2 * i + 1]);
-      dst[r + 2 * i] = from_f32<T>(x0 * c - x1 * s);
-      dst[r + 2 * i + 1] = from_f32<T>(x0 * s + x1 * c);
+      store2(dst + r + 2 * i, x.x * c - x.y * s, x.x * s + x.y * c);
     }
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+      if ((lane + 32 * k) * E < r) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) ss = fmaf(v[k][e], v[k][e], ss);
+      }
     ss = warp_sum(ss);
     const float inv = 1.0f / sqrtf(ss / (float)r + eps);
 #pragma unroll
@@ -128,7 +147,7 @@ template <typename T, int NP>
 cudaError_t append_slots_go(const mla_config& c, const void* ckv, const void* kr,
                             const float* gamma, const int32_t* pos, const int64_t* slots,
                             void* pool, int num_blocks, int n, uint32_t* err, cudaStream_t st) {
-  const int grid = std::min((n + kAppendWarps - 1) / kAppendWarps, 148 * 8);
+  const int grid = std::min((n + kAppendWarps - 1) / kAppendWarps, 148 * kAppendCtas);
   RopeTheta theta = {};
   // by products: the error of the 128th is 1e-14 of it, 3e-9 in any angle
   if (c.rope_dim > 0) {
