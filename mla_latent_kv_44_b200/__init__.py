@@ -140,16 +140,23 @@ class Config:
                          self.rms_eps, scale, MLA_BF16 if self.dtype == "bf16" else MLA_F32,
                          self.decode_kernel)
 
-    def ref(self):
-        """A reference to the C struct for a call; built again only when a field has changed."""
+    def _held(self):
         key = (self.num_heads, self.head_dim, self.kv_rank, self.rope_dim, self.block_size,
                self.dtype, self.head_dim_v, self.rope_base, self.rms_eps, self.softmax_scale,
                self.decode_kernel)
-        held = self.__dict__.get("_ref")
+        held = self.__dict__.get("_struct")
         if held is None or held[0] != key:
-            held = (key, ctypes.byref(self.c()))
-            self.__dict__["_ref"] = held
-        return held[1]
+            c = self.c()
+            held = self.__dict__["_struct"] = (key, c, ctypes.byref(c), ctypes.addressof(c))
+        return held
+
+    def ref(self):
+        """A reference to the C struct for a call; built again only when a field has changed."""
+        return self._held()[2]
+
+    def address(self) -> int:
+        """The address of that struct; good until a field changes."""
+        return self._held()[3]
 
     @property
     def row_width(self) -> int:
@@ -334,54 +341,72 @@ def prefill(cfg: Config, q_nope, q_rope, pos, rows, w_uk, w_uv, cu_seqlens, max_
 # ---- speculative decoding with a drafted tree ------------------------------------------------
 # These calls check what a raw pointer cannot carry (device, dtype, shape, contiguity) and raise
 # MlaError before anything is launched; they launch on the tensors' device whichever device is
-# current. The checks are written out in each call, and only a failed one asks _refuse which it
-# was: a call of a few microseconds on the GPU should not take longer on the host.
+# current. Checks and call are in a compiled module (csrc/fast_call.cpp): a call of a few
+# microseconds on the GPU should not take longer on the host. _refuse says what it refused.
 
-torch = None  # imported by the first of these calls
+class _Fast:
+    """The compiled module, loaded on first use and given the library's functions."""
+
+    def __getattr__(self, name):
+        import torch  # noqa: F401  (its libraries are the module's)
+        try:
+            from . import _fast_call
+        except ImportError as e:
+            raise ImportError("mla_latent_kv_44_b200/_fast_call.so cannot be loaded: build it with "
+                              f"`python -m mla_latent_kv_44_b200.build` ({e})") from e
+        for call in ("build_tables", "tree_masks", "append_slots", "decode_tree", "commit_tree"):
+            fn = getattr(lib, "mla_" + call)
+            _fast_call.bind("mla_" + call, ctypes.cast(fn, _vp).value)
+            self.__dict__[call] = getattr(_fast_call, call)
+        return self.__dict__[name]
 
 
-def _import_torch():
-    global torch
-    import torch as module
-    torch = module
+_fast = _Fast()
 
 
-def _refuse(where: str, device: int, *tensors):
+def _raw(stream):
+    """None (the current stream of the tensors' device) or the handle of a stream."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse(where: str, *tensors):
     """Raise for the first (name, tensor, dtype, shape) that is not a contiguous tensor of that
-    kind on GPU `device`."""
+    kind on the first one's GPU. A None in a shape stands for any size."""
+    import torch
+    device = None
     for name, t, dtype, shape in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is {type(t).__name__}, not a tensor")
+        if t.dim() != len(shape):
+            raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} has shape {tuple(t.shape)}, wanted "
+                           f"{len(shape)} dimensions")
         if not t.is_cuda:
             raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is on {t.device}, not on a GPU")
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == device and
-                t.is_contiguous()):
+        device = t.device if device is None else device
+        if (t.dtype is dtype and t.device == device and t.is_contiguous() and
+                all(w is None or w == n for n, w in zip(t.shape, shape))):
             continue
         raise MlaError(MLA_ERR_INVALID_ARG,
                        f"{where}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}"
                        f"{'' if t.is_contiguous() else ' (not contiguous)'}, wanted {dtype} "
-                       f"{tuple(shape)} on cuda:{device}")
+                       f"({', '.join('any' if n is None else str(n) for n in shape)}) on {device}")
+    raise MlaError(MLA_ERR_INVALID_ARG, where)
 
 
-def _sizes(where: str, name: str, t, dims: int):
-    """The shape of a tensor whose sizes the call takes from it."""
-    shape = t.shape
-    if len(shape) != dims:
-        raise MlaError(MLA_ERR_INVALID_ARG,
-                       f"{where}: {name} has shape {tuple(shape)}, wanted {dims} dimensions")
-    return shape
+def _size(t, dim: int):
+    """A size that the other tensors' shapes follow; None where t has no such dimension."""
+    return t.shape[dim] if getattr(t, "ndim", 0) > dim else None
 
 
-def _on(device: int, stream) -> int:
-    """The raw handle of `stream`; None is the device's current one. (torch.cuda.current_stream()
-    makes a Stream object, which takes longer than the rest of a small call.)"""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _elsewhere(where: str, device: int, fn, *args):
-    """fn(*args) with `device` current, which it was not."""
-    with torch.cuda.device(device):
-        _check(fn(*args), where)
+def _finish(where: str, st: int, first, call, args, tensors):
+    """What is left to do when a fast call did not return MLA_OK."""
+    if st == -2:  # the tensors are on another device than the current one
+        import torch
+        with torch.cuda.device(first.device):
+            st = call(*args)
+    if st == -1:
+        _refuse(where, *tensors())
+    _check(st, where)
 
 
 def build_tables(cfg: Config, seq_lens, new_lens, block_table, blocks_held, free_blocks,
@@ -392,120 +417,57 @@ def build_tables(cfg: Config, seq_lens, new_lens, block_table, blocks_held, free
     The pool has free_blocks.shape[0] blocks; blocks_held_out and free_count_out may be
     blocks_held and free_count.
     """
-    if torch is None:
-        _import_torch()
-    w, i32 = "mla_build_tables", torch.int32
-    dev = seq_lens.get_device()
-    per, rows = _sizes(w, "seq_lens", seq_lens, 1), _sizes(w, "slots", slots, 1)
-    blocks, width = _sizes(w, "free_blocks", free_blocks, 1)[0], _sizes(
-        w, "block_table", block_table, 2)[1]
-    n, tokens = per[0], rows[0]
-    if not (seq_lens.is_cuda and seq_lens.dtype is i32 and seq_lens.is_contiguous() and
-            new_lens.dtype is i32 and new_lens.shape == per and new_lens.get_device() == dev and
-            new_lens.is_contiguous() and
-            block_table.dtype is i32 and block_table.shape[0] == n and
-            block_table.get_device() == dev and block_table.is_contiguous() and
-            blocks_held.dtype is i32 and blocks_held.shape == per and
-            blocks_held.get_device() == dev and blocks_held.is_contiguous() and
-            free_blocks.dtype is i32 and free_blocks.get_device() == dev and
-            free_blocks.is_contiguous() and
-            free_count.dtype is i32 and free_count.shape == (1,) and
-            free_count.get_device() == dev and
-            blocks_held_out.dtype is i32 and blocks_held_out.shape == per and
-            blocks_held_out.get_device() == dev and blocks_held_out.is_contiguous() and
-            free_count_out.dtype is i32 and free_count_out.shape == (1,) and
-            free_count_out.get_device() == dev and
-            cu_new.dtype is i32 and cu_new.shape == (n + 1,) and cu_new.get_device() == dev and
-            cu_new.is_contiguous() and
-            seq_idx.dtype is i32 and seq_idx.shape == rows and seq_idx.get_device() == dev and
-            seq_idx.is_contiguous() and
-            pos.dtype is i32 and pos.shape == rows and pos.get_device() == dev and
-            pos.is_contiguous() and
-            slots.dtype is torch.int64 and slots.get_device() == dev and slots.is_contiguous() and
-            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev):
-        _refuse(w, dev, ("seq_lens", seq_lens, i32, (n,)), ("new_lens", new_lens, i32, (n,)),
-                ("block_table", block_table, i32, (n, width)),
-                ("blocks_held", blocks_held, i32, (n,)),
-                ("free_blocks", free_blocks, i32, (blocks,)),
-                ("free_count", free_count, i32, (1,)),
-                ("blocks_held_out", blocks_held_out, i32, (n,)),
-                ("free_count_out", free_count_out, i32, (1,)), ("cu_new", cu_new, i32, (n + 1,)),
-                ("seq_idx", seq_idx, i32, (tokens,)), ("pos", pos, i32, (tokens,)),
-                ("slots", slots, torch.int64, (tokens,)), ("dev_err", dev_err, i32, (1,)))
-    args = (cfg.ref(), seq_lens.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(), width,
-            blocks_held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(), blocks,
-            blocks_held_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(),
-            seq_idx.data_ptr(), pos.data_ptr(), slots.data_ptr(), tokens, dev_err.data_ptr(),
-            _on(dev, stream))
-    if dev != torch._C._cuda_getDevice():
-        return _elsewhere(w, dev, lib.mla_build_tables, *args)
-    st = lib.mla_build_tables(*args)
+    args = (cfg.address(), seq_lens, new_lens, block_table, blocks_held, free_blocks, free_count,
+            blocks_held_out, free_count_out, cu_new, seq_idx, pos, slots, dev_err, _raw(stream))
+    st = _fast.build_tables(*args)
     if st:
-        raise MlaError(st, w)
+        def tensors():
+            import torch
+            i32, n, m = torch.int32, _size(seq_lens, 0), _size(slots, 0)
+            return (("seq_lens", seq_lens, i32, (n,)), ("new_lens", new_lens, i32, (n,)),
+                    ("block_table", block_table, i32, (n, None)),
+                    ("blocks_held", blocks_held, i32, (n,)),
+                    ("free_blocks", free_blocks, i32, (None,)),
+                    ("free_count", free_count, i32, (1,)),
+                    ("blocks_held_out", blocks_held_out, i32, (n,)),
+                    ("free_count_out", free_count_out, i32, (1,)),
+                    ("cu_new", cu_new, i32, (None if n is None else n + 1,)),
+                    ("seq_idx", seq_idx, i32, (m,)), ("pos", pos, i32, (m,)),
+                    ("slots", slots, torch.int64, (m,)), ("dev_err", dev_err, i32, (1,)))
+        _finish("mla_build_tables", st, seq_lens, _fast.build_tables, args, tensors)
 
 
 def tree_masks(parents, seq_lens, mask, pos, dev_err, stream=None):
     """mla_tree_masks: ancestor masks (int32 words) and RoPE positions of drafted trees given by
     their parent indices, (batch, T), or (1, T) for one tree that all sequences share."""
-    if torch is None:
-        _import_torch()
-    w, i32 = "mla_tree_masks", torch.int32
-    dev = parents.get_device()
-    n = _sizes(w, "seq_lens", seq_lens, 1)[0]
-    rows, T = _sizes(w, "parents", parents, 2)
-    if not (parents.is_cuda and parents.dtype is i32 and parents.is_contiguous() and
-            seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous() and
-            mask.dtype is i32 and mask.shape == (n * T, (T + 31) // 32) and
-            mask.get_device() == dev and mask.is_contiguous() and
-            pos.dtype is i32 and pos.shape == (n * T,) and pos.get_device() == dev and
-            pos.is_contiguous() and
-            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev):
-        _refuse(w, dev, ("parents", parents, i32, (rows, T)), ("seq_lens", seq_lens, i32, (n,)),
-                ("mask", mask, i32, (n * T, (T + 31) // 32)), ("pos", pos, i32, (n * T,)),
-                ("dev_err", dev_err, i32, (1,)))
-    args = (parents.data_ptr(), rows, seq_lens.data_ptr(), n, T, mask.data_ptr(), pos.data_ptr(),
-            dev_err.data_ptr(), _on(dev, stream))
-    if dev != torch._C._cuda_getDevice():
-        return _elsewhere(w, dev, lib.mla_tree_masks, *args)
-    st = lib.mla_tree_masks(*args)
+    args = (parents, seq_lens, mask, pos, dev_err, _raw(stream))
+    st = _fast.tree_masks(*args)
     if st:
-        raise MlaError(st, w)
+        def tensors():
+            import torch
+            i32, n, T = torch.int32, _size(seq_lens, 0), _size(parents, 1)
+            m = None if n is None or T is None else n * T
+            return (("parents", parents, i32, (None, T)), ("seq_lens", seq_lens, i32, (n,)),
+                    ("mask", mask, i32, (m, None if T is None else (T + 31) // 32)),
+                    ("pos", pos, i32, (m,)), ("dev_err", dev_err, i32, (1,)))
+        _finish("mla_tree_masks", st, parents, _fast.tree_masks, args, tensors)
 
 
 def append_slots(cfg: Config, ckv_raw, krope_raw, gamma, pos, slots, pool, dev_err, stream=None):
     """mla_append_slots: mla_append_latent's rows written to the pool rows `slots` (a negative
     slot is skipped), RoPE positions given apart. krope_raw may be None when rope_dim is 0."""
-    if torch is None:
-        _import_torch()
-    w, dt, i32 = "mla_append_slots", cfg.torch_dtype, torch.int32
-    dev = pool.get_device()
-    per = _sizes(w, "slots", slots, 1)
-    n, blocks, r, dr = per[0], _sizes(w, "pool", pool, 3)[0], cfg.kv_rank, cfg.rope_dim
-    if not (pool.is_cuda and pool.dtype is dt and pool.is_contiguous() and
-            pool.shape == (blocks, cfg.block_size, r + dr) and
-            ckv_raw.dtype is dt and ckv_raw.shape == (n, r) and ckv_raw.get_device() == dev and
-            ckv_raw.is_contiguous() and
-            gamma.dtype is torch.float32 and gamma.shape == (r,) and gamma.get_device() == dev and
-            gamma.is_contiguous() and
-            pos.dtype is i32 and pos.shape == per and pos.get_device() == dev and
-            pos.is_contiguous() and
-            slots.dtype is torch.int64 and slots.get_device() == dev and slots.is_contiguous() and
-            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev and
-            (dr == 0 or (krope_raw.dtype is dt and krope_raw.shape == (n, dr) and
-                         krope_raw.get_device() == dev and krope_raw.is_contiguous()))):
-        _refuse(w, dev, ("pool", pool, dt, (blocks, cfg.block_size, r + dr)),
-                ("ckv_raw", ckv_raw, dt, (n, r)), ("gamma", gamma, torch.float32, (r,)),
-                ("pos", pos, i32, (n,)), ("slots", slots, torch.int64, (n,)),
-                ("dev_err", dev_err, i32, (1,)),
-                *([("krope_raw", krope_raw, dt, (n, dr))] if dr else []))
-    args = (cfg.ref(), ckv_raw.data_ptr(), krope_raw.data_ptr() if dr else None, gamma.data_ptr(),
-            pos.data_ptr(), slots.data_ptr(), pool.data_ptr(), blocks, n, dev_err.data_ptr(),
-            _on(dev, stream))
-    if dev != torch._C._cuda_getDevice():
-        return _elsewhere(w, dev, lib.mla_append_slots, *args)
-    st = lib.mla_append_slots(*args)
+    args = (cfg.address(), ckv_raw, krope_raw, gamma, pos, slots, pool, dev_err, _raw(stream))
+    st = _fast.append_slots(*args)
     if st:
-        raise MlaError(st, w)
+        def tensors():
+            import torch
+            dt, n, r, dr = cfg.torch_dtype, _size(slots, 0), cfg.kv_rank, cfg.rope_dim
+            return (("pool", pool, dt, (None, cfg.block_size, r + dr)),
+                    ("ckv_raw", ckv_raw, dt, (n, r)), ("gamma", gamma, torch.float32, (r,)),
+                    ("pos", pos, torch.int32, (n,)), ("slots", slots, torch.int64, (n,)),
+                    ("dev_err", dev_err, torch.int32, (1,)),
+                    *((("krope_raw", krope_raw, dt, (n, dr)),) if dr else ()))
+        _finish("mla_append_slots", st, pool, _fast.append_slots, args, tensors)
 
 
 def decode_tree_workspace_size(cfg: Config, batch: int, q_per_seq: int) -> int:
@@ -516,89 +478,45 @@ def decode_tree(cfg: Config, q, pool, block_table, seq_lens, q_per_seq: int, tre
                 workspace, o, lse, dev_err, stream=None):
     """mla_decode_tree: attention of every drafted token over its sequence's cache and the drafted
     rows its mask names (None: a chain), then W_UV. lse may be None."""
-    if torch is None:
-        _import_torch()
-    w, dt, i32 = "mla_decode_tree", cfg.torch_dtype, torch.int32
-    dev = pool.get_device()
-    n = _sizes(w, "seq_lens", seq_lens, 1)[0]
-    blocks, width = _sizes(w, "pool", pool, 3)[0], _sizes(w, "block_table", block_table, 2)[1]
-    size = _sizes(w, "workspace", workspace, 1)[0]
-    nt, H, r, bs = n * q_per_seq, cfg.num_heads, cfg.kv_rank, cfg.block_size
-    D, dv = r + cfg.rope_dim, cfg.head_dim_v or cfg.head_dim
-    if not (pool.is_cuda and pool.dtype is dt and pool.shape == (blocks, bs, D) and
-            pool.is_contiguous() and
-            q.dtype is dt and q.shape == (nt, H, D) and q.get_device() == dev and
-            q.is_contiguous() and
-            block_table.dtype is i32 and block_table.shape[0] == n and
-            block_table.get_device() == dev and block_table.is_contiguous() and
-            seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous() and
-            w_uv.dtype is dt and w_uv.shape == (H, dv, r) and w_uv.get_device() == dev and
-            w_uv.is_contiguous() and
-            workspace.dtype is torch.uint8 and workspace.get_device() == dev and
-            workspace.is_contiguous() and
-            o.dtype is dt and o.shape == (nt, H, dv) and o.get_device() == dev and
-            o.is_contiguous() and
-            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev and
-            (tree_mask is None or
-             (tree_mask.dtype is i32 and tree_mask.shape == (nt, (q_per_seq + 31) // 32) and
-              tree_mask.get_device() == dev and tree_mask.is_contiguous())) and
-            (lse is None or
-             (lse.dtype is torch.float32 and lse.shape == (nt, H) and lse.get_device() == dev and
-              lse.is_contiguous()))):
-        _refuse(w, dev, ("pool", pool, dt, (blocks, bs, D)), ("q", q, dt, (nt, H, D)),
-                ("block_table", block_table, i32, (n, width)), ("seq_lens", seq_lens, i32, (n,)),
-                ("w_uv", w_uv, dt, (H, dv, r)), ("workspace", workspace, torch.uint8, (size,)),
-                ("o", o, dt, (nt, H, dv)), ("dev_err", dev_err, i32, (1,)),
-                *([] if tree_mask is None else
-                  [("tree_mask", tree_mask, i32, (nt, (q_per_seq + 31) // 32))]),
-                *([] if lse is None else [("lse", lse, torch.float32, (nt, H))]))
-    args = (cfg.ref(), q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), width, blocks,
-            seq_lens.data_ptr(), n, q_per_seq, None if tree_mask is None else tree_mask.data_ptr(),
-            w_uv.data_ptr(), workspace.data_ptr(), size, o.data_ptr(),
-            None if lse is None else lse.data_ptr(), dev_err.data_ptr(), _on(dev, stream))
-    if dev != torch._C._cuda_getDevice():
-        return _elsewhere(w, dev, lib.mla_decode_tree, *args)
-    st = lib.mla_decode_tree(*args)
+    args = (cfg.address(), q, pool, block_table, seq_lens, q_per_seq, tree_mask, w_uv, workspace, o,
+            lse, dev_err, _raw(stream))
+    st = _fast.decode_tree(*args)
     if st:
-        raise MlaError(st, w)
+        def tensors():
+            import torch
+            dt, i32, n = cfg.torch_dtype, torch.int32, _size(seq_lens, 0)
+            nt = None if n is None else n * q_per_seq
+            H, r, dv = cfg.num_heads, cfg.kv_rank, cfg.head_dim_v or cfg.head_dim
+            return (("pool", pool, dt, (None, cfg.block_size, r + cfg.rope_dim)),
+                    ("q", q, dt, (nt, H, r + cfg.rope_dim)),
+                    ("block_table", block_table, i32, (n, None)),
+                    ("seq_lens", seq_lens, i32, (n,)), ("w_uv", w_uv, dt, (H, dv, r)),
+                    ("workspace", workspace, torch.uint8, (None,)), ("o", o, dt, (nt, H, dv)),
+                    ("dev_err", dev_err, i32, (1,)),
+                    *(() if tree_mask is None else
+                      (("tree_mask", tree_mask, i32, (nt, (q_per_seq + 31) // 32)),)),
+                    *(() if lse is None else (("lse", lse, torch.float32, (nt, H)),)))
+        _finish("mla_decode_tree", st, pool, _fast.decode_tree, args, tensors)
 
 
 def commit_tree(cfg: Config, path, path_len, q_per_seq: int, block_table, pool, seq_lens,
                 seq_lens_out, dev_err, stream=None):
     """mla_commit_tree: the accepted path's rows moved together, seq_lens_out the lengths with it
     (may be seq_lens). path: (batch, width) node numbers, path_len of them count."""
-    if torch is None:
-        _import_torch()
-    w, dt, i32 = "mla_commit_tree", cfg.torch_dtype, torch.int32
-    dev = pool.get_device()
-    per = _sizes(w, "seq_lens", seq_lens, 1)
-    n, blocks, width = per[0], _sizes(w, "pool", pool, 3)[0], _sizes(
-        w, "block_table", block_table, 2)[1]
-    steps, D = _sizes(w, "path", path, 2)[1], cfg.kv_rank + cfg.rope_dim
-    if not (pool.is_cuda and pool.dtype is dt and pool.shape == (blocks, cfg.block_size, D) and
-            pool.is_contiguous() and
-            path.dtype is i32 and path.shape[0] == n and path.get_device() == dev and
-            path.is_contiguous() and
-            path_len.dtype is i32 and path_len.shape == per and path_len.get_device() == dev and
-            path_len.is_contiguous() and
-            block_table.dtype is i32 and block_table.shape[0] == n and
-            block_table.get_device() == dev and block_table.is_contiguous() and
-            seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous() and
-            seq_lens_out.dtype is i32 and seq_lens_out.shape == per and
-            seq_lens_out.get_device() == dev and seq_lens_out.is_contiguous() and
-            dev_err.dtype is i32 and dev_err.shape == (1,) and dev_err.get_device() == dev):
-        _refuse(w, dev, ("pool", pool, dt, (blocks, cfg.block_size, D)),
-                ("path", path, i32, (n, steps)), ("path_len", path_len, i32, (n,)),
-                ("block_table", block_table, i32, (n, width)), ("seq_lens", seq_lens, i32, (n,)),
-                ("seq_lens_out", seq_lens_out, i32, (n,)), ("dev_err", dev_err, i32, (1,)))
-    args = (cfg.ref(), path.data_ptr(), path_len.data_ptr(), steps, q_per_seq,
-            block_table.data_ptr(), width, pool.data_ptr(), blocks, seq_lens.data_ptr(),
-            seq_lens_out.data_ptr(), n, dev_err.data_ptr(), _on(dev, stream))
-    if dev != torch._C._cuda_getDevice():
-        return _elsewhere(w, dev, lib.mla_commit_tree, *args)
-    st = lib.mla_commit_tree(*args)
+    args = (cfg.address(), path, path_len, q_per_seq, block_table, pool, seq_lens, seq_lens_out,
+            dev_err, _raw(stream))
+    st = _fast.commit_tree(*args)
     if st:
-        raise MlaError(st, w)
+        def tensors():
+            import torch
+            i32, n = torch.int32, _size(seq_lens, 0)
+            return (("pool", pool, cfg.torch_dtype,
+                     (None, cfg.block_size, cfg.kv_rank + cfg.rope_dim)),
+                    ("path", path, i32, (n, None)), ("path_len", path_len, i32, (n,)),
+                    ("block_table", block_table, i32, (n, None)),
+                    ("seq_lens", seq_lens, i32, (n,)), ("seq_lens_out", seq_lens_out, i32, (n,)),
+                    ("dev_err", dev_err, i32, (1,)))
+        _finish("mla_commit_tree", st, pool, _fast.commit_tree, args, tensors)
 
 
 def abi_version() -> int:
