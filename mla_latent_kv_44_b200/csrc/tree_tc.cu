@@ -319,8 +319,8 @@ struct Range {
   int item, x;     // the item that holds the first chunk, and that item's first chunk
 };
 
-// Chunks of 384 items from `base` on, scanned over the CTA: returns this thread's (inclusive).
-__device__ int scan_chunks(int v, int* s_warp) {
+// This thread's value summed over the threads up to it (returned) and over all of them.
+__device__ int scan_chunks(int v, int* s_warp, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -329,73 +329,89 @@ __device__ int scan_chunks(int v, int* s_warp) {
   }
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
-  int before = 0;
+  int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w)
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s_warp[w];
+    all += s_warp[w];
+  }
+  *total = all;
   return v + before;
 }
 
+// First chunk of range q of R over C chunks (floor(q C / R), as range_start); 32-bit division, which
+// takes a fraction of the time, where it does.
+__device__ __forceinline__ int first_chunk(int q, int R, int C) {
+  if (C < 1 << 25) return (int)((uint32_t)(q * C) / (uint32_t)R);  // q <= 74
+  return range_start(q, R, C);
+}
+static_assert(kRanges <= 127, "q C below 2^32");
+
 __device__ Range plan_range(const TreeParams& p, int range, int* s_plan, int* s_len) {
   const int tid = threadIdx.x, items = p.batch * p.groups;
-  int* s_total = s_plan + 32;  // total, begin of this pass, item, x
-  if (tid < 4) s_total[tid] = 0;
-  __syncthreads();
-  auto chunks = [&](int it) {
+  int* s_found = s_plan + 32;  // item, x
+  auto rows = [&](int it) {
     if (it >= items) return 0;
     const int b = it / p.groups;
-    return (tree_length(p, b, blockIdx.x == 0 && it == b * p.groups) + kChunk - 1) / kChunk;
+    return tree_length(p, b, blockIdx.x == 0 && it == b * p.groups);
   };
   // all chunks of the call (with one pass of items, this scan is the one that places them too)
   const bool one = items <= kThreads;
-  int inc = 0, mine = 0;
+  int len = 0, mine = 0, inc = 0, C = 0;
   for (int base = 0; base < items; base += kThreads) {
-    mine = chunks(base + tid);
-    inc = scan_chunks(mine, s_plan);
-    if (tid == kThreads - 1) s_total[0] += inc;
-    __syncthreads();
+    int all;
+    if (base > 0) __syncthreads();
+    len = rows(base + tid);
+    mine = (len + kChunk - 1) / kChunk;
+    inc = scan_chunks(mine, s_plan, &all);
+    C += all;
   }
-  const int C = s_total[0];
   // A range holds two chunks at least, four where more would mean many partial results (each is
   // 256 KB): 8 tokens x 1000 rows took 32.4 us cut into single chunks, 32.0 into twos, 29.6 into
   // fours; 3 x 5 tokens of 16 heads x up to 1000 rows 28.9, 26.1 and 30.4.
   const int R = min(p.ranges, max((C + 3) / 4, min((C + 1) / 2, 32 / p.team)));
   Range w{0, 0, 0, 0};
-  // one thread block per range says whether an item that began in the range before goes on here
+  // one CTA per range says whether an item that began in the range before goes on here
   const bool writer = range < p.ranges && (blockIdx.x & 1) == 0 && (blockIdx.x >> 1) % p.team == 0;
-  if (writer && tid == 0) p.cuts[range] = make_int4(-1, 0, 0, 0);
-  __syncthreads();
   if (range < R) {
-    w.begin = range_start(range, R, C);
-    w.end = range_start(range + 1, R, C);
+    w.begin = first_chunk(range, R, C);
+    w.end = first_chunk(range + 1, R, C);
+  } else if (writer && tid == 0) {
+    p.cuts[range] = make_int4(-1, 0, 0, 0);
   }
+  int done = 0;
   for (int base = 0; base < items; base += kThreads) {
     const int it = base + tid;
+    int all = 0;
     if (!one) {
-      mine = chunks(it);
-      inc = scan_chunks(mine, s_plan);
+      __syncthreads();
+      len = rows(it);
+      mine = (len + kChunk - 1) / kChunk;
+      inc = scan_chunks(mine, s_plan, &all);
     }
-    const int x = s_total[1] + inc - mine, e = x + mine;
+    const int x = done + inc - mine, e = x + mine;
+    done += all;
     if (mine > 0 && w.begin < w.end && x <= w.begin && w.begin < e) {
-      s_total[2] = it;
-      s_total[3] = x;
-      if (writer && range > 0) {
-        const int before = range_start(range - 1, R, C);
+      s_found[0] = it;
+      s_found[1] = x;
+      if (writer) {
+        int4 cut = make_int4(-1, 0, 0, 0);
+        const int before = range > 0 ? first_chunk(range - 1, R, C) : 0;
         if (x < w.begin && x >= before) {
           const int last = starts_below(e, R, C) - 1;  // the range that holds its last chunk
-          p.cuts[range] = make_int4(it, last - (range - 1) + 1,
-                                    2 * (range - 1) + (x > before ? 1 : 0), 0);
+          cut = make_int4(it, last - (range - 1) + 1, 2 * (range - 1) + (x > before ? 1 : 0), 0);
         }
+        p.cuts[range] = cut;
       }
     }
-    __syncthreads();
-    if (tid == kThreads - 1) s_total[1] += inc;
-    __syncthreads();
   }
-  w.item = s_total[2];
-  w.x = s_total[3];
-  if (tid < kLenCache && w.item + tid < items)
-    s_len[tid] = tree_length(p, (w.item + tid) / p.groups, false);
+  if (w.begin < w.end) {  // the same in all threads
+    __syncthreads();
+    w.item = s_found[0];
+    w.x = s_found[1];
+    const int at = one ? tid - w.item : tid;  // one pass: the lengths are at hand
+    if (at >= 0 && at < kLenCache && w.item + at < items) s_len[at] = one ? len : rows(w.item + at);
+  }
   return w;
 }
 
