@@ -181,8 +181,8 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
 
   if (warp == 0) {
     // ------------------------------------------------------------------------------------ TMA
-    // the weights come from before the attention kernel, which waited for what came before it
-    // and is over when the kernel in front of this one writes
+    // The weights come from before the attention kernel, whose CTAs let the kernels behind it
+    // start only once their own wait for what came before is over.
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < kSlabs; ++k) {

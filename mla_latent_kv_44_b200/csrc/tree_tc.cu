@@ -506,9 +506,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  // the output kernel may start on SMs that are done; it waits for this grid before it reads
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   wait_prior_grid();  // the lengths, Q and the cache rows come from earlier kernels
+  // The kernels behind may start on SMs that are done; they wait for this grid before they read
+  // its results. Not before the wait above: what they read before theirs (W_UV) must be there.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int cluster = blockIdx.x >> 1;
   const int range = cluster / p.team, member = cluster - range * p.team;

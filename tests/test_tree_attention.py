@@ -311,6 +311,27 @@ def test_captured_and_replayed_with_other_lengths(mla, kernel):
     assert int(t["err"]) == 0
 
 
+@pytest.mark.parametrize("kernel", [1, 2])
+def test_weights_written_just_before_the_call(mla, kernel):
+    """W_UV, Q, the lengths and the rows come from kernels that are still queued or running."""
+    c = Case(mla, 16, 3, [300, 65], kernel=kernel)
+    t = c.device(mla)
+    names = ("w_uv", "q", "pool", "lens", "table", "mask")
+    real = {k: t[k].clone() for k in names}
+    busy = torch.randn(4096, 4096, device=D_)
+    for _ in range(5):
+        for k in names:
+            t[k].zero_()
+        c.call(mla, t)
+        for _ in range(3):
+            busy = busy @ busy * 1e-2
+        for k in reversed(names):
+            t[k].copy_(real[k])
+        c.call(mla, t)
+        t["err"].zero_()
+        c.check(t["o"], t["lse"])
+
+
 def test_many_short_sequences(mla):
     """More sequences than a range's list in shared memory holds."""
     g = torch.Generator().manual_seed(5)
