@@ -478,10 +478,14 @@ MLA_API size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t bat
  * dtype; lse (batch * T, H) float32 or NULL. A drafted row that a node's mask leaves out does not
  * reach that node's result, whatever it holds (NaN, infinities, a row never written). A node
  * that attends nothing gets o = 0 and lse = -inf, and so does every node of an empty sequence
- * (seq_lens[b] = 0); a length in (0, T) or above max_blocks * block_size does too and sets
- * MLA_DEV_BAD_LENGTH. q, pool, w_uv and o must be 16-byte aligned. The latent sums are held in
- * fp32 (in the workspace) between the attention and W_UV. Deterministic.
- * 1 <= q_per_seq <= MLA_MAX_TREE (MLA_ERR_UNSUPPORTED above).
+ * (seq_lens[b] = 0); a length in (0, T), above max_blocks * block_size or above 2^31 - 8193 does too
+ * and sets MLA_DEV_BAD_LENGTH. q, pool, w_uv and o must be 16-byte aligned. Deterministic.
+ * decode_kernel chooses as in mla_decode: the tensor-core kernel needs bf16, r = 512, d_r = 64 and
+ * a block_size that is a multiple of 64, and takes any H. Between the attention and W_UV that path
+ * keeps the latent sums as two bf16 terms (16 bits), the other in fp32.
+ * MLA_ERR_UNSUPPORTED: q_per_seq > MLA_MAX_TREE, batch * q_per_seq > 2^24 or times H > 2^28; on the
+ * tensor-core path also a pool of 2^31 rows or more, or batch * (query tiles per sequence) * (64-row
+ * pieces that a table row can hold) >= 2^31.
  */
 MLA_API mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* pool,
                                    const int32_t* block_table, int32_t max_blocks,

@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstdint>
 #include <cstring>
 
 #include "mla.h"
@@ -43,13 +44,14 @@ struct Args {
     }
     return &THPVariable_Unpack(a[i]);
   }
-  // the tensor whose device and some of whose sizes the call takes over
-  const at::Tensor* lead(int i, int dims) {
+  // the tensor whose device and some of whose sizes the call takes over, as 32-bit numbers
+  const at::Tensor* lead(int i, int dims, int64_t most = INT32_MAX) {
     const at::Tensor* t = tensor(i);
     if (!t || !t->is_cuda() || t->dim() != dims) {
       ok = false;
       return nullptr;
     }
+    for (const int64_t n : t->sizes()) ok = ok && n <= most;
     if (dev < 0) dev = t->get_device();
     return t;
   }
@@ -65,7 +67,11 @@ struct Args {
     return static_cast<T*>(t->data_ptr());
   }
   const mla_config* config(int i) { return static_cast<const mla_config*>(PyLong_AsVoidPtr(a[i])); }
-  int number(int i) { return static_cast<int>(PyLong_AsLong(a[i])); }
+  int number(int i) {
+    const long v = PyLong_AsLong(a[i]);
+    if (v != static_cast<int>(v)) ok = false;
+    return static_cast<int>(v);
+  }
   void* stream(int i) {
     if (a[i] == Py_None) return c10::cuda::getCurrentCUDAStream(dev).stream();
     return PyLong_AsVoidPtr(a[i]);
@@ -160,7 +166,7 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Args g{a};
   const mla_config* c = g.config(0);
   const at::Tensor *pool = g.lead(2, 3), *table = g.lead(3, 2), *lens = g.lead(4, 1),
-                   *ws = g.lead(8, 1);
+                   *ws = g.lead(8, 1, INT64_MAX);
   const int64_t T = g.number(5);
   if (!g.ok || T < 0) return status(kRefused);
   const auto dt = dtype_of(c);

@@ -643,6 +643,13 @@ mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* poo
   const TreeLayout L = tree_layout(c, batch, q_per_seq);
   if (workspace_bytes < L.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
   if (c.decode_kernel == MLA_DECODE_TENSOR && !L.tc) return MLA_ERR_UNSUPPORTED;
+  if (L.tc) {
+    // 32-bit on this path: rows of the pool (a TMA coordinate) and the call's 64-row pieces
+    const int64_t rows = (int64_t)num_blocks * c.block_size;
+    const int64_t held = std::min<int64_t>((int64_t)max_blocks * c.block_size, kTreeMaxLen);
+    if (rows > INT32_MAX || (int64_t)batch * L.groups * ((held + 63) / 64) > INT32_MAX)
+      return MLA_ERR_UNSUPPORTED;
+  }
   char* ws = (char*)workspace;
   TreeParams p{};
   p.q = q;

@@ -33,12 +33,15 @@ struct TreeParams {
                // k > 0 is in slot 2 * (z / 2 + k)
 };
 
+// Longest sequence: row numbers rounded up to whole tiles stay below 2^31.
+constexpr int kTreeMaxLen = 0x7fffffff - 8192;
+
 // Rows of sequence b, its drafted ones included: 0 for an empty place of the batch and for a
 // length that cannot be (fewer rows than drafted tokens, or more than the table holds), which
 // `report` flags.
 __device__ __forceinline__ int tree_length(const TreeParams& p, int b, bool report) {
   const int len = p.seq_lens[b];
-  if (len >= p.T && (int64_t)len <= (int64_t)p.max_blocks * p.bs) return len;
+  if (len >= p.T && len <= kTreeMaxLen && (int64_t)len <= (int64_t)p.max_blocks * p.bs) return len;
   if (len != 0 && report) set_error(p.err, MLA_DEV_BAD_LENGTH);
   return 0;
 }

@@ -105,6 +105,19 @@ def test_decode_tree_refusals(mla):
     assert _tree(mla, c, batch=0) == mla.MLA_OK
 
 
+def test_decode_tree_refuses_what_32_bits_cannot_number(mla):
+    """The tensor-core kernel's pool rows and 64-row pieces; the CUDA cores' are 64-bit."""
+    c, size = _ref(mla), 1 << 40
+    assert _tree(mla, c, blocks=1 << 25, size=size) == mla.MLA_ERR_UNSUPPORTED  # 2^31 rows
+    assert _tree(mla, c, batch=1 << 16, width=1 << 15, size=size) == mla.MLA_ERR_UNSUPPORTED
+    assert _tree(mla, c, T=1, batch=1 << 24, width=128, size=size) == mla.MLA_ERR_UNSUPPORTED
+    # heads and tokens: 2^28 query rows at most
+    assert _tree(mla, c, T=256, batch=(1 << 13) + 1, size=size) == mla.MLA_ERR_UNSUPPORTED
+    # one below the limits: refused for its workspace only
+    for kw in (dict(blocks=(1 << 25) - 1), dict(batch=1 << 16, width=(1 << 15) - 1)):
+        assert _tree(mla, c, size=0, **kw) == mla.MLA_ERR_WORKSPACE, kw
+
+
 def test_commit_tree_refusals(mla):
     c, f = _ref(mla), mla.lib.mla_commit_tree
     good = [A, A, 4, 4, A, 4, A, 8, A, A, 2, A]
@@ -156,6 +169,22 @@ def test_binding_names_the_wrong_tensor(mla):
                        ((parents, lens.cpu(), mask, pos, err), "seq_lens")):
         with pytest.raises(mla.MlaError, match=name):
             mla.tree_masks(*args)
+
+
+@GPU
+def test_binding_takes_no_number_modulo_2_to_32(mla):
+    i32, d = torch.int32, "cuda"
+    cfg = mla.Config(16, 64, 64, 32, 64, dtype="f32")
+    pool, table = torch.zeros(2, 64, 96, device=d), torch.zeros(1, 1, dtype=i32, device=d)
+    path, one = torch.zeros(1, 4, dtype=i32, device=d), torch.ones(1, dtype=i32, device=d)
+    lens, out = torch.full((1,), 9, dtype=i32, device=d), torch.full((1,), -7, dtype=i32, device=d)
+    for T in (2 ** 32 + 4, -2 ** 32 + 4):
+        with pytest.raises(mla.MlaError):
+            mla.commit_tree(cfg, path, one, T, table, pool, lens, out, torch.zeros_like(one))
+    with pytest.raises((TypeError, OverflowError)):
+        mla.commit_tree(cfg, path, one, 4.0, table, pool, lens, out, torch.zeros_like(one))
+    torch.cuda.synchronize()
+    assert int(out) == -7
 
 
 # --------------------------------------------------------------------------------- build_tables
