@@ -683,9 +683,7 @@ mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* poo
     p.latent_lo = (__nv_bfloat16*)(ws + L.latent_lo);
     p.cuts = (int4*)(ws + L.cuts);
     cudaError_t e = launch_tree_tc(p, (cudaStream_t)stream);
-    if (e == cudaSuccess) e = launch_tree_merge(p, (cudaStream_t)stream);
-    if (e == cudaSuccess)
-      e = launch_tree_out(p, w_uv, c.head_dim_v, o, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = launch_tree_out(p, w_uv, c.head_dim_v, o, (cudaStream_t)stream);
     return from_cuda(e);
   }
   // no more ranges than 64-row pieces of the longest sequence the table can hold

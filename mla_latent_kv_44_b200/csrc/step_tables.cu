@@ -9,9 +9,11 @@
 // map. Three phases are separated by cluster barriers, because each reads what the one before
 // wrote in global memory: blocks given back are pushed on the free stack; blocks taken come off
 // its top into the table; slots are read from the table. Everything is placed by prefix sums,
-// none by atomics: the same inputs give the same tables.
-// What bounds it: latency (a chain of dependent loads and two barriers) at decode sizes; 16 B
-// written per token for prompts.
+// none by atomics: the same inputs give the same tables. A block moved is a thread's, which finds
+// its request by a search in the prefix sums (a warp per request: 7.0 us instead of 4.0 for 64
+// requests, 14.6 instead of 9.8 for 128 with 32 prompts among them).
+// What bounds it: latency (a chain of dependent loads and two barriers) at decode sizes, 4.0 us for
+// 64 requests; for prompts also the 16 B written per token (131,072 tokens: 9.8 us, 0.21 TB/s).
 #include <algorithm>
 
 #include "tree.cuh"
@@ -19,7 +21,7 @@
 namespace mla {
 namespace {
 
-constexpr int kTabThreads = 1024;
+constexpr int kTabThreads = 1024, kTabSmall = 512;
 constexpr int kTabMaxCtas = 8;  // portable cluster size
 
 struct TableParams {
@@ -35,9 +37,13 @@ struct TableParams {
   bool map_apart;  // the slot map is the second kernel's
 };
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
+__device__ __forceinline__ void cluster_barrier(int ctas) {
+  if (ctas == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+  }
 }
 
 // Token counts saturate here: above any max_tokens (at most 2^26), below overflow. A request's
@@ -45,6 +51,7 @@ __device__ __forceinline__ void cluster_barrier() {
 constexpr int kTokenSat = 1 << 29, kTokenCap = 1 << 28;
 
 // Inclusive scan of three ints over the CTA (a saturating); s holds 3 x 32 ints.
+template <int NT>
 __device__ void scan3(int* s, int& a, int& b, int& c) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -64,7 +71,7 @@ __device__ void scan3(int* s, int& a, int& b, int& c) {
   }
   __syncthreads();
   if (warp < 3) {
-    int v = s[32 * warp + lane];
+    int v = lane < NT / 32 ? s[32 * warp + lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -99,6 +106,17 @@ __device__ __forceinline__ Request load_request(const TableParams& p, int b) {
   return q;
 }
 
+// The last request with off <= i (offsets rise; off[0] <= i < off[batch]): the one that holds i.
+__device__ __forceinline__ int holder(const int* off, int batch, int i) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 // Tokens i0 .. i0 + per - 1: one search and one division for all of them while they stay in a
 // request. cu: offsets of the requests; start_of(b): its first new row, or -1 - row when it was not
 // served; `real` tokens in all.
@@ -112,13 +130,7 @@ __device__ __forceinline__ void map_tokens(const TableParams& p, const int* cu, 
   if (p.vec && i0 + 4 <= real) {
     // four tokens of one request, as most are: everything follows from the first (a warp whose
     // lanes part here runs both ways, so a block's end inside the four stays on this one)
-    int lo = 0, hi = p.batch - 1;
-    const int i = (int)i0;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu[mid] <= i) lo = mid;
-      else hi = mid - 1;
-    }
+    const int i = (int)i0, lo = holder(cu, p.batch, i);
     const int start = start_of(lo);
     if (cu[lo + 1] - i >= 4 && start >= 0 && p.bs >= 4) {
       const int row0 = start + i - cu[lo], at0 = row0 / p.bs, in0 = row0 - at0 * p.bs;
@@ -147,18 +159,12 @@ __device__ __forceinline__ void map_tokens(const TableParams& p, const int* cu, 
     if (u >= per || i >= real) continue;
     bool look = false;
     if (left == 0) {  // the request that holds token i
-      int lo = 0, hi = p.batch - 1;  // the last one with cu <= i
       if (b >= 0) {
-        lo = b + 1;
-        while (cu[lo + 1] <= i) ++lo;
+        ++b;
+        while (cu[b + 1] <= i) ++b;
       } else {
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (cu[mid] <= i) lo = mid;
-          else hi = mid - 1;
-        }
+        b = holder(cu, p.batch, i);
       }
-      b = lo;
       left = cu[b + 1] - i;
       const int from = start_of(b);
       served = from >= 0;
@@ -201,12 +207,13 @@ __device__ __forceinline__ void map_tokens(const TableParams& p, const int* cu, 
   }
 }
 
-__global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TableParams p) {
+template <int NT>
+__global__ void __launch_bounds__(NT) build_tables_kernel(const TableParams p) {
   extern __shared__ int s_dyn[];
-  int* s_cu = s_dyn;                   // batch + 1: new tokens before request b
-  int* s_back = s_cu + p.batch + 1;    // batch: blocks given back by earlier requests
-  int* s_take = s_back + p.batch;      // batch: blocks due to earlier requests
-  int* s_start = s_take + p.batch;     // batch: first new row, or -1 - row when not served
+  int* s_cu = s_dyn;                    // batch + 1: new tokens before request b
+  int* s_back = s_cu + p.batch + 1;     // batch + 1: blocks given back by earlier requests
+  int* s_take = s_back + p.batch + 1;   // batch + 1: blocks due to earlier requests
+  int* s_start = s_take + p.batch + 1;  // batch: first new row, or -1 - row when not served
   __shared__ int s_scan[96], s_carry[3];
   const int tid = threadIdx.x, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -215,8 +222,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablePa
   // requests, scanned by every CTA
   const int count = p.free_count[0];
   if (tid < 3) s_carry[tid] = 0;
-  __syncthreads();
-  for (int base = 0; base < p.batch; base += kTabThreads) {
+  for (int base = 0; base < p.batch; base += NT) {
     const int b = base + tid;
     int n = 0, back = 0, take = 0;
     if (b < p.batch) {
@@ -228,14 +234,14 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablePa
       s_start[b] = q.ok ? q.len - q.fresh : 0;
     }
     int a0 = n, a1 = back, a2 = take;
-    scan3(s_scan, a0, a1, a2);
+    scan3<NT>(s_scan, a0, a1, a2);
     if (b < p.batch) {
       s_cu[b] = min(s_carry[0] + a0, kTokenSat) - n;
       s_back[b] = s_carry[1] + a1 - back;
       s_take[b] = s_carry[2] + a2 - take;
     }
     __syncthreads();
-    if (tid == kTabThreads - 1) {
+    if (tid == NT - 1) {
       s_carry[0] = min(s_carry[0] + a0, kTokenSat);
       s_carry[1] += a1;
       s_carry[2] += a2;
@@ -243,63 +249,72 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablePa
     __syncthreads();
   }
   const int tokens = s_carry[0], backs = s_carry[1], takes = s_carry[2];
-  if (tid == 0) s_cu[p.batch] = tokens;
+  if (tid == 0) {
+    s_cu[p.batch] = tokens;
+    s_back[p.batch] = backs;
+    s_take[p.batch] = takes;
+  }
+  __syncthreads();
   // a stack that cannot be one: no block moves
   const bool stack_ok = count >= 0 && count <= p.num_blocks && backs <= p.num_blocks - count;
   if (!stack_ok && cta == 0 && tid == 0) set_error(p.err, MLA_DEV_BAD_LENGTH);
   const int stack = stack_ok ? count + backs : 0;
 
-  // blocks given back, in (request, index) order; a warp per request
-  const int gwarp = cta * (kTabThreads / 32) + (tid >> 5), gwarps = ctas * (kTabThreads / 32);
-  if (stack_ok && backs > 0) {
-    for (int b = gwarp; b < p.batch; b += gwarps) {
-      const Request q = load_request(p, b);
-      for (int i = q.want + lane; i < q.held; i += 32)
-        p.free_blocks[count + s_back[b] + i - q.want] = p.table[(size_t)b * p.max_blocks + i];
-    }
-  }
-  cluster_barrier();
-
-  // blocks taken: the k-th off the top; a request whose share runs past the bottom gets none
-  if (takes > 0) {
-    for (int b = gwarp; b < p.batch; b += gwarps) {
-      const Request q = load_request(p, b);
-      const int take = q.want - q.held;
-      if (take <= 0 || s_take[b] > stack - take) continue;
-      for (int i = lane; i < take; i += 32) {
-        const int blk = __ldcg(p.free_blocks + (stack - 1 - s_take[b] - i));
-        if (blk < 0 || blk >= p.num_blocks) set_error(p.err, MLA_DEV_OOB_BLOCK);
-        p.table[(size_t)b * p.max_blocks + q.held + i] = blk;
+  // blocks given back, in (request, index) order: a thread per block, whoever's it was
+  const int gtid = cta * NT + tid, threads = ctas * NT;
+  if (backs > 0) {
+    if (stack_ok) {
+      for (int i = gtid; i < backs; i += threads) {
+        const int b = holder(s_back, p.batch, i), kept = p.held[b] - (s_back[b + 1] - s_back[b]);
+        p.free_blocks[count + i] = p.table[(size_t)b * p.max_blocks + kept + i - s_back[b]];
       }
     }
+    cluster_barrier(ctas);
   }
-  __syncthreads();
-  for (int b = tid; b < p.batch; b += kTabThreads) {
-    const Request q = load_request(p, b);
-    const int take = q.want - q.held;
-    if (take > 0 && s_take[b] > stack - take) {
+
+  // blocks taken: the k-th off the top; a request whose share runs past the bottom gets none
+  const int most = min(takes, stack);
+  for (int i0 = gtid; i0 < most; i0 += 4 * threads) {
+    int blk[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * threads;
+      blk[u] = i < most ? __ldcg(p.free_blocks + (stack - 1 - i)) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * threads;
+      if (i >= most) break;
+      const int b = holder(s_take, p.batch, i);
+      if (s_take[b + 1] > stack) break;  // nor any later one
+      if (blk[u] < 0 || blk[u] >= p.num_blocks) set_error(p.err, MLA_DEV_OOB_BLOCK);
+      p.table[(size_t)b * p.max_blocks + p.held[b] + i - s_take[b]] = blk[u];
+    }
+  }
+  for (int b = tid; b < p.batch; b += NT) {
+    if (s_take[b + 1] > max(s_take[b], stack)) {
       s_start[b] = -1 - s_start[b];
       if (cta == 0) set_error(p.err, MLA_DEV_NO_BLOCKS);
     }
   }
-  cluster_barrier();  // the table is complete, and held and free_count are read
+  cluster_barrier(ctas);  // the table is complete, and held and free_count are read
 
   // counts
   if (cta == 0) {
     int last = 0;  // blocks taken by the requests that were served
-    for (int b = tid; b < p.batch; b += kTabThreads) {
-      const Request q = load_request(p, b);
-      const int take = q.want - q.held;
+    for (int b = tid; b < p.batch; b += NT) {
       const bool served = s_start[b] >= 0;
-      if (take > 0 && served) last = max(last, s_take[b] + take);
-      p.held_out[b] = (take > 0 ? served : stack_ok) ? q.want : q.held;
+      const int take = served ? s_take[b + 1] - s_take[b] : 0;
+      if (take > 0) last = max(last, s_take[b + 1]);
+      p.held_out[b] = p.held[b] + take -
+                      (stack_ok ? s_back[b + 1] - s_back[b] : 0);
       p.cu[b] = min(s_cu[b], p.max_tokens);
     }
     last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) s_scan[tid >> 5] = last;
     __syncthreads();
     if (tid < 32) {
-      last = __reduce_max_sync(0xffffffffu, s_scan[tid]);
+      last = __reduce_max_sync(0xffffffffu, tid < NT / 32 ? s_scan[tid] : 0);
       if (tid == 0) {
         p.free_count_out[0] = stack_ok ? stack - last : count;
         p.cu[p.batch] = min(tokens, p.max_tokens);
@@ -311,8 +326,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablePa
   // tokens
   if (p.map_apart) return;
   const int per = p.per_thread, real = min(tokens, p.max_tokens);
-  for (int64_t i0 = (int64_t)(cta * kTabThreads + tid) * per; i0 < p.max_tokens;
-       i0 += (int64_t)ctas * kTabThreads * per)
+  for (int64_t i0 = (int64_t)gtid * per; i0 < p.max_tokens; i0 += (int64_t)threads * per)
     map_tokens(p, s_cu, [&](int b) { return s_start[b]; }, i0, per, real);
 }
 
@@ -347,24 +361,28 @@ cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens
   // one token per thread while that takes one pass of one CTA, else four; and lists that take
   // the cluster more than one pass go to a kernel of their own (131,072 tokens: 17.0 us in the
   // cluster alone)
-  const int per = max_tokens <= kTabThreads ? 1 : 4;
+  const int per = max_tokens <= kTabSmall ? 1 : 4;
   const bool vec = per == 4 && (((uintptr_t)seq_idx | (uintptr_t)pos | (uintptr_t)slots) & 15) == 0;
   const bool apart = max_tokens > kTabMaxCtas * kTabThreads * 4;
   TableParams p{seq_lens, new_lens, held,  table, free_blocks, free_count, held_out,
                 free_count_out, cu, seq_idx, pos, slots, err, batch, max_blocks, num_blocks, bs,
                 max_tokens, per, vec, apart};
-  const size_t smem = sizeof(int) * (4 * (size_t)batch + 1);
+  const size_t smem = sizeof(int) * (4 * (size_t)batch + 3);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e =
+        cudaFuncSetAttribute(build_tables_kernel<kTabThreads>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  // one CTA while a pass of it covers the tokens and the requests, else a full cluster
+  // one CTA while a pass of it covers the tokens and the requests, else a full cluster. A CTA of 512
+  // threads where that is enough: 64 requests take 4.0 us (1024 threads 4.5, 256 4.4), 128 with 32
+  // prompts 9.8 (10.2, 13.1).
+  const bool small = (apart || max_tokens <= 4 * kTabSmall) && batch <= kTabSmall;
   const int ctas =
-      (apart || max_tokens <= kTabThreads) && batch <= kTabThreads ? 1 : kTabMaxCtas;
+      (apart || max_tokens <= 4 * kTabThreads) && batch <= kTabThreads ? 1 : kTabMaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTabThreads);
+  cfg.blockDim = dim3(small ? kTabSmall : kTabThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -376,7 +394,8 @@ cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
+  cudaError_t e = small ? cudaLaunchKernelEx(&cfg, build_tables_kernel<kTabSmall>, p)
+                        : cudaLaunchKernelEx(&cfg, build_tables_kernel<kTabThreads>, p);
   if (e == cudaSuccess && apart)
     e = launch_pdl(slot_map_kernel, dim3((max_tokens + 4 * kMapThreads - 1) / (4 * kMapThreads)),
                    dim3(kMapThreads), sizeof(int) * ((size_t)batch + 1), st, p);

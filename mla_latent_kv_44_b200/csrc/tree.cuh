@@ -59,7 +59,6 @@ bool tree_tc_supported(const mla_config& c);
 void tree_team(int tiles, int* team, int* ranges);
 cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t st);
 // tree_out.cu
-cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t st);
 cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void* o,
                             cudaStream_t st);
 

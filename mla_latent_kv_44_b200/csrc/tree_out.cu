@@ -7,8 +7,9 @@
 // both bf16 terms of each value (hi = bf16(x), lo = bf16(x - hi); one term alone would add as large
 // an error as the rounding of o). M = 128 (dims), N = the tile's tokens: 8 MMAs per stage into
 // one of two tensor-memory accumulators; the epilogue of a tile of tokens runs while the next
-// one's products do. (With 32 tokens per tile the MMAs' issue took 146 us for 1024 tokens.) What
-// bounds it: the weights' bytes for few tokens, the latent rows' for many.
+// one's products do. (With 32 tokens per tile the MMAs' issue took 146 us for 1024 tokens.) With few
+// tokens the CTA merges its head's partial results itself, into the operand's layout. What bounds
+// it: latency and the weights' bytes for few tokens, the latent rows' for many.
 #include <atomic>
 
 #include "tc_ptx.cuh"
@@ -24,6 +25,7 @@ constexpr int kSlabs = kR / 64;
 constexpr int kDims = 128;                         // rows of W_UV per CTA
 constexpr int kTok = 128;                          // tokens per tile
 constexpr int kRing = 3;
+constexpr int kMergeTok = 16;                      // most tokens that are merged here
 constexpr int kThreads = 256;
 constexpr int kWSlab = kDims * 128, kTerm = kTok * 128;
 constexpr int kStage = 2 * kTerm;                  // hi and lo: 32 KB
@@ -40,6 +42,7 @@ enum Bar {
 };
 constexpr int kSmem = kBars + kNumBars * 8 + 16 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+static_assert(kSlabs * 2 * kMergeTok * 128 <= kRing * kStage, "the merged operand's place");
 constexpr unsigned long long kTimeoutNs = 1000000000ull, kSettleNs = 20000000ull;
 
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
@@ -78,20 +81,10 @@ __device__ __forceinline__ void mma1(uint32_t d, uint32_t a_lo, uint32_t b_lo, u
       : "memory");
 }
 
-// ---- merge: one warp per query row of an item in the list of cuts -------------------------
-constexpr int kMergeWarps = 8;
-
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_parts_kernel(const TreeParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  wait_prior_grid();
-  constexpr int kPer = kTreeTile / kMergeWarps;  // CTAs per tile of query rows
-  const int lane = threadIdx.x & 31, m = blockIdx.x % kPer * kMergeWarps + (threadIdx.x >> 5);
-  const int member = blockIdx.x / kPer % p.team;
-  const int4 cut = p.cuts[blockIdx.x / (kPer * p.team)];
-  if (cut.x < 0) return;
-  const int b = cut.x / p.groups, mt = (cut.x - b * p.groups) * p.team + member;
-  const int row = mt * kTreeTile + m;
-  if (row >= p.T * p.H) return;
+// ---- merge of a cut item's pieces for one query row, by a warp ---------------------------------
+// m: row of the tile. acc: lane's dims 128 u + 4 lane .. + 3, divided by the sum; returns the lse.
+__device__ __forceinline__ float merge_row(const TreeParams& p, const int4 cut, int member, int m,
+                                           int lane, float4 (&acc)[4]) {
   auto at = [&](int k) -> size_t {  // the k-th piece's result
     const int slot = k == 0 ? cut.z : 2 * (cut.z / 2 + k);
     return ((size_t)slot * p.team + member) * kTreeTile + m;
@@ -105,45 +98,72 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_parts_kernel(cons
   }
   mx = warp_max(mx);
   const bool empty = mx == -INFINITY && !__any_sync(0xffffffffu, nan);
-  float4 acc[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (empty) return -INFINITY;
   float z = 0.f;
-  if (!empty) {
 #pragma unroll 4
-    for (int k = 0; k < cut.y; ++k) {
-      const size_t part = at(k);
-      const float x = p.part_lse[part];
-      const float e = x == -INFINITY ? 0.f : expf(x - mx);
-      z += e;
-      const float4* src = (const float4*)(p.part_o + part * kR) + lane;
+  for (int k = 0; k < cut.y; ++k) {
+    const size_t part = at(k);
+    const float x = p.part_lse[part];
+    const float e = x == -INFINITY ? 0.f : expf(x - mx);
+    z += e;
+    const float4* src = (const float4*)(p.part_o + part * kR) + lane;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float4 v = __ldcs(src + 32 * u);
-        acc[u].x = fmaf(e, v.x, acc[u].x);
-        acc[u].y = fmaf(e, v.y, acc[u].y);
-        acc[u].z = fmaf(e, v.z, acc[u].z);
-        acc[u].w = fmaf(e, v.w, acc[u].w);
-      }
+    for (int u = 0; u < 4; ++u) {
+      const float4 v = __ldcs(src + 32 * u);
+      acc[u].x = fmaf(e, v.x, acc[u].x);
+      acc[u].y = fmaf(e, v.y, acc[u].y);
+      acc[u].z = fmaf(e, v.z, acc[u].z);
+      acc[u].w = fmaf(e, v.w, acc[u].w);
     }
   }
-  const float inv = empty ? 0.f : 1.f / z;
+  const float inv = 1.f / z;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    acc[u].x *= inv;
+    acc[u].y *= inv;
+    acc[u].z *= inv;
+    acc[u].w *= inv;
+  }
+  return mx + logf(z);
+}
+// the two bf16 terms of four values
+__device__ __forceinline__ void split4(const float4 v, uint2* hi, uint2* lo) {
+  const uint2 h = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  *hi = h;
+  *lo = make_uint2(
+      pack_bf16(v.x - __uint_as_float(h.x << 16), v.y - __uint_as_float(h.x & 0xffff0000u)),
+      pack_bf16(v.z - __uint_as_float(h.y << 16), v.w - __uint_as_float(h.y & 0xffff0000u)));
+}
+
+// One warp per query row of an item in the list of cuts.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_parts_kernel(const TreeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_prior_grid();
+  constexpr int kPer = kTreeTile / kMergeWarps;  // CTAs per tile of query rows
+  const int lane = threadIdx.x & 31, m = blockIdx.x % kPer * kMergeWarps + (threadIdx.x >> 5);
+  const int member = blockIdx.x / kPer % p.team;
+  const int4 cut = p.cuts[blockIdx.x / (kPer * p.team)];
+  if (cut.x < 0) return;
+  const int b = cut.x / p.groups, mt = (cut.x - b * p.groups) * p.team + member;
+  const int row = mt * kTreeTile + m;
+  if (row >= p.T * p.H) return;
+  float4 acc[4];
+  const float lse = merge_row(p, cut, member, m, lane, acc);
   const size_t out = (size_t)b * p.T * p.H + row;
   uint2* hi = (uint2*)(p.latent_hi + out * kR) + lane;
   uint2* lo = (uint2*)(p.latent_lo + out * kR) + lane;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const float v[4] = {acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv};
-    const uint2 h = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    hi[32 * u] = h;
-    lo[32 * u] = make_uint2(pack_bf16(v[0] - __uint_as_float(h.x << 16),
-                                      v[1] - __uint_as_float(h.x & 0xffff0000u)),
-                            pack_bf16(v[2] - __uint_as_float(h.y << 16),
-                                      v[3] - __uint_as_float(h.y & 0xffff0000u)));
-  }
-  if (lane == 0 && p.lse) p.lse[out] = empty ? -INFINITY : mx + logf(z);
+  for (int u = 0; u < 4; ++u) split4(acc[u], hi + 32 * u, lo + 32 * u);
+  if (lane == 0 && p.lse) p.lse[out] = lse;
 }
 
+// kMerge: few tokens, whose cut items this kernel merges itself, straight into the layout of the
+// MMA's operand; there is no merge kernel then.
+template <bool kMerge>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_hi,
                 const __grid_constant__ CUtensorMap tm_lo, const TreeParams p, int dv, int splits,
@@ -179,7 +199,85 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  if (warp == 0) {
+  const uint32_t w_lo = desc_lo(s_base + kW, 16), b_lo = desc_lo(s_base + kB, 16);
+  const int pad = kMerge ? (p.BT + 15) / 16 * 16 : 0;  // tokens of an operand tile
+  if (kMerge) {
+    if (warp == 0 && elect_one()) {
+#pragma unroll
+      for (int k = 0; k < kSlabs; ++k) {
+        mbar_expect_tx(bar(kWFull + k), kWSlab);
+        tma_load(s_base + kW + k * kWSlab, &tm_w, bar(kWFull + k), 64 * k, h * dv + dim0);
+      }
+    }
+    __syncwarp();
+    wait_prior_grid();
+    int4 cuts[3];  // the list, three entries per lane
+    static_assert(kRanges <= 96, "entries held");
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      cuts[i] = lane + 32 * i < p.ranges ? p.cuts[lane + 32 * i] : make_int4(-1, 0, 0, 0);
+    for (int n = warp; n < p.BT; n += kThreads / 32) {
+      const int b = n / p.T, row = (n - b * p.T) * p.H + h;
+      const int mt = row / kTreeTile, m = row - mt * kTreeTile;
+      const int group = mt / p.team, member = mt - group * p.team, item = b * p.groups + group;
+      int4 cut = make_int4(-1, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t found = __ballot_sync(0xffffffffu, cuts[i].x == item);
+        if (found) {
+          const int from = __ffs(found) - 1;
+          cut.x = item;
+          cut.y = __shfl_sync(0xffffffffu, cuts[i].y, from);
+          cut.z = __shfl_sync(0xffffffffu, cuts[i].z, from);
+        }
+      }
+      uint2 hi[4], lo_[4];
+      if (cut.x >= 0) {
+        float4 acc[4];
+        const float lse = merge_row(p, cut, member, m, lane, acc);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) split4(acc[u], &hi[u], &lo_[u]);
+        if (lane == 0 && dim0 == 0 && p.lse) p.lse[(size_t)n * p.H + h] = lse;
+      } else {
+        // finished by the attention (or of an empty sequence, whose outputs are zeros whatever
+        // is here)
+        const size_t at = ((size_t)n * p.H + h) * kR;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          hi[u] = *((const uint2*)(p.latent_hi + at) + lane + 32 * u);
+          lo_[u] = *((const uint2*)(p.latent_lo + at) + lane + 32 * u);
+        }
+      }
+      // slab 2 u + lane / 16 of 64 dims, term, token: 128-byte rows swizzled by row % 8
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint8_t* at = smem + kB + (2 * (2 * u + (lane >> 4)) * pad + n) * 128 +
+                      16 * (((lane & 15) >> 1) ^ (n & 7)) + 8 * (lane & 1);
+        *(uint2*)at = hi[u];
+        *(uint2*)(at + pad * 128) = lo_[u];
+      }
+    }
+    fence_proxy_async();
+    __syncthreads();
+    if (warp == 1) {
+      const uint32_t id = idesc(kDims, pad, 0);
+      bool ok = true;
+      for (int k = 0; k < kSlabs && ok; ++k) {
+        ok = wait(bar(kWFull + k), 0, p.err, abort);
+        if (!ok) break;
+        tc_after();
+        if (elect_one()) {
+          const uint32_t a = w_lo + k * (kWSlab >> 4), b = b_lo + k * (2 * pad * 128 >> 4);
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma1(tmem, a + 2 * (s & 3), b + (s >> 2) * (pad * 128 >> 4) + 2 * (s & 3), id,
+                 (k > 0 || s > 0) ? 1u : 0u);
+          if (k == kSlabs - 1) tc_commit(bar(kDFull));
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 0) {
     // ------------------------------------------------------------------------------------ TMA
     // The weights come from before the attention kernel, whose CTAs let the kernels behind it
     // start only once their own wait for what came before is over.
@@ -219,7 +317,6 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     int stage = 0;
     uint32_t round = 0;
     bool ok = true;
-    const uint32_t w_lo = desc_lo(s_base + kW, 16), b_lo = desc_lo(s_base + kB, 16);
     for (int i = 0; i < hi - lo && ok; ++i) {
       const int tokens = min(kTok, p.BT - (lo + i) * kTok);
       const uint32_t id = idesc(kDims, (tokens + 15) / 16 * 16, 0);
@@ -246,11 +343,12 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
         }
       }
     }
-  } else if (warp >= 4) {
+  }
+  if (warp >= 4) {
     // ------------------------------------------------------------------------------- epilogue
     // A thread holds one dim of the tile's tokens; neighbours swap, so that each stores two dims
     // of every second token.
-    wait_prior_grid();
+    if (!kMerge) wait_prior_grid();
     const int dim = dim0 + 32 * (warp & 3) + lane;
     const bool even = (lane & 1) == 0;
     for (int i = 0; i < hi - lo; ++i) {
@@ -318,12 +416,6 @@ bool latent_map(CUtensorMap* m, const void* base, int n, int H) {
 
 }  // namespace
 
-cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t st) {
-  const int ctas = p.ranges * p.team * (kTreeTile / kMergeWarps);
-  return launch_pdl(tree_merge_parts_kernel, dim3((unsigned)ctas), dim3(kMergeWarps * 32), 0, st,
-                    p);
-}
-
 cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void* o,
                             cudaStream_t st) {
   CUtensorMap w, hi, lo;
@@ -336,15 +428,28 @@ cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void*
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
   if (!bit || !(attr_devices.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(tree_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
+    for (auto k : {tree_out_kernel<false>, tree_out_kernel<true>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+    }
     attr_devices.fetch_or(bit, std::memory_order_acq_rel);
   }
   // one CTA per 128 rows of W_UV; its tokens are split where that leaves SMs idle
   const int ctas = p.H * ((dv + kDims - 1) / kDims), tiles = (p.BT + kTok - 1) / kTok;
+  // Up to 16 tokens the merge is done here: 1 x 8 tokens of 128 heads over 1000 rows take 22.9 us
+  // against 27.9 with a merge kernel in between, 32768 rows 70.3 against 76.7, 4 x 4 over 1000 26.3
+  // against 28.8, 3 x 5 of 16 heads 24.2 against 25.6; 8 x 4 37.8 against 37.1, 12 x 4 of 16 heads
+  // over 4096 rows 51 against 43 (a CTA reads all partial results of its head).
+  if (p.BT <= kMergeTok)
+    return launch_pdl(tree_out_kernel<true>, dim3((unsigned)ctas), dim3(kThreads), kSmem, st, w, hi,
+                      lo, p, dv, 1, (__nv_bfloat16*)o);
+  e = launch_pdl(tree_merge_parts_kernel,
+                 dim3((unsigned)(p.ranges * p.team * (kTreeTile / kMergeWarps))),
+                 dim3(kMergeWarps * 32), 0, st, p);
+  if (e != cudaSuccess) return e;
   const int splits = ctas >= 148 ? 1 : (148 / ctas < tiles ? 148 / ctas : tiles);
-  return launch_pdl(tree_out_kernel, dim3((unsigned)(ctas * splits)), dim3(kThreads), kSmem, st,
-                    w, hi, lo, p, dv, splits, (__nv_bfloat16*)o);
+  return launch_pdl(tree_out_kernel<false>, dim3((unsigned)(ctas * splits)), dim3(kThreads), kSmem,
+                    st, w, hi, lo, p, dv, splits, (__nv_bfloat16*)o);
 }
 
 }  // namespace mla
