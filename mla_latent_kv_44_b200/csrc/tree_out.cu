@@ -25,6 +25,7 @@ constexpr int kSlabs = kR / 64;
 constexpr int kDims = 128;                         // rows of W_UV per CTA
 constexpr int kTok = 128;                          // tokens per tile
 constexpr int kRing = 3;
+constexpr int kMergeThreads = 512;                 // of the kernel that merges them
 constexpr int kMergeTok = 16;                      // most tokens that are merged here
 constexpr int kThreads = 256;
 constexpr int kWSlab = kDims * 128, kTerm = kTok * 128;
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_parts_kernel(cons
 // kMerge: few tokens, whose cut items this kernel merges itself, straight into the layout of the
 // MMA's operand; there is no merge kernel then.
 template <bool kMerge>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kMerge ? kMergeThreads : kThreads, 1)
 tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_hi,
                 const __grid_constant__ CUtensorMap tm_lo, const TreeParams p, int dv, int splits,
                 __nv_bfloat16* __restrict__ o) {
@@ -216,7 +217,7 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
 #pragma unroll
     for (int i = 0; i < 3; ++i)
       cuts[i] = lane + 32 * i < p.ranges ? p.cuts[lane + 32 * i] : make_int4(-1, 0, 0, 0);
-    for (int n = warp; n < p.BT; n += kThreads / 32) {
+    for (int n = warp; n < p.BT; n += kMergeThreads / 32) {
       const int b = n / p.T, row = (n - b * p.T) * p.H + h;
       const int mt = row / kTreeTile, m = row - mt * kTreeTile;
       const int group = mt / p.team, member = mt - group * p.team, item = b * p.groups + group;
@@ -344,7 +345,7 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
       }
     }
   }
-  if (warp >= 4) {
+  if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------------------------- epilogue
     // A thread holds one dim of the tile's tokens; neighbours swap, so that each stores two dims
     // of every second token.
@@ -437,11 +438,11 @@ cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void*
   // one CTA per 128 rows of W_UV; its tokens are split where that leaves SMs idle
   const int ctas = p.H * ((dv + kDims - 1) / kDims), tiles = (p.BT + kTok - 1) / kTok;
   // Up to 16 tokens the merge is done here: 1 x 8 tokens of 128 heads over 1000 rows take 22.9 us
-  // against 27.9 with a merge kernel in between, 32768 rows 70.3 against 76.7, 4 x 4 over 1000 26.3
-  // against 28.8, 3 x 5 of 16 heads 24.2 against 25.6; 8 x 4 37.8 against 37.1, 12 x 4 of 16 heads
+  // against 27.9 with a merge kernel in between, 32768 rows 70.3 against 76.7, 4 x 4 over 1000 25.0
+  // against 28.8, 3 x 5 of 16 heads 23.8 against 25.6; 8 x 4 37.8 against 37.1, 12 x 4 of 16 heads
   // over 4096 rows 51 against 43 (a CTA reads all partial results of its head).
   if (p.BT <= kMergeTok)
-    return launch_pdl(tree_out_kernel<true>, dim3((unsigned)ctas), dim3(kThreads), kSmem, st, w, hi,
+    return launch_pdl(tree_out_kernel<true>, dim3((unsigned)ctas), dim3(kMergeThreads), kSmem, st, w, hi,
                       lo, p, dv, 1, (__nv_bfloat16*)o);
   e = launch_pdl(tree_merge_parts_kernel,
                  dim3((unsigned)(p.ranges * p.team * (kTreeTile / kMergeWarps))),
