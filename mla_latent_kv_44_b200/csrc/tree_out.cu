@@ -26,7 +26,7 @@ constexpr int kDims = 128;                         // rows of W_UV per CTA
 constexpr int kTok = 128;                          // tokens per tile
 constexpr int kRing = 3;
 constexpr int kMergeThreads = 512;                 // of the kernel that merges them
-constexpr int kMergeTok = 16;                      // most tokens that are merged here
+constexpr int kMergeTok = 32;                      // most tokens that are merged here
 constexpr int kThreads = 256;
 constexpr int kWSlab = kDims * 128, kTerm = kTok * 128;
 constexpr int kStage = 2 * kTerm;                  // hi and lo: 32 KB
@@ -353,18 +353,24 @@ tree_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant_
     const int dim = dim0 + 32 * (warp & 3) + lane;
     const bool even = (lane & 1) == 0;
     for (int i = 0; i < hi - lo; ++i) {
+      // tokens of sequences without rows (their latent rows were not written): zeros
+      const int n0 = (lo + i) * kTok;
+      uint32_t none[kTok / 32];
+#pragma unroll
+      for (int j = 0; j < kTok / 32; ++j) {
+        const int mine = n0 + 32 * j + lane;
+        const bool is = mine < p.BT && tree_length(p, mine / p.T, false) == 0;
+        none[j] = __ballot_sync(0xffffffffu, is);
+        if (is && dim0 == 0 && (warp & 3) == 0 && p.lse) p.lse[(size_t)mine * p.H + h] = -INFINITY;
+      }
       if (!wait(bar(kDFull + (i & 1)), (i >> 1) & 1, p.err, abort)) break;
       tc_after();
-      const int n0 = (lo + i) * kTok;
       for (int c0 = 0; c0 < kTok && n0 + c0 < p.BT; c0 += 32) {
         uint32_t v[32];
         tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTok * (i & 1) + c0, v);
-        // tokens of sequences without rows (their latent rows were not written): zeros
-        const int mine = n0 + c0 + lane;
-        const bool none = mine < p.BT && tree_length(p, mine / p.T, false) == 0;
-        const uint32_t empty = __ballot_sync(0xffffffffu, none);
-        if (none && dim0 == 0 && (warp & 3) == 0 && p.lse)
-          p.lse[(size_t)mine * p.H + h] = -INFINITY;
+        uint32_t empty = none[0];
+#pragma unroll
+        for (int j = 1; j < kTok / 32; ++j) empty = c0 == 32 * j ? none[j] : empty;
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           const uint32_t got = __shfl_xor_sync(0xffffffffu, even ? v[c + 1] : v[c], 1);
@@ -437,10 +443,10 @@ cudaError_t launch_tree_out(const TreeParams& p, const void* w_uv, int dv, void*
   }
   // one CTA per 128 rows of W_UV; its tokens are split where that leaves SMs idle
   const int ctas = p.H * ((dv + kDims - 1) / kDims), tiles = (p.BT + kTok - 1) / kTok;
-  // Up to 16 tokens the merge is done here: 1 x 8 tokens of 128 heads over 1000 rows take 22.9 us
-  // against 27.9 with a merge kernel in between, 32768 rows 70.3 against 76.7, 4 x 4 over 1000 25.0
-  // against 28.8, 3 x 5 of 16 heads 23.8 against 25.6; 8 x 4 37.8 against 37.1, 12 x 4 of 16 heads
-  // over 4096 rows 51 against 43 (a CTA reads all partial results of its head).
+  // Up to 32 tokens the merge is done here: 1 x 8 tokens of 128 heads over 1000 rows take 22.9 us
+  // against 27.9 with a merge kernel in between, 32768 rows 70.3 against 76.7, 8 x 4 over 1000 34.9
+  // against 37.6, 8 x 4 of 16 heads over 4096 rows 41 against 45; 1 x 48 44.9 against 43.8 (a CTA
+  // reads all partial results of its head).
   if (p.BT <= kMergeTok)
     return launch_pdl(tree_out_kernel<true>, dim3((unsigned)ctas), dim3(kMergeThreads), kSmem, st, w, hi,
                       lo, p, dv, 1, (__nv_bfloat16*)o);

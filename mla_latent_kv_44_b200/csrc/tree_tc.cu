@@ -506,6 +506,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  // this CTA's barriers are initialised; waited for behind the schedule, which hides the exchange
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   wait_prior_grid();  // the lengths, Q and the cache rows come from earlier kernels
   // The kernels behind may start on SMs that are done; they wait for this grid before they read
   // its results. Not before the wait above: what they read before theirs (W_UV) must be there.
@@ -517,7 +520,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
   tc_before();
   __syncthreads();
   tc_after();
-  cluster_sync();  // barriers of both CTAs initialised before any remote traffic
+  // barriers of both CTAs initialised before any remote traffic
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   TileWalk walk{&p, s_len, work.item, member, range, work.begin, work.end,
