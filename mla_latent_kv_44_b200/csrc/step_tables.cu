@@ -393,7 +393,7 @@ cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   cudaError_t e = small ? cudaLaunchKernelEx(&cfg, build_tables_kernel<kTabSmall>, p)
                         : cudaLaunchKernelEx(&cfg, build_tables_kernel<kTabThreads>, p);
   if (e == cudaSuccess && apart)
