@@ -4,17 +4,22 @@
 // A sequence's T drafted tokens and H heads are T * H query rows over the same cache rows, so
 // they are tiled together: one CTA takes 8 * RPW of them (8 warps, RPW rows per warp) against a
 // range of cache rows, staged 32 * KPL at a time in shared memory as fp32. Scores: lane j of a
-// warp takes cache rows j (and j + 32) for the warp's RPW query rows (one conflict-free 16-byte read of the row,
-// its pitch D + 4 words, per RPW broadcast reads of the queries). Softmax: running maximum and
-// sum in fp32. Values: lane owns r / 32 columns; the weights go through shared memory four cache
-// rows at a time. Rows of the cache that precede the drafted ones are seen by every token; for
-// the drafted ones the token's mask word decides, and a masked score is replaced, never added to,
-// so that nothing of a masked row (NaN included) reaches the result.
+// warp takes cache rows j (and j + 32) for the warp's RPW query rows (one conflict-free 16-byte
+// read of the row, its pitch D + 4 words, per RPW broadcast reads of the queries). Softmax:
+// running maximum and sum in fp32, the warp's rows side by side (their shuffles overlap), the sums
+// kept per lane until the end. Values: lane owns r / 32 columns; the weights go through shared
+// memory four cache rows at a time. Rows of the cache that precede the drafted ones are seen by
+// every token; for the drafted ones the token's mask word decides, and a masked score is
+// replaced, never added to, so that nothing of a masked row (NaN included) reaches the result.
 // The keys of a sequence are cut into `splits` equal ranges when there are too few query tiles to
 // fill the GPU. The second kernel weighs the ranges by their log-sum-exp, in range order, and
 // applies W_UV to the merged rows where it has them, in shared memory.
 // What bounds it: latency at the sizes that it is for (fp32 models, small heads): a CTA's chain of
-// block id, cache rows, scores, softmax, values. So 64 cache rows go in one tile where they fit.
+// block id, cache rows, scores, softmax, values, and shared-memory reads in scores and values
+// (three for eight FMAs). So 64 cache rows go in one tile where two CTAs of that fit an SM (128
+// registers a thread: 8 x 5 tokens of 16 heads, r = 64, over 1024 rows 24.7 us; with three CTAs
+// and ranges for them 23.4, but 64 x 4 tokens 77 against 72 and 4 x 16 tokens over 4000 rows 47
+// against 42; with one 29.6).
 #include <algorithm>
 
 #include "tree.cuh"
@@ -42,7 +47,8 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
 }
 
 template <typename T, int RPW, int KPL, int RW>  // RW: latent columns per lane (r <= 32 * RW)
-__global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, KPL == 2 ? 2 : 1)
+tree_simt_kernel(const TreeParams p) {
   constexpr int M = kWarps * RPW, kKeys = 32 * KPL;
   extern __shared__ __align__(16) float smem[];
   const int D = p.D, ld = D + 4, r = p.r, quads = D / 4;
@@ -61,6 +67,22 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
   // this CTA's cache rows, whole tiles of kKeys
   const int tiles = (len + kKeys - 1) / kKeys, per = (tiles + p.splits - 1) / p.splits;
   const int lo = min(split * per, tiles) * kKeys, hi = min((split + 1) * per * kKeys, len);
+
+  // the pool row of a cache row, or -1 (past the range, or a block outside the pool)
+  auto place = [&](int row) -> int64_t {
+    if (row >= hi) return -1;
+    const int at = row / p.bs, blk = p.table[(size_t)b * p.max_blocks + at];
+    if (blk < 0 || blk >= p.num_blocks) {
+      set_error(p.err, MLA_DEV_OOB_BLOCK);
+      return -1;
+    }
+    return (int64_t)blk * p.bs + (row - at * p.bs);
+  };
+
+  // a warp takes every eighth row of a tile; lane j finds where row j of the warp's rows lies, one
+  // tile ahead
+  constexpr int kPer = kKeys / kWarps;
+  int64_t next_at = place(lo + warp + kWarps * (lane % kPer));
 
   // queries, times softmax_scale / ln 2: scores come out in base-2 units
   const float c2 = p.scale * 1.4426950408889634f;
@@ -91,22 +113,9 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
   const float* qw = s_q + warp * RPW * D;
   float* pw = s_p + warp * RPW * kKeys;
 
-  // the pool row of a cache row, or -1 (past the range, or a block outside the pool)
-  auto place = [&](int row) -> int64_t {
-    if (row >= hi) return -1;
-    const int at = row / p.bs, blk = p.table[(size_t)b * p.max_blocks + at];
-    if (blk < 0 || blk >= p.num_blocks) {
-      set_error(p.err, MLA_DEV_OOB_BLOCK);
-      return -1;
-    }
-    return (int64_t)blk * p.bs + (row - at * p.bs);
-  };
-
   for (int t0 = lo; t0 < hi; t0 += kKeys) {
     __syncthreads();  // previous tile consumed
-    // a warp takes every eighth row; lane j finds where row j of its rows lies
-    constexpr int kPer = kKeys / kWarps;
-    const int64_t my_at = place(t0 + warp + kWarps * (lane % kPer));
+    const int64_t my_at = next_at;
     int64_t at[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) at[j] = __shfl_sync(0xffffffffu, my_at, j) * D;
@@ -120,6 +129,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
       for (int j = 0; j < kPer; ++j) *(float4*)(s_k + (warp + kWarps * j) * ld + 4 * qd) = v[j];
     }
     if (lane < kPer) s_there[warp + kWarps * lane] = my_at >= 0;
+    next_at = place(t0 + kKeys + warp + kWarps * (lane % kPer));
     __syncthreads();
     if (m0 + warp * RPW >= rows) continue;  // this warp has no query rows
     bool there[KPL];
@@ -151,28 +161,48 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
       }
     }
     const bool drafted = t0 + kKeys > first;  // the tile holds drafted rows
+    bool seen[RPW][KPL];
+#pragma unroll
+    for (int a = 0; a < RPW; ++a)
+#pragma unroll
+      for (int c = 0; c < KPL; ++c) seen[a][c] = there[c];
+    if (drafted) {
+#pragma unroll
+      for (int a = 0; a < RPW; ++a)
+#pragma unroll
+        for (int c = 0; c < KPL; ++c) {
+          const int node = t0 + lane + 32 * c - first;
+          if (node >= 0 && there[c]) seen[a][c] = tree_sees(p, b, tok[a], node);
+        }
+    }
+    // the warp's rows side by side, so that their shuffles overlap
+    float top[RPW];
 #pragma unroll
     for (int a = 0; a < RPW; ++a) {
-      float top = -INFINITY;
-      bool seen[KPL];
+      top[a] = -INFINITY;
 #pragma unroll
       for (int c = 0; c < KPL; ++c) {
-        const int node = t0 + lane + 32 * c - first;
-        seen[c] = there[c];
-        if (drafted && node >= 0 && seen[c]) seen[c] = tree_sees(p, b, tok[a], node);
-        s[a][c] = seen[c] ? s[a][c] : -INFINITY;
-        top = fmaxf(top, s[a][c]);
+        s[a][c] = seen[a][c] ? s[a][c] : -INFINITY;
+        top[a] = fmaxf(top[a], s[a][c]);
       }
-      const float m = fmaxf(mx[a], warp_max(top));
+    }
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1)
+#pragma unroll
+      for (int a = 0; a < RPW; ++a)
+        top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], step));
+#pragma unroll
+    for (int a = 0; a < RPW; ++a) {
+      const float m = fmaxf(mx[a], top[a]);
       const float alpha = mx[a] == -INFINITY ? 0.f : ex2_(mx[a] - m);
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < KPL; ++c) {
-        const float e = seen[c] && s[a][c] != -INFINITY ? ex2_(s[a][c] - m) : 0.f;
+        const float e = seen[a][c] && s[a][c] != -INFINITY ? ex2_(s[a][c] - m) : 0.f;
         sum += e;
         pw[a * kKeys + lane + 32 * c] = e;
       }
-      l[a] = l[a] * alpha + warp_sum(sum);
+      l[a] = l[a] * alpha + sum;  // the lane's share; summed over the warp at the end
       mx[a] = m;
 #pragma unroll
       for (int k = 0; k < RW; ++k) o[a][k] *= alpha;
@@ -226,6 +256,10 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
   }
 
 #pragma unroll
+  for (int step = 16; step > 0; step >>= 1)
+#pragma unroll
+    for (int a = 0; a < RPW; ++a) l[a] += __shfl_xor_sync(0xffffffffu, l[a], step);
+#pragma unroll
   for (int a = 0; a < RPW; ++a) {
     const int m = warp * RPW + a;
     if (m0 + m >= rows) continue;
@@ -246,6 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const TreeParams
 }
 
 // ---- merge of the ranges and W_UV: one CTA per head and NT tokens -------------------------
+// (4.3 us of the 24.7: two rounds of loads, of the log-sum-exps and the partial rows, and W_UV.)
 // stage: W_UV[h] fits shared memory; it is fetched before the wait for the attention (it is no
 // result of it) and read from there.
 template <typename T, int NT>
@@ -296,10 +331,13 @@ tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restri
     const bool empty = mx == -INFINITY && !nan;
     const float inv = empty ? 0.f : 1.f / z;
     __syncwarp();
-    for (int d = 4 * lane; d < r; d += 128) {
+    // r / 4 lanes cover a row; where that is half a warp or less, groups of lanes share the ranges
+    const int share = r <= 32 ? 4 : r <= 64 ? 2 : 1, width = 32 / share;
+    for (int d = 4 * (lane % width); d < (r + 4 * width - 1) / (4 * width) * (4 * width);
+         d += 4 * width) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-      for (int k = 0; k < p.splits; ++k) {
+      for (int k = lane / width; k < (d < r ? p.splits : 0); k += share) {
         const float e = s_w[t][k] * inv;
         // a range without rows holds zeros
         const float4 v = __ldcs((const float4*)(p.part_o + (k * part + at) * r + d));
@@ -308,7 +346,13 @@ tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restri
         a.z = fmaf(e, v.z, a.z);
         a.w = fmaf(e, v.w, a.w);
       }
-      *(float4*)(s_lat + t * r + d) = a;
+      for (int step = width; step < 32; step <<= 1) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, step);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, step);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, step);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, step);
+      }
+      if (d < r && lane < width) *(float4*)(s_lat + t * r + d) = a;
     }
     if (lane == 0 && p.lse) p.lse[at] = empty ? -INFINITY : mx + logf(z);
   }
