@@ -60,7 +60,8 @@ typedef enum { MLA_F32 = 0, MLA_BF16 = 1 } mla_dtype;
 /* Which kernels the calls use. AUTO: tcgen05 tensor-core kernels where dtype and shape allow
  * them -- mla_decode's attention for bf16 at H=128, r=512, d_r=64, block_size=64; the
  * projections of mla_absorb_query (d_h a multiple of 64 up to 256, r a multiple of 64) and
- * mla_output (r a multiple of 64) for bf16 -- and CUDA-core kernels otherwise. SIMT: CUDA-core
+ * mla_output (r a multiple of 64) for bf16; mla_decode_tree for bf16 at r=512, d_r=64, block_size
+ * a multiple of 64, any H -- and CUDA-core kernels otherwise. SIMT: CUDA-core
  * kernels for every call. TENSOR: tensor-core kernels, MLA_ERR_UNSUPPORTED where the shape
  * has none. (The name is historical: the choice covers every call, not only mla_decode.) */
 typedef enum { MLA_DECODE_AUTO = 0, MLA_DECODE_SIMT = 1, MLA_DECODE_TENSOR = 2 } mla_decode_kernel;
@@ -415,8 +416,8 @@ MLA_API mla_status mla_combine_partials(const mla_config* cfg, const float* part
  * and has no tokens), for more than max_tokens tokens (those behind are dropped, cu_new stops
  * there) and for a free_count outside [0, num_blocks] or more blocks given back than the list
  * has room for (no block moves); MLA_DEV_OOB_BLOCK for a block id outside the pool (slot -1).
- * One launch (two for more than 32,768 tokens); deterministic. batch <= MLA_MAX_TABLE_BATCH, max_tokens <= 2^26 and
- * batch * max_blocks <= 2^30 (MLA_ERR_UNSUPPORTED). max_tokens may be 0.
+ * One launch (two for more than 32,768 tokens); deterministic. batch <= MLA_MAX_TABLE_BATCH,
+ * max_tokens <= 2^26 and batch * max_blocks <= 2^30 (MLA_ERR_UNSUPPORTED). max_tokens may be 0.
  */
 MLA_API mla_status mla_build_tables(const mla_config* cfg, const int32_t* seq_lens,
                                     const int32_t* new_lens, int32_t batch, int32_t* block_table,
@@ -478,14 +479,14 @@ MLA_API size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t bat
  * dtype; lse (batch * T, H) float32 or NULL. A drafted row that a node's mask leaves out does not
  * reach that node's result, whatever it holds (NaN, infinities, a row never written). A node
  * that attends nothing gets o = 0 and lse = -inf, and so does every node of an empty sequence
- * (seq_lens[b] = 0); a length in (0, T), above max_blocks * block_size or above 2^31 - 8193 does too
- * and sets MLA_DEV_BAD_LENGTH. q, pool, w_uv and o must be 16-byte aligned. Deterministic.
+ * (seq_lens[b] = 0); a length in (0, T), above max_blocks * block_size or above 2^31 - 8193 does
+ * too and sets MLA_DEV_BAD_LENGTH. q, pool, w_uv and o must be 16-byte aligned. Deterministic.
  * decode_kernel chooses as in mla_decode: the tensor-core kernel needs bf16, r = 512, d_r = 64 and
  * a block_size that is a multiple of 64, and takes any H. Between the attention and W_UV that path
  * keeps the latent sums as two bf16 terms (16 bits), the other in fp32.
- * MLA_ERR_UNSUPPORTED: q_per_seq > MLA_MAX_TREE, batch * q_per_seq > 2^24 or times H > 2^28; on the
- * tensor-core path also a pool of 2^31 rows or more, or batch * (query tiles per sequence) * (64-row
- * pieces that a table row can hold) >= 2^31.
+ * MLA_ERR_UNSUPPORTED: q_per_seq > MLA_MAX_TREE, batch * q_per_seq > 2^24 or times H > 2^28; on
+ * the tensor-core path also a pool of 2^31 rows or more, or 2^31 or more 64-row pieces of work, as
+ * many as a table row can hold for each group of 128-row query tiles.
  */
 MLA_API mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* pool,
                                    const int32_t* block_table, int32_t max_blocks,

@@ -376,10 +376,11 @@ def _refuse(where: str, *tensors):
     device = None
     for name, t, dtype, shape in tensors:
         if not isinstance(t, torch.Tensor):
-            raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is {type(t).__name__}, not a tensor")
+            raise MlaError(MLA_ERR_INVALID_ARG,
+                           f"{where}: {name} is {type(t).__name__}, not a tensor")
         if t.dim() != len(shape):
-            raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} has shape {tuple(t.shape)}, wanted "
-                           f"{len(shape)} dimensions")
+            raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} has shape {tuple(t.shape)}, "
+                           f"wanted {len(shape)} dimensions")
         if not t.is_cuda:
             raise MlaError(MLA_ERR_INVALID_ARG, f"{where}: {name} is on {t.device}, not on a GPU")
         device = t.device if device is None else device

@@ -5,11 +5,13 @@
 // A drafted token's RoPE position is its depth's while its row is its own, so the position and
 // the place are two inputs here. One warp per row, rows dealt round the grid: a lane holds up to
 // NP 16-byte pieces of the row (coalesced across the warp), fp32 statistics by a butterfly. The
-// angles are p * theta_i in double, as everywhere in the library, and are brought into [-pi, pi] in
-// double (Cody and Waite's two-term reduction); their sine and cosine are then taken in fp32, 1e-7 off
-// at most. theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a double pow per
+// angles are p * theta_i in double, as everywhere in the library, and are brought into [-pi, pi]
+// in double (Cody and Waite's two-term reduction); their sine and cosine are then taken in fp32,
+// 1e-7 off at most. theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a double pow per
 // lane, and sincos in double, took most of the 16 us that 16,384 rows needed.
-// What bounds it: HBM for prompts (the row in and out), latency for a decode step.
+// What bounds it: HBM for prompts (the row in and out: 16,384 tokens, 37.9 MB, 8.4 us with the rows
+// in L2 and 11.5, 3.3 TB/s, from HBM; a row's load, sum and store follow one another), latency for
+// a decode step (128 tokens: 2.7 us).
 #include <algorithm>
 #include <cmath>
 
@@ -190,7 +192,8 @@ cudaError_t launch_append_slots(const mla_config& c, const void* ckv, const void
 // per sequence; a thread owns one 16-byte (8-byte) column of the rows and moves it for all d, so
 // no two threads touch the same bytes and nothing has to be waited for between rows: kMove loads
 // are in flight, then their stores (the stores of rows d .. d + kMove - 1 cannot reach a source
-// path[d'] >= d' >= d + kMove). The path is checked before anything moves.
+// path[d'] >= d' >= d + kMove). The path is checked before anything moves. What bounds it: latency
+// (32 sequences of 4 nodes 2.4 us, 256 of 64 nodes 3.9).
 // ------------------------------------------------------------------------------------------
 namespace {
 

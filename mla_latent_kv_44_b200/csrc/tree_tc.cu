@@ -13,14 +13,19 @@
 // SM that computed it: nothing but MMA operands crosses between the two.
 //
 // Per 256 keys a CTA streams 9 stages of K (128 keys x 64 dims) and 8 of V (64 keys x 128 dims), 16
-// KB each, through a ring for each. One warp issues the score products and another P . V, so the
-// scores of tile t + 1 and P . V of tile t share the tensor core while the softmax of tile t + 1
-// waits for the one and that of tile t + 2 ... What bounds the tensor core's use is not the data but
-// the issue: four MMAs of 64 cycles each use a stage, and the wait, the four issues and the commit
-// take a warp about 400 cycles (386 per K stage and 435 per V stage measured with one warp for
-// both, a tile then 7.9k cycles for 4.35k of products). The whole warp runs the issue loop and
-// one elected lane issues: from a single thread in a divergent branch an MMA took 132 cycles to
-// issue whatever its size, with the warp converged and the descriptors' low words at hand 25.
+// KB each, through a ring for each. One warp issues the score products and another P . V, so that
+// P . V of a tile runs while the scores of the next are made, waited for and exponentiated. The
+// whole warp runs the issue loop and one elected lane issues: from a single thread in a divergent
+// branch an MMA took 132 cycles to issue whatever its size, with the warp converged and the
+// descriptors' low words at hand 25.
+//
+// What bounds it. 32 sequences x 16384 rows x 4 tokens of 128 heads take 480 us in short bursts,
+// 1.22 PFLOP/s (0.72 of the measured burst rate, 0.86 of the sustained one: the power limit holds
+// the clock near 1.4 GHz), the tensor core and its issue: four MMAs of 64 cycles use a stage, and
+// the wait, the issues and the commit of a stage take a warp about 400 cycles. Few heads (a tile
+// of 128 rows half empty) are bound by HBM: 3 x 32768 rows x 5 tokens of 16 heads stream at 4.9
+// TB/s. One short sequence is bound by latency: of 15 us for 8 tokens x 1000 rows the schedule
+// takes 2, the first loads 1.5, a tile's scores, softmax and P . V 6, the partial results 3.
 //
 // Softmax: four warps, a thread holds one query row and half of the tile's keys (TMEM lane), two
 // threads of a row exchange their maxima; base-2 exponents, the running maximum moved only when
@@ -130,8 +135,9 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
       : "memory");
 }
 __device__ __forceinline__ void commit_one(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
 }
 // load into this CTA's shared memory, bytes counted on a barrier of either CTA of the pair
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -339,8 +345,8 @@ __device__ int scan_chunks(int v, int* s_warp, int* total) {
   return v + before;
 }
 
-// First chunk of range q of R over C chunks (floor(q C / R), as range_start); 32-bit division, which
-// takes a fraction of the time, where it does.
+// First chunk of range q of R over C chunks (floor(q C / R), as range_start); a 32-bit division,
+// which takes a fraction of the time, where that is enough.
 __device__ __forceinline__ int first_chunk(int q, int R, int C) {
   if (C < 1 << 25) return (int)((uint32_t)(q * C) / (uint32_t)R);  // q <= 74
   return range_start(q, R, C);
@@ -890,7 +896,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
           if (elect_one()) {
             const uint32_t a = q_lo + kSlabLo * k, b = ring + kStageLo * at.stage;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma2(d, a + 2 * i, b + 2 * i, id, (k > 0 || i > 0) ? 1u : 0u);
+            for (int i = 0; i < 4; ++i)
+              mma2(d, a + 2 * i, b + 2 * i, id, (k > 0 || i > 0) ? 1u : 0u);
             commit_both(bar(kKEmpty + at.stage));
           }
           __syncwarp();
@@ -906,7 +913,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
         has = walk.next(cur);
       }
     } else if (warp == 2 && rank == 0) {
-      // ---------------------------------------------------------------------------- MMA: O += P . V
+      // -------------------------------------------------------------------------- MMA: O += P . V
       Cursor<kVRing> at;
       int t = 0, seg = 0;
       bool ok = true;
