@@ -7,8 +7,8 @@
 // both bf16 terms of each value (hi = bf16(x), lo = bf16(x - hi); one term alone would add as large
 // an error as the rounding of o). M = 128 (dims), N = the tile's tokens: 8 MMAs per stage into
 // one of two tensor-memory accumulators; the epilogue of a tile of tokens runs while the next
-// one's products do. (1024 tokens of 128 heads take 59 us, 0.42 GB at 7 TB/s out of L2 and HBM; with
-// 32 tokens per tile the MMAs' issue took 146.) With few tokens the CTA merges its head's partial
+// one's products do. (1024 tokens of 128 heads take 59 us, 0.32 GB at 5.4 TB/s; with 32 tokens per
+// tile the MMAs' issue took 146.) With few tokens the CTA merges its head's partial
 // results itself, into the operand's layout (6 us for 8 tokens, of them the merge 2.8). What
 // bounds it: latency and the weights' bytes for few tokens, the latent rows' for many.
 #include <atomic>
