@@ -21,11 +21,14 @@
 //
 // What bounds it. 32 sequences x 16384 rows x 4 tokens of 128 heads take 480 us in short bursts,
 // 1.22 PFLOP/s (0.72 of the measured burst rate, 0.86 of the sustained one: the power limit holds
-// the clock near 1.4 GHz). Four MMAs of 64 cycles use a 16 KB stage, 64 bytes per clock and SM;
-// a stage takes about 400 cycles, 40 bytes per clock and SM, 11.6 TB/s out of L2 in all (8 x 16384
-// x 4: 1.53 GB in 131 us, the tensor cores active 58% of it): the operands' way from L2 is what
-// more products would wait for. More query rows per pair would halve it but for O, which fills the
-// tensor memory beside S; half of V lies in the K stages, which leave too little room to keep.
+// the clock near 1.4 GHz). A tile takes about 7k cycles for 4.35k of products. Beside them its
+// softmax takes 4.3k (scores out of TMEM and the maximum 1.7k, exponentials 1.7k, P 0.4k, waits),
+// so that any instruction more in it shows: scores read twice to save registers 516 us against
+// 493, exponentials begun before the two halves' maxima are exchanged 512. The operands come out of
+// L2 at 40 bytes per clock and SM, 11.6 TB/s in all; with no loads at all (and wrong results) 8 x
+// 16384 x 4 took 113 us instead of 137, without V's 128, without K's 137. More query rows per pair
+// would halve the operands but for O, which fills the tensor memory beside S.
+//
 // Few heads (a tile
 // of 128 rows half empty) are bound by HBM: 3 x 32768 rows x 5 tokens of 16 heads take 43 us, and
 // once under way stream at 4.9 TB/s. One short sequence is bound by latency: of 15 us for 8 tokens x 1000 rows the schedule
