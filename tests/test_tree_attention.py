@@ -131,6 +131,17 @@ def test_cuda_cores(mla, kw, dtype):
     Case(mla, dtype=dtype, kernel=mla.DECODE_SIMT, **kw).run(mla)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(H=16, T=32, lens=[5000]), dict(H=16, T=33, lens=[5000]), dict(H=1, T=1, lens=[20000]),
+    dict(H=2, T=40, lens=[20000]), dict(H=128, T=1, lens=[64 * k for k in range(32)], dv=192),
+    dict(H=128, T=1, lens=[64 * k for k in range(33)]), dict(H=24, T=4, lens=[900] * 8, dv=33),
+    dict(H=128, T=16, lens=[900, 0]), dict(H=128, T=11, lens=[900, 11, 0])],
+    ids=lambda k: f"H{k['H']}-T{k['T']}-B{len(k['lens'])}-L{k['lens'][0]}")
+def test_partial_results_merged_with_the_output_or_before(mla, kw):
+    """Up to 32 tokens the output kernel merges; items of one to 74 pieces, empty sequences."""
+    Case(mla, kernel=mla.DECODE_TENSOR, **kw).run(mla)
+
+
 @pytest.mark.parametrize("kernel", [1, 2])
 def test_padded_batch(mla, kernel):
     """Empty places between sequences: zeros, lse -inf, no error."""

@@ -244,6 +244,17 @@ def test_tables_match_the_plain_form(mla, batch, width, bs, spare, tokens, seed,
 
 
 @GPU
+@pytest.mark.parametrize("batch,width,bs,spare,tokens,seed", [
+    (512, 2, 8, 900, 512, 11), (512, 2, 8, 900, 513, 12), (300, 2, 8, 500, 2048, 13),
+    (513, 2, 8, 900, 2049, 14), (1024, 3, 4, 2500, 4096, 15), (1025, 2, 4, 2000, 4097, 16),
+    (700, 2, 16, 1200, 33000, 17), (1100, 2, 16, 1200, 33000, 18), (8192, 2, 4, 15000, 32768, 19),
+    (600, 2, 4, 100, 3000, 20)])
+def test_tables_at_the_sizes_where_the_launch_changes(mla, batch, width, bs, spare, tokens, seed):
+    lens, new, table, held, free, count = _requests(seed, batch, width, bs, spare)
+    _run_tables(mla, bs, lens, new, table, held, free, count, tokens, in_place=seed % 2 == 0)
+
+
+@GPU
 def test_tables_of_bad_input(mla):
     table = [[0, 1, -1], [2, -1, -1], [3, 4, 5]]
     good = dict(lens=[130, 64, 192], new=[3, 1, 0], held=[2, 1, 3], free=[6, 7, -1, -1, -1, -1, -1, -1],
