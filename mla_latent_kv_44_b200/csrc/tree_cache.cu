@@ -7,8 +7,8 @@
 // NP 16-byte pieces of the row (coalesced across the warp), fp32 statistics by a butterfly. The
 // angles are p * theta_i in double, as everywhere in the library, and are brought into [-pi, pi]
 // in double (Cody and Waite's two-term reduction); their sine and cosine are then taken in fp32,
-// 1e-7 off at most. theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a double pow per
-// lane, and sincos in double, took most of the 16 us that 16,384 rows needed.
+// 1e-7 off at most. theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a double
+// pow per lane, and sincos in double, took most of the 16 us that 16,384 rows needed.
 // What bounds it: HBM for prompts (the row in and out: 16,384 tokens, 37.9 MB, 8.4 us with the rows
 // in L2 and 11.5, 3.3 TB/s, from HBM; a row's load, sum and store follow one another), latency for
 // a decode step (128 tokens: 2.7 us).

@@ -29,10 +29,10 @@
 // 16384 x 4 took 113 us instead of 137, without V's 128, without K's 137. More query rows per pair
 // would halve the operands but for O, which fills the tensor memory beside S.
 //
-// Few heads (a tile
-// of 128 rows half empty) are bound by HBM: 3 x 32768 rows x 5 tokens of 16 heads take 43 us, and
-// once under way stream at 4.9 TB/s. One short sequence is bound by latency: of 15 us for 8 tokens x 1000 rows the schedule
-// takes 2, the first loads 1.5, a tile's scores, softmax and P . V 6, the partial results 3.
+// Few heads (a tile of 128 rows half empty) are bound by HBM: 3 x 32768 rows x 5 tokens of 16 heads
+// take 43 us, and once under way stream at 4.9 TB/s. One short sequence is bound by latency: of 15
+// us for 8 tokens x 1000 rows the schedule takes 2, the first loads 1.5, a tile's scores, softmax
+// and P . V 6, the partial results 3.
 //
 // Softmax: four warps, a thread holds one query row and half of the tile's keys (TMEM lane), two
 // threads of a row exchange their maxima; base-2 exponents, the running maximum moved only when
