@@ -9,9 +9,9 @@
 // in double (Cody and Waite's two-term reduction); their sine and cosine are then taken in fp32,
 // 1e-7 off at most. theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a double
 // pow per lane, and sincos in double, took most of the 16 us that 16,384 rows needed.
-// What bounds it: HBM for prompts (the row in and out: 16,384 tokens, 37.9 MB, 8.4 us with the rows
-// in L2 and 11.5, 3.3 TB/s, from HBM; a row's load, sum and store follow one another), latency for
-// a decode step (128 tokens: 2.7 us).
+// What bounds it: HBM and its latency for prompts (the row in and out: 16,384 tokens, 37.9 MB, 10.5
+// us or 3.6 TB/s from HBM, 7.7 with the rows in L2; a warp has a row and the next in flight),
+// latency for a decode step (128 tokens: 2.5 us).
 #include <algorithm>
 #include <cmath>
 
@@ -25,8 +25,7 @@ constexpr int kAppendWarps = 8;
 template <typename T> struct Piece;  // 16 bytes of a row
 template <> struct Piece<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *(const uint4*)p;
+  static __device__ __forceinline__ void widen(const uint4 u, float (&v)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -46,12 +45,11 @@ template <> struct Piece<__nv_bfloat16> {
 };
 template <> struct Piece<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
-    const float4 u = *(const float4*)p;
-    v[0] = u.x;
-    v[1] = u.y;
-    v[2] = u.z;
-    v[3] = u.w;
+  static __device__ __forceinline__ void widen(const uint4 u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x);
+    v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z);
+    v[3] = __uint_as_float(u.w);
   }
   static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
     *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
@@ -75,12 +73,13 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
   *(__nv_bfloat162*)p = __floats2bfloat162_rn(x, y);
 }
 
-// four CTAs per SM: with more the registers no longer hold what a row has in flight (16,384 rows:
-// 10.5 us at four, 11.3 at three and five, 14.8 at six; two rows per warp 14.0)
-constexpr int kAppendCtas = 4;
+// Four CTAs per SM, fewer for longer rows: with more the registers no longer hold a row and the
+// next (16,384 rows of 512 bf16 out of HBM: 10.5 us at four, 10.8 at three, 12.9 at five; without
+// the next row's fetch 12.2, two rows per warp at a time longer still).
+constexpr int append_ctas(int pieces) { return pieces <= 2 ? 4 : pieces <= 4 ? 3 : 2; }
 
 template <typename T, int NP>
-__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas)
+__global__ void __launch_bounds__(kAppendWarps * 32, append_ctas(NP))
 append_slots_kernel(const T* __restrict__ ckv, const T* __restrict__ kr,
                     const float* __restrict__ gamma, const int32_t* __restrict__ pos,
                     const int64_t* __restrict__ slots, T* pool, int64_t pool_rows, int n, int r,
@@ -91,18 +90,31 @@ append_slots_kernel(const T* __restrict__ ckv, const T* __restrict__ kr,
   const int half = dr / 2, D = r + dr;
   const double theta0 = lane < half ? theta.t[lane] : 0.0;
   wait_prior_grid();
-  for (int row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5); row < n; row += warps) {
-    // everything that the row reads, before anything is done with it
-    const int64_t slot = slots[row];
-    const double p = (double)pos[row];
-    float v[NP][E];
+  // what a row reads is fetched while the row before is worked on
+  uint4 raw[NP];
+  float2 k_next;
+  int64_t slot_next = -1;
+  int pos_next = 0;
+  auto fetch = [&](int row) {
+    slot_next = slots[row];
+    pos_next = pos[row];
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int at = (lane + 32 * k) * E;
-      if (at < r) Piece<T>::load(ckv + (size_t)row * r + at, v[k]);
+      if (at < r) raw[k] = *(const uint4*)(ckv + (size_t)row * r + at);
     }
-    float2 k0;
-    if (lane < half) k0 = load2(kr + (size_t)row * dr + 2 * lane);
+    if (lane < half) k_next = load2(kr + (size_t)row * dr + 2 * lane);
+  };
+  int row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (row < n) fetch(row);
+  for (; row < n; row += warps) {
+    const int64_t slot = slot_next;
+    const double p = (double)pos_next;
+    const float2 k0 = k_next;
+    float v[NP][E];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) Piece<T>::widen(raw[k], v[k]);
+    if (row + warps < n) fetch(row + warps);
     if (slot < 0) continue;  // a step's padding
     if (slot >= pool_rows) {
       if (lane == 0) set_error(err, MLA_DEV_OOB_BLOCK);
@@ -149,7 +161,7 @@ template <typename T, int NP>
 cudaError_t append_slots_go(const mla_config& c, const void* ckv, const void* kr,
                             const float* gamma, const int32_t* pos, const int64_t* slots,
                             void* pool, int num_blocks, int n, uint32_t* err, cudaStream_t st) {
-  const int grid = std::min((n + kAppendWarps - 1) / kAppendWarps, 148 * kAppendCtas);
+  const int grid = std::min((n + kAppendWarps - 1) / kAppendWarps, 148 * append_ctas(NP));
   RopeTheta theta = {};
   // by products: the error of the 128th is 1e-14 of it, 3e-9 in any angle
   if (c.rope_dim > 0) {
