@@ -141,22 +141,30 @@ class Config:
                          self.decode_kernel)
 
     def _held(self):
+        # a struct is kept as long as the Config, so that no call's address outlives it, whatever
+        # another thread does with the Config meanwhile
         key = (self.num_heads, self.head_dim, self.kv_rank, self.rope_dim, self.block_size,
                self.dtype, self.head_dim_v, self.rope_base, self.rms_eps, self.softmax_scale,
                self.decode_kernel)
-        held = self.__dict__.get("_struct")
-        if held is None or held[0] != key:
+        structs = self.__dict__.get("_structs")
+        if structs is None:
+            structs = self.__dict__.setdefault("_structs", {})
+        held = structs.get(key)
+        if held is None:
             c = self.c()
-            held = self.__dict__["_struct"] = (key, c, ctypes.byref(c), ctypes.addressof(c))
+            held = structs.setdefault(key, (c, ctypes.byref(c), ctypes.addressof(c)))
         return held
+
+    def __getstate__(self):  # copies and pickles without the structs
+        return {k: v for k, v in self.__dict__.items() if k != "_structs"}
 
     def ref(self):
         """A reference to the C struct for a call; built again only when a field has changed."""
-        return self._held()[2]
+        return self._held()[1]
 
     def address(self) -> int:
-        """The address of that struct; good until a field changes."""
-        return self._held()[3]
+        """The address of that struct."""
+        return self._held()[2]
 
     @property
     def row_width(self) -> int:

@@ -1,7 +1,9 @@
 """mla_build_tables, mla_tree_masks, mla_append_slots and mla_commit_tree against plain forms, and the
 refusals of all tree calls."""
+import copy
 import ctypes
 import math
+import pickle
 
 import pytest
 import torch
@@ -139,6 +141,22 @@ def test_workspace_sizes_are_host_arithmetic(mla):
     assert size(c, 32, 4) >= 4 * n + 148 * 128 * 512 * 4
     f32 = _ref(mla, num_heads=16, head_dim=64, kv_rank=64, rope_dim=32, dtype="f32")
     assert size(f32, 8, 5) >= 8 * 5 * 16 * 64 * 4
+
+
+@pytest.mark.parametrize("again", [copy.copy, copy.deepcopy, lambda c: pickle.loads(pickle.dumps(c))],
+                         ids=["copy", "deepcopy", "pickle"])
+def test_a_used_config_copies_and_pickles(mla, again):
+    cfg = mla.Config(16, 64, 64, 32, 64)
+    at = cfg.address()
+    other = again(cfg)
+    assert other == cfg and other.address() != at and cfg.address() == at
+    other.num_heads = 8
+    assert mla.MlaConfig.from_address(other.address()).num_heads == 8
+    cfg.num_heads = 4  # the first struct stays as it was, and where it was
+    assert mla.MlaConfig.from_address(cfg.address()).num_heads == 4
+    assert mla.MlaConfig.from_address(at).num_heads == 16
+    cfg.num_heads = 16
+    assert cfg.address() == at
 
 
 def test_binding_refuses_what_a_pointer_cannot_carry(mla):
