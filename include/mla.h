@@ -404,18 +404,21 @@ MLA_API mla_status mla_combine_partials(const mla_config* cfg, const float* part
  *   - tokens: its new_lens[b] last rows are this step's tokens, numbered request after request:
  *     cu_new (batch + 1) int32 are the offsets (usable as mla_prefill's cu_seqlens where every
  *     row is new), and token i of request b has seq_idx[i] = b, pos[i] = its row and
- *     slots[i] = block * block_size + row % block_size, its row of the pool. Entries behind the
- *     last token, up to max_tokens, get seq_idx -1, pos 0 and slot -1.
+ *     slots[i] = block * block_size + row % block_size, its row of the pool. A request of length 0
+ *     may have tokens too: they are the padding of an empty place, so that with new_lens[b] = T
+ *     for every request token t of request b is b * T + t, as mla_decode_tree numbers it. Padding,
+ *     and entries behind the last token up to max_tokens, get seq_idx -1, pos 0 and slot -1.
  * seq_lens, new_lens, blocks_held, blocks_held_out (batch) int32; block_table
  * (batch, max_blocks) int32, in and out; free_blocks (num_blocks) int32, in and out, of which the
  * first free_count[0] are free; free_count, free_count_out (1) int32; seq_idx, pos
  * (max_tokens) int32; slots (max_tokens) int64. blocks_held_out and free_count_out may be
  * blocks_held and free_count; no other arrays may overlap. Of cfg only block_size is used.
- * Data errors: MLA_DEV_BAD_LENGTH for a length outside [0, max_blocks * block_size], new_lens[b]
- * outside [0, seq_lens[b]] or blocks_held[b] outside [0, max_blocks] (the request keeps its blocks
- * and has no tokens), for more than max_tokens tokens (those behind are dropped, cu_new stops
- * there) and for a free_count outside [0, num_blocks] or more blocks given back than the list
- * has room for (no block moves); MLA_DEV_OOB_BLOCK for a block id outside the pool (slot -1).
+ * Data errors: MLA_DEV_BAD_LENGTH for a length outside [0, max_blocks * block_size], a negative
+ * new_lens[b] or one above seq_lens[b] > 0, or blocks_held[b] outside [0, max_blocks] (the request
+ * keeps its blocks and has no tokens), for more than max_tokens tokens (those behind are dropped,
+ * cu_new stops there) and for a free_count outside [0, num_blocks] or more blocks given back than
+ * the list has room for (no block moves); MLA_DEV_OOB_BLOCK for a block id outside the pool (slot
+ * -1).
  * One launch (two for more than 32,768 tokens); deterministic. batch <= MLA_MAX_TABLE_BATCH,
  * max_tokens <= 2^26 and batch * max_blocks <= 2^30 (MLA_ERR_UNSUPPORTED). max_tokens may be 0.
  */

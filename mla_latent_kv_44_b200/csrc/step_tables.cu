@@ -50,6 +50,10 @@ __device__ __forceinline__ void cluster_barrier(int ctas) {
 // own count is capped at kTokenCap, so that every offset below 2^28 is exact.
 constexpr int kTokenSat = 1 << 29, kTokenCap = 1 << 28;
 
+// In place of the first new row: the request is an empty place of a padded batch, and its tokens
+// are padding.
+constexpr int kPadding = -2147483647 - 1;
+
 // Inclusive scan of three ints over the CTA (a saturating); s holds 3 x 32 ints.
 template <int NT>
 __device__ void scan3(int* s, int& a, int& b, int& c) {
@@ -100,7 +104,7 @@ __device__ __forceinline__ Request load_request(const TableParams& p, int b) {
   q.fresh = p.new_lens[b];
   q.held = p.held[b];
   q.ok = q.len >= 0 && (int64_t)q.len <= (int64_t)p.max_blocks * p.bs && q.fresh >= 0 &&
-         q.fresh <= q.len && q.held >= 0 && q.held <= p.max_blocks;
+         (q.fresh <= q.len || q.len == 0) && q.held >= 0 && q.held <= p.max_blocks;
   q.want = q.ok ? (int)(((int64_t)q.len + p.bs - 1) / p.bs) : q.held;
   if (!q.ok) q.fresh = 0;
   return q;
@@ -118,15 +122,15 @@ __device__ __forceinline__ int holder(const int* off, int batch, int i) {
 }
 
 // Tokens i0 .. i0 + per - 1: one search and one division for all of them while they stay in a
-// request. cu: offsets of the requests; start_of(b): its first new row, or -1 - row when it was not
-// served; `real` tokens in all.
+// request. cu: offsets of the requests; start_of(b): its first new row, -1 - row when it was not
+// served, kPadding where its tokens are padding; `real` tokens in all.
 template <typename F>
 __device__ __forceinline__ void map_tokens(const TableParams& p, const int* cu, F start_of,
                                            int64_t i0, int per, int real) {
   int seq[4], row[4];
   int64_t slot[4];
   int b = -1, left = 0, r = 0, at = 0, in = 0, blk = -1;
-  bool served = false;
+  bool served = false, padding = false;
   if (p.vec && i0 + 4 <= real) {
     // four tokens of one request, as most are: everything follows from the first (a warp whose
     // lanes part here runs both ways, so a block's end inside the four stays on this one)
@@ -168,7 +172,8 @@ __device__ __forceinline__ void map_tokens(const TableParams& p, const int* cu, 
       left = cu[b + 1] - i;
       const int from = start_of(b);
       served = from >= 0;
-      r = (served ? from : -1 - from) + i - cu[b];
+      padding = from == kPadding;
+      r = padding ? 0 : (served ? from : -1 - from) + i - cu[b];
       at = r / p.bs;
       in = r - at * p.bs;
       look = true;
@@ -184,8 +189,8 @@ __device__ __forceinline__ void map_tokens(const TableParams& p, const int* cu, 
         blk = -1;
       }
     }
-    seq[u] = b;
-    row[u] = r;
+    seq[u] = padding ? -1 : b;
+    row[u] = padding ? 0 : r;
     if (served && blk >= 0) slot[u] = (int64_t)blk * p.bs + in;
     ++r;
     ++in;
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(NT) build_tables_kernel(const TableParams p) {
   int* s_cu = s_dyn;                    // batch + 1: new tokens before request b
   int* s_back = s_cu + p.batch + 1;     // batch + 1: blocks given back by earlier requests
   int* s_take = s_back + p.batch + 1;   // batch + 1: blocks due to earlier requests
-  int* s_start = s_take + p.batch + 1;  // batch: first new row, or -1 - row when not served
+  int* s_start = s_take + p.batch + 1;  // batch: as map_tokens takes it
   __shared__ int s_scan[96], s_carry[3];
   const int tid = threadIdx.x, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(NT) build_tables_kernel(const TableParams p) {
       n = min(q.fresh, kTokenCap);
       back = max(q.held - q.want, 0);
       take = max(q.want - q.held, 0);
-      s_start[b] = q.ok ? q.len - q.fresh : 0;
+      s_start[b] = !q.ok ? 0 : q.len == 0 ? kPadding : q.len - q.fresh;
     }
     int a0 = n, a1 = back, a2 = take;
     scan3<NT>(s_scan, a0, a1, a2);
@@ -345,6 +350,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const TableParams
       p, s_cu,
       [&](int b) {
         const int len = p.seq_lens[b], start = len - p.new_lens[b];
+        if (len == 0) return kPadding;
         return (int64_t)p.held_out[b] * p.bs >= len ? start : -1 - start;
       },
       i0, p.per_thread, s_cu[p.batch]);

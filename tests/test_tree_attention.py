@@ -508,6 +508,75 @@ def test_steps_of_speculative_decoding(mla, dtype, H, dh, r, dr, bs):
         assert sorted(used + rest) == list(range(blocks))   # no block lost, none held twice
 
 
+@pytest.mark.parametrize("dtype,H,dh,r,dr,bs", [("bf16", 16, 64, 512, 64, 64),
+                                                 ("f32", 4, 32, 64, 32, 16)])
+def test_a_whole_step_of_a_padded_batch_in_one_graph(mla, dtype, H, dh, r, dr, bs):
+    """Tables to commit captured once and replayed over a batch whose requests grow, end and come:
+    the same bits as call by call, in the outputs, the pool and the tables."""
+    cfg = mla.Config(H, dh, r, dr, bs, dtype=dtype)
+    dt, i32, D, B, T, width, blocks = cfg.torch_dtype, torch.int32, r + dr, 5, 4, 12, 64
+    g = torch.Generator().manual_seed(5)
+    randn = lambda *s: torch.randn(*s, generator=g).to(dt).to(D_)  # noqa: E731
+    w_uk, w_uv, gamma = randn(H, dh, r) / r ** 0.5, randn(H, dh, r) / r ** 0.5, torch.ones(r, device=D_)
+    pool, free = randn(blocks, bs, D), torch.randperm(blocks, generator=g).int().to(D_)
+
+    def fresh():
+        e = lambda *s, t=i32: torch.zeros(*s, dtype=t, device=D_)  # noqa: E731
+        return dict(n=e(B), new=torch.full((B,), T, dtype=i32, device=D_), table=e(B, width) - 1,
+                    held=e(B), free=free.clone(), count=e(1) + blocks, cu=e(B + 1), seq=e(B * T),
+                    pos_=e(B * T), slots=e(B * T, t=torch.int64), parents=e(B, T), mask=e(B * T, 1),
+                    pos=e(B * T), ckv=e(B * T, r, t=dt), kr=e(B * T, dr, t=dt),
+                    qn=e(B * T, H, dh, t=dt), qr=e(B * T, H, dr, t=dt), q=e(B * T, H, D, t=dt),
+                    o=e(B * T, H, dh, t=dt), path=e(B, T), many=e(B), out=e(B), pool=pool.clone(),
+                    ws=e(mla.decode_tree_workspace_size(cfg, B, T), t=torch.uint8), err=e(1))
+
+    def step(s):
+        mla.build_tables(cfg, s["n"], s["new"], s["table"], s["held"], s["free"], s["count"], s["held"],
+                         s["count"], s["cu"], s["seq"], s["pos_"], s["slots"], s["err"])
+        mla.tree_masks(s["parents"], s["n"], s["mask"], s["pos"], s["err"])
+        mla.absorb_query(cfg, s["qn"], s["qr"], s["pos"], w_uk, s["q"], dev_err=s["err"])
+        mla.append_slots(cfg, s["ckv"], s["kr"], gamma, s["pos"], s["slots"], s["pool"], s["err"])
+        mla.decode_tree(cfg, s["q"], s["pool"], s["table"], s["n"], T, s["mask"], w_uv, s["ws"],
+                        s["o"], None, s["err"])
+        mla.commit_tree(cfg, s["path"], s["many"], T, s["table"], s["pool"], s["n"], s["out"], s["err"])
+
+    eager, graphed = fresh(), fresh()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step(graphed)
+    kept = [40, 0, 7, 0, 100]
+    for k in range(6):
+        if k == 2:
+            kept[1], kept[4] = 13, 0
+        if k == 4:
+            kept[0], kept[3], kept[4] = 0, bs, 1
+        parents = tu.parents_of("random", B, T, seed=k)
+        seen = tu.seen_of(parents)
+        paths = [seen[b, k % T].nonzero().flatten().tolist() if kept[b] else [] for b in range(B)]
+        new = dict(n=torch.tensor([x + T if x else 0 for x in kept], dtype=i32), parents=parents,
+                   path=torch.tensor([p + [-1] * (T - len(p)) for p in paths], dtype=i32),
+                   many=torch.tensor([len(p) for p in paths], dtype=i32),
+                   **{x: randn(*eager[x].shape) for x in ("ckv", "kr", "qn", "qr")})
+        for s in (eager, graphed):
+            for name, value in new.items():
+                s[name].copy_(value)
+        torch.cuda.synchronize()
+        step(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in eager:
+            if name != "ws":
+                assert torch.equal(eager[name], graphed[name]), (k, name)
+        assert int(eager["err"]) == 0
+        kept = [x + len(p) for x, p in zip(kept, paths)]
+        assert eager["out"].tolist() == kept
+        empty = [b for b in range(B) if not kept[b]]
+        assert (eager["slots"].view(B, T)[empty] == -1).all() and (eager["o"].view(B, T, -1)[empty] == 0).all()
+        assert all((eager["o"].view(B, T, -1)[b] != 0).any() for b in range(B) if kept[b])
+
+
 # ------------------------------------------------------------------- a wait that runs out
 
 CHILD = r"""

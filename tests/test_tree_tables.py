@@ -273,6 +273,28 @@ def test_tables_at_the_sizes_where_the_launch_changes(mla, batch, width, bs, spa
 
 
 @GPU
+@pytest.mark.parametrize("batch,T,bs,tokens", [(4, 6, 64, 24), (4, 6, 64, 40), (9, 4, 16, 36),
+                                               (300, 8, 8, 2400), (1200, 5, 16, 6000),
+                                               (500, 70, 64, 35000), (7, 3, 1, 20)])
+@pytest.mark.parametrize("full", [True, False])
+def test_tables_of_a_padded_batch(mla, batch, T, bs, tokens, full):
+    """T tokens for every place, the empty ones too: token t of request b is b * T + t."""
+    g = torch.Generator().manual_seed(batch + T)
+    width = -(-400 // bs)
+    lens = torch.randint(T, 400, (batch,), generator=g)
+    lens[torch.rand(batch, generator=g) < 0.4] = 0
+    lens[0] = 0
+    held = [int(h) for h in torch.randint(0, 2, (batch,), generator=g)]
+    need = int(((lens + bs - 1) // bs).sum()) // (1 if full else 2)
+    total = need + sum(held) + 1
+    ids = torch.randperm(total, generator=g).tolist()
+    table = [[ids.pop() if i < h else -1 for i in range(width)] for h in held]
+    count = len(ids)
+    _run_tables(mla, bs, lens.tolist(), [T] * batch, table, held, ids + [-1] * (total - count), count,
+                tokens)
+
+
+@GPU
 def test_tables_of_bad_input(mla):
     table = [[0, 1, -1], [2, -1, -1], [3, 4, 5]]
     good = dict(lens=[130, 64, 192], new=[3, 1, 0], held=[2, 1, 3], free=[6, 7, -1, -1, -1, -1, -1, -1],

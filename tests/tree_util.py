@@ -86,7 +86,7 @@ def tables(bs, lens, new, table, held, free, count, num_blocks, max_tokens):
     OOB, LEN, FULL = 1, 8, 32
     table = [list(row) for row in table]
     free, held, width, bits = list(free), list(held), len(table[0]), 0
-    ok = [0 <= n <= width * bs and 0 <= m <= n and 0 <= h <= width
+    ok = [0 <= n <= width * bs and 0 <= m and (m <= n or n == 0) and 0 <= h <= width
           for n, m, h in zip(lens, new, held)]
     want = [-(-n // bs) if good else h for n, h, good in zip(lens, held, ok)]
     if not all(ok):
@@ -125,6 +125,11 @@ def tables(bs, lens, new, table, held, free, count, num_blocks, max_tokens):
         for p in range(lens[b] - m, lens[b]):
             if len(seq) == max_tokens:
                 break
+            if lens[b] == 0:  # padding
+                seq.append(-1)
+                pos.append(0)
+                slots.append(-1)
+                continue
             blk = row[p // bs]
             seq.append(b)
             pos.append(p)
