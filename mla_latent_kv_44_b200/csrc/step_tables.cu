@@ -13,7 +13,7 @@
 // its request by a search in the prefix sums (a warp per request: 7.0 us instead of 4.0 for 64
 // requests, 14.6 instead of 9.8 for 128 with 32 prompts among them).
 // What bounds it: latency (a chain of dependent loads and two barriers) at decode sizes, 4.0 us for
-// 64 requests; for prompts also the 16 B written per token (131,072 tokens: 9.8 us, 0.21 TB/s).
+// 64 requests; for prompts also the 16 B written per token (131,072 tokens: 10.2 us, 0.21 TB/s).
 #include <algorithm>
 
 #include "tree.cuh"
