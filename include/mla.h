@@ -381,7 +381,8 @@ MLA_API mla_status mla_combine_partials(const mla_config* cfg, const float* part
  *   mla_build_tables (blocks and slots for P + T rows), mla_tree_masks (masks, positions),
  *   mla_absorb_query, mla_append_slots, mla_decode_tree, then mla_commit_tree.
  * A sequence whose length is 0 is an empty place of a padded batch: no call reads its rows or
- * flags it.
+ * flags what it holds. (mla_build_tables takes back its blocks, so blocks_held and new_lens are
+ * checked there as for any other.)
  */
 
 /* Most requests mla_build_tables takes in one call, and most nodes of a drafted tree. */
@@ -438,9 +439,10 @@ MLA_API mla_status mla_build_tables(const mla_config* cfg, const int32_t* seq_le
  *   pos[n] = seq_lens[b] - T + |A_t| - 1 (its RoPE position).
  * parents (parents_batch, T) int32 with parents_batch = batch, or 1 for one tree that all
  * sequences share; seq_lens (batch) int32, the drafted rows counted; mask
- * (batch * T, ceil(T / 32)) uint32; pos (batch * T) int32. A parent outside [-1, t) sets
- * MLA_DEV_BAD_TREE and counts as -1; 0 < seq_lens[b] < T sets MLA_DEV_BAD_LENGTH (positions 0, as
- * for an empty sequence). 1 <= q_per_seq <= MLA_MAX_TREE (MLA_ERR_UNSUPPORTED above).
+ * (batch * T, ceil(T / 32)) uint32; pos (batch * T) int32. A parent outside [-1, t) counts as -1
+ * and sets MLA_DEV_BAD_TREE, but not for a sequence of length 0, whose parents may be anything;
+ * 0 < seq_lens[b] < T and a negative length set MLA_DEV_BAD_LENGTH (positions 0, as for an empty
+ * sequence). 1 <= q_per_seq <= MLA_MAX_TREE (MLA_ERR_UNSUPPORTED above).
  */
 MLA_API mla_status mla_tree_masks(const int32_t* parents, int32_t parents_batch,
                                   const int32_t* seq_lens, int32_t batch, int32_t q_per_seq,

@@ -431,10 +431,12 @@ tree_masks_kernel(const int32_t* __restrict__ parents, int parents_batch,
   const int k = threadIdx.x / T, t = threadIdx.x - k * T;
   const int b = blockIdx.x * per + k;
   const bool live = k < per && b < batch;
+  int len = 0;
   if (live) {
     int a = parents[(parents_batch == 1 ? 0 : (size_t)b * T) + t];
-    if (a < -1 || a >= t) {
-      set_error(err, MLA_DEV_BAD_TREE);
+    len = seq_lens[b];
+    if (a < -1 || a >= t) {  // what an empty place holds is no error
+      if (len != 0) set_error(err, MLA_DEV_BAD_TREE);
       a = -1;
     }
     s_parent[threadIdx.x] = a;
@@ -456,7 +458,6 @@ tree_masks_kernel(const int32_t* __restrict__ parents, int parents_batch,
 #pragma unroll
   for (int i = 0; i < W; ++i)
     if (i < words) mask[n * words + i] = w[i];
-  const int len = seq_lens[b];
   const bool bad = len < T;
   if (bad && len != 0 && t == 0) set_error(err, MLA_DEV_BAD_LENGTH);
   pos[n] = bad ? 0 : len - T + depth;

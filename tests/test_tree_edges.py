@@ -62,3 +62,40 @@ def test_tables_where_shared_memory_passes_the_default_limit(batch):
                          capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, out.stderr[-2000:]
     assert json.loads(out.stdout.splitlines()[-1]) == [True] * 9
+
+
+# --------------------------------------------------------------------------------- tree_masks
+
+@GPU
+@pytest.mark.parametrize("T", [1, 5, 33, 100, 256])
+def test_parents_of_an_empty_place_are_not_flagged(mla, T):
+    """Unused places of a captured step hold whatever was there: no error, whatever their parents; a
+    live place's bad parents are flagged as before."""
+    i32, junk = torch.int32, 0x7ADE7ADE
+    parents = tu.parents_of("random", 4, T, seed=T)
+    parents[1], parents[3] = junk, -junk
+    lens = torch.tensor([T + 7, 0, T, 0], dtype=i32)
+    mask = torch.full((4 * T, (T + 31) // 32), -7, dtype=i32, device=D_)
+    pos, err = torch.full((4 * T,), -7, dtype=i32, device=D_), torch.zeros(1, dtype=i32, device=D_)
+    mla.tree_masks(parents.to(D_), lens.to(D_), mask, pos, err)
+    assert int(err) == 0
+    mended = parents.clone()
+    mended[[1, 3]] = -1                                # a bad parent counts as -1
+    seen = tu.seen_of(mended)
+    assert torch.equal(mask.cpu(), tu.words_of(seen))
+    want = lens[:, None] - T + seen.sum(-1).int() - 1
+    want[[1, 3]] = 0
+    assert torch.equal(pos.cpu().view(4, T), want)
+    mla.tree_masks(parents.to(D_), torch.full_like(lens, T).to(D_), mask, pos, err)
+    assert int(err) == mla.DEV_BAD_TREE
+
+
+@GPU
+def test_a_shared_tree_is_flagged_only_where_it_is_used(mla):
+    i32 = torch.int32
+    bad = torch.tensor([[-1, 5, 1]], dtype=i32, device=D_)
+    mask, pos = torch.zeros(6, 1, dtype=i32, device=D_), torch.zeros(6, dtype=i32, device=D_)
+    for lens, bits in (([0, 0], 0), ([0, 9], mla.DEV_BAD_TREE)):
+        err = torch.zeros(1, dtype=i32, device=D_)
+        mla.tree_masks(bad, torch.tensor(lens, dtype=i32, device=D_), mask, pos, err)
+        assert int(err) == bits
