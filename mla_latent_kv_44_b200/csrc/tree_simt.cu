@@ -418,8 +418,6 @@ cudaError_t simt_dispatch(const TreeParams& p, const void* w_uv, int dv, void* o
     else if (p.r <= 128 && p.D <= 192) e = simt_go<T, 4, 2, 4>(p, st);
     else if (p.r <= 256) e = simt_go<T, 4, 1, 8>(p, st);
     else e = simt_go<T, 4, 1, 16>(p, st);
-  } else if (p.r <= 512) {
-    e = simt_go<T, 1, 1, 16>(p, st);
   } else {
     e = simt_go<T, 1, 1, 32>(p, st);
   }
@@ -438,10 +436,8 @@ cudaError_t launch_tree_simt(const mla_config& c, const TreeParams& p, const voi
                              : simt_dispatch<float>(p, w_uv, c.head_dim_v, o, st);
 }
 
-// Query rows per tile: 32 (four per warp) where r <= 512 and the tile and 32 cache rows fit
-// shared memory, else 8.
-int tree_simt_tile_rows(const mla_config& c) {
-  return c.kv_rank <= 512 && c.kv_rank + c.rope_dim <= 768 ? 4 * kWarps : kWarps;
-}
+// Query rows per tile: 32 (four per warp) where r <= 512, whose tile and 32 cache rows fit shared
+// memory whatever d_r is (at most 256), else 8.
+int tree_simt_tile_rows(const mla_config& c) { return c.kv_rank <= 512 ? 4 * kWarps : kWarps; }
 
 }  // namespace mla
