@@ -4,11 +4,13 @@ import json
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
 
 from tests import tree_util as tu
+from tests.test_tree_attention import Case
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 GPU = pytest.mark.gpu
@@ -99,3 +101,50 @@ def test_a_shared_tree_is_flagged_only_where_it_is_used(mla):
         err = torch.zeros(1, dtype=i32, device=D_)
         mla.tree_masks(bad, torch.tensor(lens, dtype=i32, device=D_), mask, pos, err)
         assert int(err) == bits
+
+
+# -------------------------------------------------------------------------------- decode_tree
+
+@GPU
+@pytest.mark.parametrize("kw", [dict(r=64, dr=128), dict(r=128, dr=64), dict(r=256, dr=256),
+                                dict(r=512, dr=256, dv=200), dict(r=1024, dr=256),
+                                dict(r=1024, dr=0, dv=600, T=60)], ids=str)
+def test_cuda_cores_at_each_kernels_largest_rows(mla, kw):
+    kw = dict(dict(T=20, dv=64), **kw)
+    Case(mla, 3, lens=[kw["T"] + 70, 0, kw["T"]], dtype="f32", dh=64, bs=16, kernel=mla.DECODE_SIMT,
+         **kw).run(mla)
+
+
+@GPU
+def test_calls_from_two_threads_at_sizes_of_their_own(mla):
+    """Two models whose calls use the same kernels with other amounts of shared memory, a thread, a
+    stream and a workspace each. Called without the interpreter's lock, as a C program would."""
+    cases = [Case(mla, 4, 2, [70], dtype="f32", r=256, dr=dr, dh=16, dv=dv, kernel=1, seed=dr)
+             for dr, dv in ((0, 45), (256, 60))]
+    ready = [c.device(mla) for c in cases]
+    mla.lib.mla_decode_tree  # loaded before the threads start
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    bad = [[], []]
+
+    def calls(k):
+        c, t = cases[k], ready[k]
+        args = (c.cfg.ref(), t["q"].data_ptr(), t["pool"].data_ptr(), t["table"].data_ptr(),
+                c.table.shape[1], c.pool.shape[0], t["lens"].data_ptr(), 1, 2, t["mask"].data_ptr(),
+                t["w_uv"].data_ptr(), t["ws"].data_ptr(), t["ws"].numel(), t["o"].data_ptr(),
+                t["lse"].data_ptr(), t["err"].data_ptr(), streams[k].cuda_stream)
+        for _ in range(5000):
+            st = mla.lib.mla_decode_tree(*args)
+            if st:
+                bad[k].append(st)
+
+    threads = [threading.Thread(target=calls, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert bad == [[], []], (len(bad[0]), len(bad[1]))
+    for c, t in zip(cases, ready):
+        assert int(t["err"]) == 0
+        c.check(t["o"], t["lse"])
