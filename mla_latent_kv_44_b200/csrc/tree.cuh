@@ -69,6 +69,14 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int
   return (p.mask[((size_t)b * p.T + t) * p.words + (node >> 5)] >> (node & 31)) & 1u;
 }
 
+// First chunk of range q of R over C chunks, floor(q C / R); a 32-bit division, which takes a fraction
+// of the time, where that is enough.
+__host__ __device__ __forceinline__ int first_chunk(int q, int R, int C) {
+  if (C < 1 << 25) return (int)((uint32_t)q * (uint32_t)C / (uint32_t)R);
+  return (int)((int64_t)q * C / R);
+}
+static_assert(kRanges <= 127, "q C below 2^32");
+
 cudaError_t launch_tree_simt(const mla_config& c, const TreeParams& p, const void* w_uv, void* o,
                              cudaStream_t st);
 int tree_simt_tile_rows(const mla_config& c);

@@ -352,14 +352,6 @@ __device__ int scan_chunks(int v, int* s_warp, int* total) {
   return v + before;
 }
 
-// First chunk of range q of R over C chunks (floor(q C / R), as range_start); a 32-bit division,
-// which takes a fraction of the time, where that is enough.
-__device__ __forceinline__ int first_chunk(int q, int R, int C) {
-  if (C < 1 << 25) return (int)((uint32_t)(q * C) / (uint32_t)R);  // q <= 74
-  return range_start(q, R, C);
-}
-static_assert(kRanges <= 127, "q C below 2^32");
-
 __device__ Range plan_range(const TreeParams& p, int range, int* s_plan, int* s_len) {
   const int tid = threadIdx.x, items = p.batch * p.groups;
   int* s_found = s_plan + 32;  // item, x
@@ -382,7 +374,8 @@ __device__ Range plan_range(const TreeParams& p, int range, int* s_plan, int* s_
   // A range holds two chunks at least, four where more would mean many partial results (each is
   // 256 KB): 8 tokens x 1000 rows took 32.4 us cut into single chunks, 32.0 into twos, 29.6 into
   // fours; 3 x 5 tokens of 16 heads x up to 1000 rows 28.9, 26.1 and 30.4.
-  const int R = min(p.ranges, max((C + 3) / 4, min((C + 1) / 2, 32 / p.team)));
+  const uint32_t c = (uint32_t)C;  // up to 2^31 - 1
+  const int R = min(p.ranges, (int)max((c + 3) / 4, min((c + 1) / 2, 32u / (uint32_t)p.team)));
   Range w{0, 0, 0, 0};
   // one CTA per range says whether an item that began in the range before goes on here
   const bool writer = range < p.ranges && (blockIdx.x & 1) == 0 && (blockIdx.x >> 1) % p.team == 0;

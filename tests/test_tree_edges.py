@@ -148,3 +148,31 @@ def test_calls_from_two_threads_at_sizes_of_their_own(mla):
     for c, t in zip(cases, ready):
         assert int(t["err"]) == 0
         c.check(t["o"], t["lse"])
+
+
+FIRST_CHUNK = r"""
+#include <cstdio>
+#include "tree.cuh"
+int main() {
+  const int counts[] = {1, 2, 73, 74, 75, 1000, 28999999, 29020050, 33554431, 33554432, 2147483647};
+  for (int C : counts)
+    for (int R = 1; R <= mla::kRanges && R <= C; ++R)
+      for (int q = 0; q <= R; ++q)
+        if (mla::first_chunk(q, R, C) != (int)((long long)q * C / R))
+          return std::printf("q %d R %d C %d: %d\n", q, R, C, mla::first_chunk(q, R, C)), 1;
+  return 0;
+}
+"""
+
+
+def test_ranges_begin_where_they_should_at_any_number_of_chunks(mla, tmp_path):
+    """On the host, with signed overflow trapped: 74 ranges of 2^25 chunks pass 2^31 on the way."""
+    from mla_latent_kv_44_b200 import build
+
+    src, exe = tmp_path / "first_chunk.cu", tmp_path / "first_chunk"
+    src.write_text(FIRST_CHUNK)
+    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "-O1", "--expt-relaxed-constexpr", "-Xcompiler",
+                    "-fsanitize=signed-integer-overflow,-fsanitize-undefined-trap-on-error", "-I", build.INCLUDE,
+                    "-I", build.CSRC, str(src), "-o", str(exe)], check=True, capture_output=True, timeout=300)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, (out.returncode, out.stdout)
