@@ -485,7 +485,8 @@ MLA_API size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t bat
  * reach that node's result, whatever it holds (NaN, infinities, a row never written). A node
  * that attends nothing gets o = 0 and lse = -inf, and so does every node of an empty sequence
  * (seq_lens[b] = 0); a length in (0, T), above max_blocks * block_size or above 2^31 - 8193 does
- * too and sets MLA_DEV_BAD_LENGTH. q, pool, w_uv and o must be 16-byte aligned. Deterministic.
+ * too and sets MLA_DEV_BAD_LENGTH. The rows of a block whose id is outside the pool are attended by
+ * nobody, and MLA_DEV_OOB_BLOCK is set. q, pool, w_uv and o must be 16-byte aligned. Deterministic.
  * decode_kernel chooses as in mla_decode: the tensor-core kernel needs bf16, r = 512, d_r = 64 and
  * a block_size that is a multiple of 64, and takes any H. Between the attention and W_UV that path
  * keeps the latent sums as two bf16 terms (16 bits), the other in fp32.

@@ -259,7 +259,8 @@ struct TileWalk {
 };
 
 // First pool row of a sequence's 64-row chunks, 32 table entries read at a time: lane i holds
-// that of chunk base + i. Blocks outside the pool are flagged at use and replaced by block 0.
+// that of chunk base + i. Blocks outside the pool are flagged at use; in place of their rows the
+// load takes the rows in front of the pool, which read as zeros, and nobody sees them (InPool).
 struct RowWindow {
   int b = -1, base = 0, blk = 0;
   __device__ int get(const TreeParams& p, int seq, int chunk, int lane) {
@@ -270,12 +271,29 @@ struct RowWindow {
       base = at;
       blk = at + lane < p.max_blocks ? p.table[(size_t)seq * p.max_blocks + at + lane] : 0;
     }
-    int id = __shfl_sync(0xffffffffu, blk, at - base);
+    const int id = __shfl_sync(0xffffffffu, blk, at - base);
     if (id < 0 || id >= p.num_blocks) {
       if (lane == 0) set_error(p.err, MLA_DEV_OOB_BLOCK);
-      id = 0;
+      return -kRows;
     }
     return id * p.bs + (chunk - at * per) * kRows;
+  }
+};
+
+// Whether a sequence's 64-row chunks lie in the pool, looked up for 32 at a time.
+struct InPool {
+  int b = -1, base = 0;
+  uint32_t in = 0;  // bit i: chunk base + i
+  // bit i: chunk + i, for a tile's chunks (those behind the table count as in the pool)
+  __device__ uint32_t get(const TreeParams& p, int seq, int chunk, int lane) {
+    if (seq != b || chunk < base || chunk + kTileBlocks > base + 32) {  // warp-uniform
+      b = seq;
+      base = chunk;
+      const int at = (chunk + lane) / (p.bs / kRows);
+      const int id = at < p.max_blocks ? p.table[(size_t)seq * p.max_blocks + at] : 0;
+      in = __ballot_sync(0xffffffffu, id >= 0 && id < p.num_blocks);
+    }
+    return in >> (chunk - base);
   }
 };
 
@@ -550,13 +568,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
     const uint32_t s_free = peer_addr(bar(kSFree), 0), p_ready = peer_addr(bar(kPReady), 0);
     int t = 0, seg = 0;
     float m_ref = 0.f, l = 0.f;
+    InPool pool;
     while (has) {
       const int my_row = cur.row0 + kMH * (int)rank + row;  // of the sequence's T * H
       const int hb = cur.half_blocks();
       const int key0 = half * hb * kRows;  // this thread's first key of the tile
       const int lim = min(cur.ntok - key0, hb * kRows);
       const int node0 = cur.chunk * kRows + key0 - (cur.len - p.T);  // drafted node of column 0
-      const bool masked = lim < 128 || node0 + 127 >= 0;
+      // this thread's blocks of keys that are in the pool
+      const uint32_t in = pool.get(p, cur.b, cur.chunk, lane) >> (half * hb);
+      const bool masked = lim < 128 || node0 + 127 >= 0 || (in & 3) != 3;
       uint32_t seen[4];
       if (masked) {
         const int tok = min(my_row / p.H, p.T - 1);
@@ -564,7 +585,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant_
         for (int w = 0; w < 4; ++w) {
           const int left = lim - 32 * w;
           const uint32_t bits = left <= 0 ? 0u : seen_word(p, cur.b, tok, node0 + 32 * w);
-          seen[w] = left <= 0 ? 0u : left < 32 ? bits & ((1u << left) - 1) : bits;
+          seen[w] = left <= 0 || !(in >> (w >> 1) & 1) ? 0u
+                    : left < 32 ? bits & ((1u << left) - 1) : bits;
         }
       }
       if (!wait(bar(kSFull + (t & 1)), (t >> 1) & 1, ctl)) break;

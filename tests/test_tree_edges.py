@@ -176,3 +176,41 @@ def test_ranges_begin_where_they_should_at_any_number_of_chunks(mla, tmp_path):
                     "-I", build.CSRC, str(src), "-o", str(exe)], check=True, capture_output=True, timeout=300)
     out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, (out.returncode, out.stdout)
+
+
+@GPU
+@pytest.mark.parametrize("kernel,bs", [(1, 64), (1, 16), (2, 64), (2, 128), (2, 320)])
+def test_rows_of_a_block_outside_the_pool_are_left_out(mla, kernel, bs):
+    """Flagged, and attended by nobody: no other request's rows come in their place (block 0 holds NaN
+    here), in the prefix or among the drafted rows, for one block or for all."""
+    T = 6
+    c = Case(mla, 16, T, [900, 700, 64, 330, 2000], bs=bs, kernel=kernel, seed=3)
+    spare = sorted(set(range(c.pool.shape[0])) - set(c.table.flatten().tolist()))[0]
+    c.table[c.table == 0] = spare                    # nobody's block 0
+    c.pool[0] = float("nan")
+    gone = [{0}, {2, 700 // bs}, {63 // bs}, set(), set(range(-(-2000 // bs)))]
+    ids = [c.pool.shape[0], -1, 2 ** 31 - 1, -2 ** 31]
+    was = c.table.clone()
+    for b, blocks in enumerate(gone):
+        for i, k in enumerate(sorted(blocks)):
+            c.table[b, k] = ids[(b + i) % 4]
+    t = c.device(mla)
+    c.call(mla, t)
+    assert int(t["err"]) == mla.DEV_OOB_BLOCK
+    o, lse = t["o"].cpu().double(), t["lse"].cpu().double()
+    for b, n in enumerate(c.lens):
+        rows = c.pool[was[b].long()].reshape(-1, c.D)[:n]
+        out = torch.tensor([j // bs in gone[b] for j in range(n)])
+        seen = c.seen[b] & ~out[n - T:]
+        keep = ~out
+        keep[n - T:] = True
+        at = slice(b * T, (b + 1) * T)
+        if out.all():
+            assert (lse[at] == -float("inf")).all() and (o[at] == 0).all(), b
+            continue
+        want, wl, size, dot = tu.attend(c.q[at], rows[keep], seen, c.w_uv, c.r, c.scale)
+        tol, tol_l = tu.tolerances(c.cfg.torch_dtype, want, size, dot, c.D, n)
+        none = torch.isinf(wl)
+        assert (lse[at][none] == -float("inf")).all() and (o[at][none] == 0).all(), b
+        assert ((o[at] - want).abs() <= tol).all(), b
+        assert ((lse[at] - wl).abs() <= tol_l)[~none].all(), b
