@@ -454,12 +454,13 @@ MLA_API mla_status mla_tree_masks(const int32_t* parents, int32_t parents_batch,
  * block * block_size + row in block, as mla_build_tables gives them). The position and the place
  * are apart: a drafted token's position comes from its depth. A negative slot is skipped (a
  * step's padding); one outside the pool sets MLA_DEV_OOB_BLOCK and is skipped. Slots must differ:
- * of two tokens with one slot either's values may stay. ckv_raw (n_tokens, r), krope_raw
+ * of two tokens with one slot pieces of either's row may stay. ckv_raw (n_tokens, r), krope_raw
  * (n_tokens, d_r), pool (num_blocks, block_size, r + d_r) dtype; gamma (r) float32; pos
  * (n_tokens) int32; slots (n_tokens) int64. ckv_raw, gamma and pool must be 16-byte aligned,
  * krope_raw 8-byte.
- * fp32 statistics, angles in double; the sum of squares is taken in another order than
- * mla_append_latent's, so a value may round the other way.
+ * fp32 statistics, angles in double. Differences from mla_append_latent: the sum of squares is taken
+ * in another order, so a value may round the other way; and in bf16 pools the sine and cosine of the
+ * (double) angle are fp32's, 2^-22 or so off, where it takes double's.
  */
 MLA_API mla_status mla_append_slots(const mla_config* cfg, const void* ckv_raw,
                                     const void* krope_raw, const float* gamma, const int32_t* pos,

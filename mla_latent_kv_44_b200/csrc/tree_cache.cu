@@ -6,9 +6,14 @@
 // the place are two inputs here. One warp per row, rows dealt round the grid: a lane holds up to
 // NP 16-byte pieces of the row (coalesced across the warp), fp32 statistics by a butterfly. The
 // angles are p * theta_i in double, as everywhere in the library, and are brought into [-pi, pi]
-// in double (Cody and Waite's two-term reduction); their sine and cosine are then taken in fp32,
-// 1e-7 off at most. theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a double
-// pow per lane, and sincos in double, took most of the 16 us that 16,384 rows needed.
+// in double (Cody and Waite's two-term reduction; exact to a rounding while the angle's turns are
+// whole numbers of a double, any position for rope_base >= 1). An fp32 pool then gets the rotation in
+// double, rounded once, as mla_append_latent does it. For a bf16 pool, whose rounding is 2^-8, sine
+// and cosine are taken in fp32, off by 2^-23 for the angle rounded to fp32 and 2^-22 for sincosf:
+// 16,384 rows of 512 take 10.9 us instead of 11.9 from HBM, 8.0 instead of 9.2 from L2 (fp32 rows,
+// in double, 14.0 and 8.7). theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a
+// double pow per lane, and sincos of the whole angle in double, took most of the 16 us that 16,384
+// bf16 rows needed.
 // What bounds it: HBM and its latency for prompts (the row in and out: 16,384 tokens, 37.9 MB, 10.5
 // us or 3.6 TB/s from HBM, 7.7 with the rows in L2; a warp has a row and the next in flight),
 // latency for a decode step (128 tokens: 2.5 us).
@@ -126,9 +131,16 @@ append_slots_kernel(const T* __restrict__ ckv, const T* __restrict__ kr,
       const double a = p * (i < 32 ? theta0 : theta.t[i]);
       const double turns = rint(a * 0.15915494309189535);  // 1 / (2 pi)
       const double red = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, a));
-      float c, s;
-      sincosf((float)red, &s, &c);
-      store2(dst + r + 2 * i, x.x * c - x.y * s, x.x * s + x.y * c);
+      if constexpr (sizeof(T) == 4) {
+        double c, s;
+        sincos(red, &s, &c);
+        store2(dst + r + 2 * i, (float)((double)x.x * c - (double)x.y * s),
+               (float)((double)x.x * s + (double)x.y * c));
+      } else {
+        float c, s;
+        sincosf((float)red, &s, &c);
+        store2(dst + r + 2 * i, x.x * c - x.y * s, x.x * s + x.y * c);
+      }
     }
     float ss = 0.f;
 #pragma unroll
@@ -163,11 +175,13 @@ cudaError_t append_slots_go(const mla_config& c, const void* ckv, const void* kr
                             void* pool, int num_blocks, int n, uint32_t* err, cudaStream_t st) {
   const int grid = std::min((n + kAppendWarps - 1) / kAppendWarps, 148 * append_ctas(NP));
   RopeTheta theta = {};
-  // by products: the error of the 128th is 1e-14 of it, 3e-9 in any angle
+  // by products in the longest type (64 bits of mantissa): rounded to double, each theta is off by
+  // 2^-53 of itself, and so is its angle by another, 2^-52 in all: 4.8e-7 at position 2^31, 2.3e-10 at
+  // 2^20
   if (c.rope_dim > 0) {
-    const double step = std::pow((double)c.rope_base, -2.0 / c.rope_dim);
-    double t = 1.0;
-    for (int i = 0; i < c.rope_dim / 2; ++i, t *= step) theta.t[i] = t;
+    const long double step = std::pow((long double)c.rope_base, -2.0L / c.rope_dim);
+    long double t = 1.0L;
+    for (int i = 0; i < c.rope_dim / 2; ++i, t *= step) theta.t[i] = (double)t;
   }
   return launch_pdl(append_slots_kernel<T, NP>, dim3(grid), dim3(kAppendWarps * 32), 0, st,
                     (const T*)ckv, (const T*)kr, gamma, pos, slots, (T*)pool,

@@ -6,6 +6,7 @@ import subprocess
 import sys
 import threading
 
+import numpy as np
 import pytest
 import torch
 
@@ -214,3 +215,59 @@ def test_rows_of_a_block_outside_the_pool_are_left_out(mla, kernel, bs):
         assert (lse[at][none] == -float("inf")).all() and (o[at][none] == 0).all(), b
         assert ((o[at] - want).abs() <= tol).all(), b
         assert ((lse[at] - wl).abs() <= tol_l)[~none].all(), b
+
+
+# ------------------------------------------------------------------------------- append_slots
+
+def _rotated(kr, pos, base):
+    """Rotated keys in the host's longest floating type, and the angles."""
+    dr = kr.shape[1]
+    i = np.arange(dr // 2, dtype=np.longdouble)
+    theta = np.longdouble(base) ** (-2 * i / dr)
+    a = pos.numpy().astype(np.longdouble)[:, None] * theta
+    x = kr.double().numpy().astype(np.longdouble)
+    x0, x1 = x[:, 0::2], x[:, 1::2]
+    out = np.stack([x0 * np.cos(a) - x1 * np.sin(a), x0 * np.sin(a) + x1 * np.cos(a)], -1)
+    size = np.repeat(abs(x0) + abs(x1), 2, axis=1)
+    return out.reshape(kr.shape), size, np.repeat(abs(a), 2, axis=1)
+
+
+@GPU
+@pytest.mark.parametrize("dr,base", [(64, 10000.0), (256, 10000.0), (32, 500000.0), (8, 10000.0)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rotated_keys_at_near_and_far_positions(mla, dr, base, dtype):
+    """The angle is a product in double: off by 2^-53 for the frequency's rounding and 2^-53 for its
+    own, of its size. An fp32 pool holds the key rounded once from double, as mla_append_latent writes
+    it; for a bf16 pool sine and cosine are taken in fp32 (2^-23 for the angle's rounding there, 2^-22
+    for CUDA's sincosf, of 2 ulp at most) and combined in two roundings, 2^-23."""
+    n, r, bs = 96, 32, 8
+    cfg = mla.Config(16, 64, r, dr, bs, dtype=dtype, rope_base=base)
+    dt, g = cfg.torch_dtype, torch.Generator().manual_seed(dr)
+    ckv, kr = torch.randn(n, r, generator=g).to(dt), torch.randn(n, dr, generator=g).to(dt)
+    top = torch.tensor([0, 1, 2 ** 31 - 1, 2 ** 31 - 2, 2 ** 24 + 1, 2 ** 30 + 7])
+    pos = torch.cat([top, torch.randint(0, 2 ** 17, (n - 6,), generator=g)]).int()
+    d = lambda x: x.to(D_)  # noqa: E731
+    err, gamma = torch.zeros(1, dtype=torch.int32, device=D_), torch.ones(r, device=D_)
+    pool = torch.zeros(n // bs, bs, r + dr, dtype=dt, device=D_)
+    mla.append_slots(cfg, d(ckv), d(kr), gamma, d(pos), torch.arange(n, device=D_), pool, err)
+    assert int(err) == 0
+    got = pool.view(n, r + dr)[:, r:].cpu().double().numpy()
+    want, size, angle = _rotated(kr, pos, base)
+    work = 2.0 ** -23 + 2.0 ** -22 + 2.0 ** -23 if dtype == "bf16" else 0.0
+    step = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    tol = step * abs(want) + (angle * 2.0 ** -52 + 2.0 ** -32 + work) * size
+    assert (abs(got - want) <= tol).all(), float((abs(got - want) / tol).max())
+    # the same rows through a table
+    short = pos.clone()
+    short[:6] = torch.arange(6) + 2 ** 17
+    table = torch.zeros(n, 2 ** 17 // bs + 1, dtype=torch.int32, device=D_)
+    table[:] = d(torch.arange(n // bs).repeat_interleave(bs).int())[:, None]
+    short = (short // bs * bs + torch.arange(n) % bs).int()  # row n % bs of block n / bs
+    pools = [torch.zeros_like(pool) for _ in range(2)]
+    mla.append_slots(cfg, d(ckv), d(kr), gamma, d(short), torch.arange(n, device=D_), pools[0], err)
+    mla.append_latent(cfg, d(ckv), d(kr), gamma, torch.arange(n, dtype=torch.int32, device=D_), d(short),
+                      table, pools[1], err)
+    assert int(err) == 0
+    a, b = (p.view(n, r + dr)[:, r:].cpu() for p in pools)
+    if dtype == "f32":  # both round one double, whose last bit may differ: one value in 10^8
+        assert int((a != b).sum()) <= 1
