@@ -7,17 +7,22 @@ then the objects link into mla_latent_kv_44_b200/libmla.so with the CUDA runtime
 statically, so the library loads on a machine without a GPU (calls then fail with
 MLA_ERR_CUDA) and needs nothing at run time but the NVIDIA driver. A second library,
 libmla_testhook.so, differs only in a test define of the attention kernels (one K load of the first
-work range is left out in each); only the tests load it.
+work range is left out in each); only the tests load it. _fast_call.so, through which the Python
+binding makes the tree calls, is compiled by g++ against torch's headers; where torch is missing the
+libraries are built without it.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -57,22 +62,38 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _read(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
+def fast_identity() -> str | None:
+    """What the binding's compiled module is built for: this Python and torch (whose C++ interface
+    changes with its version). None where one of the things that it needs is missing."""
+    spec = importlib.util.find_spec("torch")
+    headers = sysconfig.get_paths()["include"]
+    if (spec is None or not os.path.exists(os.path.join(headers, "Python.h")) or
+            not shutil.which(os.environ.get("CXX", "g++"))):
+        return None
+    return f"torch {importlib.metadata.version('torch')} {spec.origin}\npython {sys.version}\n"
+
+
 def fast_command():
     """The g++ command of the binding's compiled module."""
-    import sysconfig
-
     import torch
-    from torch.utils import cpp_extension
 
-    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    api = os.path.join(root, "include", "torch", "csrc", "api", "include")
     includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
-                *cpp_extension.include_paths()]
+                os.path.join(root, "include"), api]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
             "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            *(f"-I{d}" for d in includes), FAST_SOURCE, "-o", FAST_LIB, f"-L{lib_dir}",
-            f"-Wl,-rpath,{lib_dir}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+            *(f"-I{d}" for d in includes), FAST_SOURCE, "-o", FAST_LIB, f"-L{root}/lib",
+            f"-Wl,-rpath,{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -99,8 +120,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         else:
             test_objs.append(obj)
 
-    if force or _stale(FAST_LIB, [FAST_SOURCE] + headers):
-        jobs.append(fast_command())
+    # built for this torch and Python, as the note beside the objects says
+    fast, fast_note = fast_identity(), os.path.join(BUILD, "fast_call.txt")
+    fast_job = None
+    if fast is None:
+        sys.stderr.write("torch, Python's headers or a C++ compiler is missing: the library is built, "
+                         "_fast_call.so (the tree calls from Python) is not\n")
+    elif force or _stale(FAST_LIB, [FAST_SOURCE] + headers) or _read(fast_note) != fast:
+        fast_job = fast_command()
 
     def run(cmd):
         if verbose:
@@ -108,13 +135,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         p = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, p
 
-    failed = []
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        for cmd, p in ex.map(run, jobs):
+    failed, fast_failed = [], False
+    todo = jobs + ([fast_job] if fast_job else [])
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as ex:
+        for cmd, p in ex.map(run, todo):
             if p.returncode != 0 or ptxas_info or verbose:
                 sys.stderr.write(p.stdout + p.stderr)
-            if p.returncode != 0:
-                failed.append(FAST_SOURCE if FAST_SOURCE in cmd else cmd[-3])
+            if cmd is fast_job:
+                fast_failed = p.returncode != 0
+            elif p.returncode != 0:
+                failed.append(cmd[-3])
+    if fast_job and not fast_failed:
+        with open(fast_note, "w") as f:
+            f.write(fast)
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
     for lib, parts in ((LIB, objs), (TEST_LIB, test_objs)):
@@ -125,6 +158,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             p = subprocess.run(cmd, capture_output=True, text=True)
             if p.returncode != 0:
                 raise RuntimeError("link failed:\n" + p.stdout + p.stderr)
+    if fast_failed:
+        raise RuntimeError(f"{LIB} is built, but {FAST_SOURCE} does not compile")
     return LIB
 
 
