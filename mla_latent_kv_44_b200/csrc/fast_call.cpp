@@ -72,9 +72,12 @@ struct Args {
     if (v != static_cast<int>(v)) ok = false;
     return static_cast<int>(v);
   }
+  // the stream's handle; what is none (not a number, or no pointer holds it) leaves Python's error
   void* stream(int i) {
     if (a[i] == Py_None) return c10::cuda::getCurrentCUDAStream(dev).stream();
-    return PyLong_AsVoidPtr(a[i]);
+    void* const handle = PyLong_AsVoidPtr(a[i]);
+    if (!handle && PyErr_Occurred()) ok = false;
+    return handle;
   }
   // checks done: the call may go out
   bool elsewhere() const { return c10::cuda::current_device() != dev; }
@@ -117,8 +120,10 @@ PyObject* build_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto* p13 = g.data<int32_t>(13, kI32, {1});
   if (!g.ok) return status(kRefused);
   if (g.elsewhere()) return status(kOtherDevice);
+  void* const stream = g.stream(14);
+  if (!g.ok) return status(kRefused);
   return status(g_build_tables(c, p1, p2, b, p3, width, p4, p5, p6, blocks, p7, p8, p9, p10, p11,
-                               p12, tokens, (uint32_t*)p13, g.stream(14)));
+                               p12, tokens, (uint32_t*)p13, stream));
 }
 
 // parents, seq_lens, mask, pos, dev_err, stream
@@ -135,7 +140,9 @@ PyObject* tree_masks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto* p4 = g.data<int32_t>(4, kI32, {1});
   if (!g.ok) return status(kRefused);
   if (g.elsewhere()) return status(kOtherDevice);
-  return status(g_tree_masks(p0, rows, p1, b, T, (uint32_t*)p2, p3, (uint32_t*)p4, g.stream(5)));
+  void* const stream = g.stream(5);
+  if (!g.ok) return status(kRefused);
+  return status(g_tree_masks(p0, rows, p1, b, T, (uint32_t*)p2, p3, (uint32_t*)p4, stream));
 }
 
 // cfg, ckv_raw, krope_raw, gamma, pos, slots, pool, dev_err, stream
@@ -156,7 +163,9 @@ PyObject* append_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto* p7 = g.data<int32_t>(7, kI32, {1});
   if (!g.ok) return status(kRefused);
   if (g.elsewhere()) return status(kOtherDevice);
-  return status(g_append_slots(c, p1, p2, p3, p4, p5, p6, blocks, m, (uint32_t*)p7, g.stream(8)));
+  void* const stream = g.stream(8);
+  if (!g.ok) return status(kRefused);
+  return status(g_append_slots(c, p1, p2, p3, p4, p5, p6, blocks, m, (uint32_t*)p7, stream));
 }
 
 // cfg, q, pool, block_table, seq_lens, q_per_seq, tree_mask, w_uv, workspace, o, lse, dev_err,
@@ -184,8 +193,10 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto* p11 = g.data<int32_t>(11, kI32, {1});
   if (!g.ok) return status(kRefused);
   if (g.elsewhere()) return status(kOtherDevice);
+  void* const stream = g.stream(12);
+  if (!g.ok) return status(kRefused);
   return status(g_decode_tree(c, p1, p2, p3, width, blocks, p4, b, T, (const uint32_t*)p6, p7, p8,
-                              ws->size(0), p9, p10, (uint32_t*)p11, g.stream(12)));
+                              ws->size(0), p9, p10, (uint32_t*)p11, stream));
 }
 
 // cfg, path, path_len, q_per_seq, block_table, pool, seq_lens, seq_lens_out, dev_err, stream
@@ -208,8 +219,10 @@ PyObject* commit_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto* p8 = g.data<int32_t>(8, kI32, {1});
   if (!g.ok) return status(kRefused);
   if (g.elsewhere()) return status(kOtherDevice);
+  void* const stream = g.stream(9);
+  if (!g.ok) return status(kRefused);
   return status(g_commit_tree(c, p1, p2, steps, T, p4, width, p5, blocks, p6, p7, b, (uint32_t*)p8,
-                              g.stream(9)));
+                              stream));
 }
 
 // name, address of the library's function

@@ -271,3 +271,33 @@ def test_rotated_keys_at_near_and_far_positions(mla, dr, base, dtype):
     a, b = (p.view(n, r + dr)[:, r:].cpu() for p in pools)
     if dtype == "f32":  # both round one double, whose last bit may differ: one value in 10^8
         assert int((a != b).sum()) <= 1
+
+
+# ------------------------------------------------------------------------------------ binding
+
+@GPU
+def test_a_stream_that_is_none_launches_nothing(mla):
+    """A handle that no pointer holds: refused before the launch, by every call."""
+    i32, bad = torch.int32, 1 << 70
+    z = lambda *s, t=i32: torch.full(s, -7, dtype=t, device=D_)  # noqa: E731
+    one, cfg = torch.ones(1, dtype=i32, device=D_), mla.Config(2, 32, 64, 32, 8, dtype="f32")
+    f32 = torch.float32
+    pool, table, err = z(2, 8, 96, t=f32), torch.zeros(1, 1, dtype=i32, device=D_), torch.zeros_like(one)
+    ws = torch.zeros(mla.decode_tree_workspace_size(cfg, 1, 1), dtype=torch.uint8, device=D_)
+    outs = dict(cu=z(2), seq=z(1), pos=z(1), slots=z(1, t=torch.int64), held=z(1), count=z(1), mask=z(1, 1),
+                tpos=z(1), pool=pool, o=z(1, 2, 32, t=f32), lens=z(1))
+    was = {k: v.clone() for k, v in outs.items()}
+    for call in (
+            lambda: mla.build_tables(cfg, one, one, table, one, z(2), one, outs["held"], outs["count"],
+                                     outs["cu"], outs["seq"], outs["pos"], outs["slots"], err, bad),
+            lambda: mla.tree_masks(z(1, 1), one, outs["mask"], outs["tpos"], err, bad),
+            lambda: mla.append_slots(cfg, z(1, 64, t=f32), z(1, 32, t=f32), z(64, t=f32), one,
+                                     torch.zeros(1, dtype=torch.int64, device=D_), pool, err, bad),
+            lambda: mla.decode_tree(cfg, z(1, 2, 96, t=f32), pool, table, one, 1, None, z(2, 32, 64, t=f32),
+                                    ws, outs["o"], None, err, bad),
+            lambda: mla.commit_tree(cfg, torch.zeros(1, 1, dtype=i32, device=D_), one, 1, table, pool, one,
+                                    outs["lens"], err, bad)):
+        with pytest.raises(OverflowError):
+            call()
+    torch.cuda.synchronize()
+    assert int(err) == 0 and all(torch.equal(outs[k], was[k]) for k in outs)
