@@ -467,7 +467,8 @@ MLA_API mla_status mla_append_slots(const mla_config* cfg, const void* ckv_raw,
                                     const int64_t* slots, void* pool, int32_t num_blocks,
                                     int32_t n_tokens, uint32_t* dev_err, void* stream);
 
-/* Workspace of mla_decode_tree in bytes (0 for an invalid configuration); 256-byte aligned. */
+/* Workspace of mla_decode_tree in bytes (0 for an invalid configuration and for the sizes that the call
+ * refuses); 256-byte aligned. */
 MLA_API size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t batch,
                                               int32_t q_per_seq);
 

@@ -480,6 +480,8 @@ def append_slots(cfg: Config, ckv_raw, krope_raw, gamma, pos, slots, pool, dev_e
 
 
 def decode_tree_workspace_size(cfg: Config, batch: int, q_per_seq: int) -> int:
+    if not (0 < batch < 1 << 31 and 0 < q_per_seq < 1 << 31):  # ctypes takes numbers modulo 2^32
+        return 0
     return int(lib.mla_decode_tree_workspace_size(cfg.ref(), batch, q_per_seq))
 
 

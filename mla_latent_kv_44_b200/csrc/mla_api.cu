@@ -556,7 +556,11 @@ TreeLayout tree_layout(const mla_config& c, int batch, int T) {
   return L;
 }
 
-bool tree_shape_ok(int32_t batch, int32_t T) { return batch >= 1 && T >= 1 && T <= MLA_MAX_TREE; }
+// The drafted tokens and query rows that mla_decode_tree can number.
+bool tree_shape_ok(const mla_config& c, int32_t batch, int32_t T) {
+  return T <= MLA_MAX_TREE && (int64_t)batch * T <= (1 << 24) &&
+         (int64_t)batch * T * c.num_heads <= (1 << 28);
+}
 
 }  // namespace
 
@@ -617,8 +621,8 @@ mla_status mla_append_slots(const mla_config* cfg, const void* ckv_raw, const vo
 }
 
 size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t batch, int32_t q_per_seq) {
-  if (!valid_config(cfg) || !tree_shape_ok(batch, q_per_seq)) return 0;
-  if ((int64_t)batch * q_per_seq * cfg->num_heads > (1 << 28)) return 0;
+  if (!valid_config(cfg) || batch < 1 || q_per_seq < 1) return 0;
+  if (!tree_shape_ok(*cfg, batch, q_per_seq)) return 0;
   return tree_layout(*cfg, batch, q_per_seq).total;
 }
 
@@ -633,10 +637,7 @@ mla_status mla_decode_tree(const mla_config* cfg, const void* q, const void* poo
   if (!q || !pool || !block_table || !seq_lens || !w_uv || !workspace || !o || !dev_err)
     return MLA_ERR_INVALID_ARG;
   if (max_blocks < 1 || num_blocks < 1) return MLA_ERR_INVALID_ARG;
-  if (q_per_seq > MLA_MAX_TREE ||
-      (int64_t)batch * q_per_seq * cfg->num_heads > (1 << 28) ||
-      (int64_t)batch * q_per_seq > (1 << 24))
-    return MLA_ERR_UNSUPPORTED;
+  if (!tree_shape_ok(*cfg, batch, q_per_seq)) return MLA_ERR_UNSUPPORTED;
   if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(w_uv, 16) || !aligned(o, 16))
     return MLA_ERR_INVALID_ARG;
   const mla_config& c = *cfg;

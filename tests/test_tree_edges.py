@@ -301,3 +301,11 @@ def test_a_stream_that_is_none_launches_nothing(mla):
             call()
     torch.cuda.synchronize()
     assert int(err) == 0 and all(torch.equal(outs[k], was[k]) for k in outs)
+
+
+def test_no_workspace_size_for_what_the_call_refuses(mla):
+    size, cfg = mla.decode_tree_workspace_size, mla.Config(1, 32, 64, 32, 8)
+    assert size(cfg, 1 << 24, 1) > 0 and size(cfg, 1 << 16, 256) > 0
+    assert size(cfg, (1 << 24) + 1, 1) == 0 and size(cfg, 1 << 17, 256) == 0
+    for n in (2 ** 32 + 1, -2 ** 32 + 1, 2 ** 63):      # not taken modulo 2^32
+        assert size(cfg, n, 4) == 0 and size(cfg, 1, n) == 0
