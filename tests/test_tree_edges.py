@@ -172,9 +172,10 @@ def test_ranges_begin_where_they_should_at_any_number_of_chunks(mla, tmp_path):
 
     src, exe = tmp_path / "first_chunk.cu", tmp_path / "first_chunk"
     src.write_text(FIRST_CHUNK)
+    trap = "-fsanitize=signed-integer-overflow,-fsanitize-undefined-trap-on-error"
     subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "-O1", "--expt-relaxed-constexpr", "-Xcompiler",
-                    "-fsanitize=signed-integer-overflow,-fsanitize-undefined-trap-on-error", "-I", build.INCLUDE,
-                    "-I", build.CSRC, str(src), "-o", str(exe)], check=True, capture_output=True, timeout=300)
+                    trap, "-I", build.INCLUDE, "-I", build.CSRC, str(src), "-o", str(exe)],
+                   check=True, capture_output=True, timeout=300)
     out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, (out.returncode, out.stdout)
 
@@ -309,3 +310,72 @@ def test_no_workspace_size_for_what_the_call_refuses(mla):
     assert size(cfg, (1 << 24) + 1, 1) == 0 and size(cfg, 1 << 17, 256) == 0
     for n in (2 ** 32 + 1, -2 ** 32 + 1, 2 ** 63):      # not taken modulo 2^32
         assert size(cfg, n, 4) == 0 and size(cfg, 1, n) == 0
+
+
+# ----------------------------------------------------------------------------- far offsets
+
+@GPU
+def test_tables_whose_slots_pass_32_bits(mla):
+    bs, blocks, i32 = 1 << 12, 1 << 20, torch.int32
+    cfg = mla.Config(16, 64, 64, 32, bs)
+    t = lambda *x: torch.tensor(x, dtype=i32, device=D_)  # noqa: E731
+    free = torch.arange(blocks, dtype=i32, device=D_)
+    for tokens in (6, 40000):                        # one launch, and a slot map of its own
+        lens, count, held = t(bs + 5, 0, 30000), t(blocks), t(0, 0, 0)
+        table, err = torch.full((3, 8), -1, dtype=i32, device=D_), t(0)
+        new = t(3, 0, 3) if tokens == 6 else t(bs + 5, 0, 30000)
+        cu, seq, pos = torch.zeros(4, dtype=i32, device=D_), *torch.zeros(2, tokens, dtype=i32, device=D_)
+        slots = torch.zeros(tokens, dtype=torch.int64, device=D_)
+        mla.build_tables(cfg, lens, new, table, held, free, count, held, count, cu, seq, pos, slots, err)
+        assert int(err) == 0 and held.tolist() == [2, 0, 8] and int(count) == blocks - 10
+        n = int(cu[-1])
+        assert n == int(new.sum())
+        want = table[seq[:n].long(), (pos[:n] // bs).long()].long() * bs + pos[:n] % bs
+        assert torch.equal(slots[:n], want) and int(slots.max()) > 1 << 31
+        assert (slots[n:] == -1).all() and table[0, :2].tolist() == [blocks - 1, blocks - 2]
+
+
+@GPU
+@pytest.mark.parametrize("dtype,kernel", [("bf16", 1), ("bf16", 2), ("f32", 1)])
+def test_a_pool_of_more_than_2_to_31_values(mla, dtype, kernel):
+    """Rows written, attended and moved at the pool's end, in a sequence that also has its begin."""
+    bs, T, H, n = 64, 5, 4, 700
+    cfg = mla.Config(H, 64, 512, 64, bs, dtype=dtype, decode_kernel=kernel)
+    dt, i32, blocks = cfg.torch_dtype, torch.int32, 2 ** 31 // (64 * 576) + 50
+    c = Case(mla, H, T, [n], dtype=dtype, dh=64, kernel=kernel, seed=4)
+    pool = torch.empty(blocks, bs, 576, dtype=dt, device=D_)
+    table = torch.arange(blocks - 1, blocks - 1 - c.table.shape[1], -1, dtype=i32, device=D_).view(1, -1)
+    table[0, 1] = 0
+    flat = pool.view(-1, 576)
+    at = torch.tensor([int(table[0, j // bs]) * bs + j % bs for j in range(n)], device=D_)
+    flat[at] = c.rows(0).to(D_)
+    # the drafted rows again, by slots
+    g = torch.Generator().manual_seed(1)
+    ckv, kr = torch.randn(T, 512, generator=g).to(dt).to(D_), torch.randn(T, 64, generator=g).to(dt).to(D_)
+    err, pos = torch.zeros(1, dtype=i32, device=D_), torch.arange(T, dtype=i32, device=D_)
+    gamma = torch.ones(512, device=D_)
+    mla.append_slots(cfg, ckv, kr, gamma, pos, at[n - T:], pool, err)
+    small = torch.zeros(1, bs, 576, dtype=dt, device=D_)
+    mla.append_slots(cfg, ckv, kr, gamma, pos, torch.arange(T, device=D_), small, err)
+    assert torch.equal(flat[at[n - T:]], small[0, :T])
+    flat[at] = c.rows(0).to(D_)
+    t = c.device(mla)
+    lens = torch.tensor([n], dtype=i32, device=D_)
+    mla.decode_tree(cfg, t["q"], pool, table, lens, T, t["mask"], t["w_uv"], t["ws"], t["o"], t["lse"], err)
+    assert int(err) == 0
+    c.check(t["o"], t["lse"])
+    out = torch.zeros(1, dtype=i32, device=D_)
+    mla.commit_tree(cfg, torch.tensor([[0, 2, 4]], dtype=i32, device=D_),
+                    torch.tensor([3], dtype=i32, device=D_), T, table, pool, lens, out, err)
+    assert int(err) == 0 and int(out) == n - T + 3
+    want = c.rows(0).to(D_)
+    want[n - T + 1], want[n - T + 2] = want[n - T + 2].clone(), want[n - T + 4].clone()
+    assert torch.equal(flat[at], want)
+
+
+@GPU
+@pytest.mark.parametrize("batch,tokens", [(8192, 40000), (3060, 33000), (1025, 32769)])
+def test_tables_of_many_requests_with_a_slot_map_of_their_own(mla, batch, tokens):
+    from tests.test_tree_tables import _requests, _run_tables
+
+    _run_tables(mla, 4, *_requests(batch, batch, 2, 4, 2 * batch), tokens, in_place=True)
