@@ -15,8 +15,8 @@
  *
  * Conventions shared by every call:
  *   - Every data pointer is DEVICE memory owned by the caller; the library allocates nothing
- *     and never frees. Between calls it keeps only which devices already have the attention
- *     kernel's shared-memory limit raised (and, for mla_decode_static_workspace, each device's
+ *     and never frees. Between calls it keeps only on which devices a kernel's shared-memory
+ *     limit is already raised (and, for mla_decode_static_workspace, each device's
  *     address of its workspace array). mla_decode always cuts the work into 74 ranges, one
  *     per pair of SMs of a 148-SM B200; a device with fewer SMs runs them in more than one wave.
  *   - Every call only enqueues work on `stream` (a cudaStream_t passed as void*; NULL is the
@@ -382,7 +382,9 @@ MLA_API mla_status mla_combine_partials(const mla_config* cfg, const float* part
  *   mla_absorb_query, mla_append_slots, mla_decode_tree, then mla_commit_tree.
  * A sequence whose length is 0 is an empty place of a padded batch: no call reads its rows or
  * flags what it holds. (mla_build_tables takes back its blocks, so blocks_held and new_lens are
- * checked there as for any other.)
+ * checked there as for any other.) The pool is in the configuration's dtype: the calls of this part
+ * have no form for the fp8 pool of mla_append_latent_fp8, whose rows' scales would have to be
+ * written, read and moved with them.
  */
 
 /* Most requests mla_build_tables takes in one call, and most nodes of a drafted tree. */
@@ -458,17 +460,17 @@ MLA_API mla_status mla_tree_masks(const int32_t* parents, int32_t parents_batch,
  * (n_tokens, d_r), pool (num_blocks, block_size, r + d_r) dtype; gamma (r) float32; pos
  * (n_tokens) int32; slots (n_tokens) int64. ckv_raw, gamma and pool must be 16-byte aligned,
  * krope_raw 8-byte.
- * fp32 statistics, angles in double. Differences from mla_append_latent: the sum of squares is taken
- * in another order, so a value may round the other way; and in bf16 pools the sine and cosine of the
- * (double) angle are fp32's, 2^-22 or so off, where it takes double's.
+ * fp32 statistics, angles in double. Differences from mla_append_latent: the sum of squares is
+ * taken in another order, so a value may round the other way; and in bf16 pools the sine and cosine
+ * of the (double) angle are fp32's, 2^-22 or so off, where it takes double's.
  */
 MLA_API mla_status mla_append_slots(const mla_config* cfg, const void* ckv_raw,
                                     const void* krope_raw, const float* gamma, const int32_t* pos,
                                     const int64_t* slots, void* pool, int32_t num_blocks,
                                     int32_t n_tokens, uint32_t* dev_err, void* stream);
 
-/* Workspace of mla_decode_tree in bytes (0 for an invalid configuration and for the sizes that the call
- * refuses); 256-byte aligned. */
+/* Workspace of mla_decode_tree in bytes (0 for an invalid configuration and for the sizes that the
+ * call refuses); 256-byte aligned. Calls that may run at the same time need one each. */
 MLA_API size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t batch,
                                               int32_t q_per_seq);
 
@@ -490,8 +492,10 @@ MLA_API size_t mla_decode_tree_workspace_size(const mla_config* cfg, int32_t bat
  * too and sets MLA_DEV_BAD_LENGTH. The rows of a block whose id is outside the pool are attended by
  * nobody, and MLA_DEV_OOB_BLOCK is set. q, pool, w_uv and o must be 16-byte aligned. Deterministic.
  * decode_kernel chooses as in mla_decode: the tensor-core kernel needs bf16, r = 512, d_r = 64 and
- * a block_size that is a multiple of 64, and takes any H. Between the attention and W_UV that path
- * keeps the latent sums as two bf16 terms (16 bits), the other in fp32.
+ * a block_size that is a multiple of 64, and takes any H. That path rounds where the other keeps
+ * fp32: the softmax weights to bf16 before their product with the rows (2^-8 of each weight; their
+ * sum and lse are of the fp32 weights), and the latent sums to two bf16 terms (16 bits) between the
+ * attention and W_UV. Other bf16 shapes and fp32 run on CUDA cores, many times slower at length.
  * MLA_ERR_UNSUPPORTED: q_per_seq > MLA_MAX_TREE, batch * q_per_seq > 2^24 or times H > 2^28; on
  * the tensor-core path also a pool of 2^31 rows or more, or 2^31 or more 64-row pieces of work, as
  * many as a table row can hold for each group of 128-row query tiles.

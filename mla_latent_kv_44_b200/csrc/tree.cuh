@@ -7,9 +7,9 @@
 
 namespace mla {
 
-// Raises a kernel's limit of dynamic shared memory on the current device, once, to the most that any
-// of its calls needs, and never lowers it: set to each call's own size, another thread's smaller call
-// could come between this one's limit and its launch. `devices` is the kernel's own.
+// Raises a kernel's limit of dynamic shared memory on the current device, once, to the most that
+// any of its calls needs, and never lowers it: set to each call's own size, another thread's
+// smaller call could come between this one's limit and its launch. `devices` is the kernel's own.
 inline cudaError_t raise_smem_limit(const void* kernel, size_t most,
                                     std::atomic<unsigned long long>& devices) {
   int dev = 0;
@@ -69,8 +69,8 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int
   return (p.mask[((size_t)b * p.T + t) * p.words + (node >> 5)] >> (node & 31)) & 1u;
 }
 
-// First chunk of range q of R over C chunks, floor(q C / R); a 32-bit division, which takes a fraction
-// of the time, where that is enough.
+// First chunk of range q of R over C chunks, floor(q C / R); a 32-bit division, which takes a
+// fraction of the time, where that is enough.
 __host__ __device__ __forceinline__ int first_chunk(int q, int R, int C) {
   if (C < 1 << 25) return (int)((uint32_t)q * (uint32_t)C / (uint32_t)R);
   return (int)((int64_t)q * C / R);

@@ -7,16 +7,16 @@
 // NP 16-byte pieces of the row (coalesced across the warp), fp32 statistics by a butterfly. The
 // angles are p * theta_i in double, as everywhere in the library, and are brought into [-pi, pi]
 // in double (Cody and Waite's two-term reduction; exact to a rounding while the angle's turns are
-// whole numbers of a double, any position for rope_base >= 1). An fp32 pool then gets the rotation in
-// double, rounded once, as mla_append_latent does it. For a bf16 pool, whose rounding is 2^-8, sine
-// and cosine are taken in fp32, off by 2^-23 for the angle rounded to fp32 and 2^-22 for sincosf:
-// 16,384 rows of 512 take 10.9 us instead of 11.9 from HBM, 8.0 instead of 9.2 from L2 (fp32 rows,
-// in double, 14.0 and 8.7). theta_i = base^(-2i/d_r) comes from the host as a kernel argument: a
-// double pow per lane, and sincos of the whole angle in double, took most of the 16 us that 16,384
-// bf16 rows needed.
-// What bounds it: HBM and its latency for prompts (the row in and out: 16,384 tokens, 37.9 MB, 10.5
-// us or 3.6 TB/s from HBM, 7.7 with the rows in L2; a warp has a row and the next in flight),
-// latency for a decode step (128 tokens: 2.5 us).
+// whole numbers of a double, any position for rope_base >= 1). An fp32 pool then gets the rotation
+// in double, rounded once, as mla_append_latent does it. For a bf16 pool, whose rounding is 2^-8,
+// sine and cosine are taken in fp32, off by 2^-23 for the angle rounded to fp32 and 2^-22 for
+// sincosf: 16,384 rows of 512 take 10.9 us instead of 11.9 from HBM, 8.0 instead of 9.2 from L2
+// (fp32 rows, in double, 14.0 and 8.7). theta_i = base^(-2i/d_r) comes from the host as a kernel
+// argument: a double pow per lane, and sincos of the whole angle in double, took most of the 16 us
+// that 16,384 bf16 rows needed.
+// What bounds it: HBM and its latency for prompts (the row in and out: 16,384 tokens, 37.9 MB, 10.9
+// us or 3.5 TB/s from HBM, 8.0 with the rows in L2; a warp has a row and the next in flight),
+// latency for a decode step (128 tokens: 2.6 us).
 #include <algorithm>
 #include <cmath>
 
@@ -176,8 +176,8 @@ cudaError_t append_slots_go(const mla_config& c, const void* ckv, const void* kr
   const int grid = std::min((n + kAppendWarps - 1) / kAppendWarps, 148 * append_ctas(NP));
   RopeTheta theta = {};
   // by products in the longest type (64 bits of mantissa): rounded to double, each theta is off by
-  // 2^-53 of itself, and so is its angle by another, 2^-52 in all: 4.8e-7 at position 2^31, 2.3e-10 at
-  // 2^20
+  // 2^-53 of itself, and so is its angle by another, 2^-52 in all: 4.8e-7 at position 2^31, 2.3e-10
+  // at 2^20
   if (c.rope_dim > 0) {
     const long double step = std::pow((long double)c.rope_base, -2.0L / c.rope_dim);
     long double t = 1.0L;

@@ -19,26 +19,33 @@
 // branch an MMA took 132 cycles to issue whatever its size, with the warp converged and the
 // descriptors' low words at hand 25.
 //
-// What bounds it. 32 sequences x 16384 rows x 4 tokens of 128 heads take 480 us in short bursts,
-// 1.22 PFLOP/s (0.72 of the measured burst rate, 0.86 of the sustained one: the power limit holds
-// the clock near 1.4 GHz). A tile takes about 7k cycles for 4.35k of products. Beside them its
-// softmax takes 4.3k (scores out of TMEM and the maximum 1.7k, exponentials 1.7k, P 0.4k, waits),
-// so that any instruction more in it shows: scores read twice to save registers 516 us against
-// 493, exponentials begun before the two halves' maxima are exchanged 512. The operands come out of
-// L2 at 40 bytes per clock and SM, 11.6 TB/s in all; with no loads at all (and wrong results) 8 x
-// 16384 x 4 took 113 us instead of 137, without V's 128, without K's 137. More query rows per pair
-// would halve the operands but for O, which fills the tensor memory beside S.
+// What bounds it. 32 sequences x 16384 rows x 4 tokens of 128 heads take 571 us when run for
+// seconds, 1.02 PFLOP/s, 0.73 of the measured sustained rate (the power limit holds the clock near
+// 1.4 GHz), and 477 us in bursts of a few launches. A tile takes about 7k cycles for 4.35k of
+// products. Beside them its softmax takes 4.3k (scores out of TMEM and the maximum 1.7k,
+// exponentials 1.7k, P 0.4k, waits), so that any instruction more in it shows: scores read twice to
+// save registers 516 us against 493, exponentials begun before the two halves' maxima are exchanged
+// 512. The operands come out of L2 at 40 bytes per clock and SM, 11.6 TB/s in all. More query rows
+// per pair would halve the operands but for O, which fills the tensor memory beside S.
 //
-// Few heads (a tile of 128 rows half empty) are bound by HBM: 3 x 32768 rows x 5 tokens of 16 heads
-// take 43 us, and once under way stream at 4.9 TB/s. One short sequence is bound by latency: of 15
-// us for 8 tokens x 1000 rows the schedule takes 2, the first loads 1.5, a tile's scores, softmax
-// and P . V 6, the partial results 3.
+// Few heads (a tile of 128 rows half empty) are bound by the tile's own time, which is that of 128
+// rows whatever part of them is real, and by the fixed parts: 3 x 32768 rows x 5 tokens of 16
+// heads, 113 MB of cache rows, take 45 us here (2.5 TB/s) and 63 with the merge and W_UV. One short
+// sequence is bound by latency: of 15 us for 8 tokens x 1000 rows the schedule takes 2, the first
+// loads 1.5, a tile's scores, softmax and P . V 6, the partial results 3.
 //
 // Softmax: four warps, a thread holds one query row and half of the tile's keys (TMEM lane), two
 // threads of a row exchange their maxima; base-2 exponents, the running maximum moved only when
 // a tile exceeds it by 2^8, the sum l of the fp32 weights. The same warps rescale O when the
 // maximum moves. At a segment's end four other warps write O / l, so that the softmax of the next
 // segment goes on meanwhile.
+//
+// P is rounded to bf16, the type of V in the product: 2^-8 of each weight at most, of random sign,
+// which takes the error of o against 64 bits from 1.66e-3 of its norm (its own rounding) to 2.05e-3
+// for 8 tokens x 1000 rows, 1.75e-3 for 16384 rows. l adds the weights as they were before that:
+// with the rounded ones o gained nothing (2.05e-3, 1.75e-3; 1.85e-3 instead of 2.06e-3 for scores
+// four times as large), lse lost (1e-6 off against 1e-4 to 3e-3), and it took 492 us instead of
+// 477.
 //
 // Rows that a token does not see: the prefix (rows before the drafted ones) is seen by all; for
 // the drafted rows a thread builds the 32-bit words of its keys from its token's mask, and a
@@ -155,8 +162,12 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 // Arrival on a barrier of either CTA of the pair. CTA scope on purpose: a release of cluster scope
-// waits for everything the thread has in flight (about 1000 cycles here); what the arrivals
-// order is ordered before them (tcgen05.wait::ld, fence.proxy.async by each writing thread).
+// waits for everything the thread has in flight (about 1000 cycles here). The memory model does not
+// order across the two CTAs at that scope; that it suffices is an assumption about the hardware,
+// the one that kernels on pairs of SMs usually make. What it rests on: no thread of the other CTA
+// reads what the arrivals hand over, only the tensor core of the writer's own SM does (P and V in
+// its shared memory, S and O in its tensor memory), and the writer has put that before the arrival
+// itself (tcgen05.wait and fence::before_thread_sync, fence.proxy.async by each writing thread).
 __device__ __forceinline__ void arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
