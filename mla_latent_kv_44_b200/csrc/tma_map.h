@@ -7,19 +7,43 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mla {
 
-inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+// A function of the driver, looked up once (F: its type; version: since when the driver has it).
+template <typename F>
+inline F driver_function(const char* name, unsigned version, std::atomic<F>& known) {
+  F fn = known.load(std::memory_order_acquire);
   if (!fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    if (cudaGetDriverEntryPointByVersion(name, &ptr, version, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      fn = reinterpret_cast<F>(ptr);
+      known.store(fn, std::memory_order_release);
+    }
   }
   return fn;
+}
+
+// Encoding a map needs a context that is current in the calling thread, and a thread that has made
+// no call of the runtime yet has none: it gets that of its current device, as its first launch would
+// give it.
+inline bool thread_has_context() {
+  static std::atomic<PFN_cuCtxGetCurrent_v4000> known{nullptr};
+  const auto current = driver_function("cuCtxGetCurrent", 4000, known);
+  CUcontext ctx = nullptr;
+  if (current && current(&ctx) == CUDA_SUCCESS && ctx) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  if (!thread_has_context()) return nullptr;
+  return driver_function("cuTensorMapEncodeTiled", 12000, known);
 }
 
 // 2-D bf16 view: `rows` rows of `cols` elements, `row_bytes` apart, copied in 128-byte swizzled
