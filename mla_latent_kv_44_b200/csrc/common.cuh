@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "mla.h"
@@ -124,6 +125,27 @@ __device__ __forceinline__ void rope_cos_sin(int p, int i, int dr, float base, d
 // are visible. Launched without the attribute, the wait returns at once.
 __device__ __forceinline__ void wait_prior_grid() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Raises a kernel's limit of dynamic shared memory on the current device, once, to all that a block
+// may have beside the kernel's static memory, and never lowers it: set to each call's own size,
+// another thread's smaller call could come between this one's limit and its launch. `devices` is
+// the kernel's own.
+inline cudaError_t raise_smem_limit(const void* kernel, std::atomic<unsigned long long>& devices) {
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes attr;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) !=
+          cudaSuccess ||
+      (e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                most - (int)attr.sharedSizeBytes)) != cudaSuccess)
+    return e;
+  devices.fetch_or(bit, std::memory_order_acq_rel);
+  return cudaSuccess;
 }
 
 template <typename... KArgs, typename... Args>

@@ -162,7 +162,8 @@ static cudaError_t simt_go(const DecodeParams& p, cudaStream_t st) {
   const size_t smem = sizeof(float) * (kSimtRows * (p.D + 1) + kSimtHeads * p.D) +
                       (sizeof(int) + sizeof(float)) * kSimtRows;
   auto k = attend_simt_kernel<TQ, TR, RW>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> devices{0};
+  const cudaError_t e = raise_smem_limit((const void*)k, devices);
   if (e != cudaSuccess) return e;
   dim3 grid(kRanges + p.BT, (p.H + kSimtHeads - 1) / kSimtHeads);
   return launch_pdl(k, grid, dim3(kSimtHeads * 32), smem, st, p);

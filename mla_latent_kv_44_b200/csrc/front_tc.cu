@@ -404,8 +404,8 @@ cudaError_t launch_front_linear(const mla_config& c, const void* x, int n, int K
     if (!make_bf16_map(&tx, x, (uint64_t)K, (uint64_t)n, (uint64_t)ldx * 2, (uint32_t)ntile))
       return cudaErrorInvalidValue;
     const size_t smem = front_smem(ntile);
-    e = cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+    static std::atomic<unsigned long long> devices{0};
+    e = raise_smem_limit((const void*)linear_tc_kernel, devices);
     if (e != cudaSuccess) return e;
     e = launch_pdl(linear_tc_kernel, dim3(mt, splits, nt), dim3(128), smem, st, tm[0], tm[1],
                    tm[2], tm[3], tx, a);
@@ -413,8 +413,8 @@ cudaError_t launch_front_linear(const mla_config& c, const void* x, int n, int K
     for (int i = 0; i < nseg; ++i) a.wf[i] = (const float*)w[i];
     const size_t smem = (size_t)K * 4;
     if (smem > 227 * 1024) return cudaErrorInvalidValue;
-    e = cudaFuncSetAttribute(linear_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+    static std::atomic<unsigned long long> devices{0};
+    e = raise_smem_limit((const void*)linear_simt_kernel, devices);
     if (e != cudaSuccess) return e;
     e = launch_pdl(linear_simt_kernel, dim3(mt, 1, std::min(n, 64)), dim3(128), smem, st,
                    (const float*)x, a);

@@ -82,10 +82,9 @@ static cudaError_t absorb_go(const mla_config& c, const void* qn, const void* qr
                              const int32_t* pos, const void* w, void* q, int n, cudaStream_t st) {
   const size_t smem = sizeof(float) * kAbsorbTokens * c.head_dim;
   auto k = absorb_kernel<T, COLS>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  static std::atomic<unsigned long long> devices{0};
+  const cudaError_t e = raise_smem_limit((const void*)k, devices);
+  if (e != cudaSuccess) return e;
   dim3 grid((n + kAbsorbTokens - 1) / kAbsorbTokens, c.num_heads);
   return launch_pdl(k, grid, dim3(256), smem, st, (const T*)qn, (const T*)qr, pos, (const T*)w,
                     (T*)q, n, c.num_heads, c.head_dim, c.kv_rank, c.rope_dim, c.rope_base);
@@ -193,20 +192,16 @@ cudaError_t launch_output(const mla_config& c, const float* lat, const void* w_u
   dim3 grid((n + kOutTokens - 1) / kOutTokens, c.num_heads);
   if (c.dtype == MLA_BF16) {
     auto k = output_kernel<__nv_bfloat16>;
-    if (smem > 48 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
+    static std::atomic<unsigned long long> devices{0};
+    const cudaError_t e = raise_smem_limit((const void*)k, devices);
+    if (e != cudaSuccess) return e;
     return launch_pdl(k, grid, dim3(256), smem, st, lat, (const __nv_bfloat16*)w_uv,
                       (__nv_bfloat16*)o, n, c.num_heads, c.head_dim_v, c.kv_rank);
   } else {
     auto k = output_kernel<float>;
-    if (smem > 48 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
+    static std::atomic<unsigned long long> devices{0};
+    const cudaError_t e = raise_smem_limit((const void*)k, devices);
+    if (e != cudaSuccess) return e;
     return launch_pdl(k, grid, dim3(256), smem, st, lat, (const float*)w_uv, (float*)o, n,
                       c.num_heads, c.head_dim_v, c.kv_rank);
   }

@@ -502,8 +502,8 @@ cudaError_t launch_absorb_tc(const mla_config& c, const void* q_nope, const void
                      (uint32_t)tile))
     return cudaErrorInvalidValue;
   const size_t smem = absorb_smem(dh, c.rope_dim, tile);
-  cudaError_t e = cudaFuncSetAttribute(absorb_tc_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> devices{0};
+  const cudaError_t e = raise_smem_limit((const void*)absorb_tc_kernel, devices);
   if (e != cudaSuccess) return e;
   AbsorbArgs a{(const __nv_bfloat16*)q_rope, pos, (__nv_bfloat16*)q_out, err, n, H, dh, r,
                c.rope_dim, tile, c.rope_base};
@@ -526,8 +526,8 @@ cudaError_t launch_output_tc(const mla_config& c, const float* lat, const void* 
   if (!make_bf16_map(&tw, w_uv, (uint64_t)r, (uint64_t)H * dv, (uint64_t)r * 2, kWRows))
     return cudaErrorInvalidValue;
   const size_t smem = output_smem(tile);
-  cudaError_t e = cudaFuncSetAttribute(output_tc_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> devices{0};
+  const cudaError_t e = raise_smem_limit((const void*)output_tc_kernel, devices);
   if (e != cudaSuccess) return e;
   OutputArgs a{lat, (__nv_bfloat16*)o, err, n, H, dv, r, tile};
   dim3 grid((n + tile - 1) / tile, mts, H);
@@ -548,8 +548,8 @@ cudaError_t launch_step_prep(const mla_config& c, const void* q_nope, const void
                      (uint32_t)tile))
     return cudaErrorInvalidValue;
   const size_t smem = absorb_smem(dh, c.rope_dim, tile);
-  cudaError_t e = cudaFuncSetAttribute(step_prep_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> devices{0};
+  const cudaError_t e = raise_smem_limit((const void*)step_prep_kernel, devices);
   if (e != cudaSuccess) return e;
   PrepArgs a;
   a.ab = AbsorbArgs{(const __nv_bfloat16*)q_rope, pos, (__nv_bfloat16*)q_out, p.err, n, H, dh, r,

@@ -356,9 +356,6 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const TableParams
       i0, p.per_thread, s_cu[p.batch]);
 }
 
-// four lists of the requests, three of them with an end
-constexpr size_t table_smem(int batch) { return sizeof(int) * (4 * (size_t)batch + 3); }
-
 }  // namespace
 
 cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens, int batch,
@@ -376,12 +373,12 @@ cudaError_t launch_build_tables(const int32_t* seq_lens, const int32_t* new_lens
   TableParams p{seq_lens, new_lens, held,  table, free_blocks, free_count, held_out,
                 free_count_out, cu, seq_idx, pos, slots, err, batch, max_blocks, num_blocks, bs,
                 max_tokens, per, vec, apart};
-  const size_t smem = table_smem(batch);
+  const size_t smem = sizeof(int) * (4 * (size_t)batch + 3);
   // (the limit of 48 KB without this covers the kernel's static shared memory too)
   if (smem > 40 * 1024) {
     static std::atomic<unsigned long long> devices{0};
-    const cudaError_t e = raise_smem_limit((const void*)build_tables_kernel<kTabThreads>,
-                                           table_smem(MLA_MAX_TABLE_BATCH), devices);
+    const cudaError_t e =
+        raise_smem_limit((const void*)build_tables_kernel<kTabThreads>, devices);
     if (e != cudaSuccess) return e;
   }
   // one CTA while a pass of it covers the tokens and the requests, else a full cluster. A CTA of

@@ -1,26 +1,9 @@
 // Declarations shared by the kernels of mla_decode_tree.
 #pragma once
 
-#include <atomic>
-
 #include "common.cuh"
 
 namespace mla {
-
-// Raises a kernel's limit of dynamic shared memory on the current device, once, to the most that
-// any of its calls needs, and never lowers it: set to each call's own size, another thread's
-// smaller call could come between this one's limit and its launch. `devices` is the kernel's own.
-inline cudaError_t raise_smem_limit(const void* kernel, size_t most,
-                                    std::atomic<unsigned long long>& devices) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (bit && (devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-  if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_acq_rel);
-  return e;
-}
 
 constexpr int kTreeTile = 128;      // query rows of a tile on the tensor-core path
 constexpr int kTreeMaxSplits = 64;  // ranges of a sequence's cache rows on the CUDA-core path

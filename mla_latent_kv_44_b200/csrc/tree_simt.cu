@@ -381,38 +381,27 @@ tree_simt_out_kernel(const TreeParams p, const T* __restrict__ w_uv, T* __restri
   }
 }
 
-// bytes of shared memory: M query rows, `keys` cache rows and the weights between them
-constexpr size_t simt_smem(int M, int keys, int D) {
-  return sizeof(float) * ((size_t)M * D + (size_t)keys * (D + 4) + (size_t)M * keys);
-}
-
 template <typename T, int RPW, int KPL, int RW>
 cudaError_t simt_go(const TreeParams& p, cudaStream_t st) {
-  constexpr int M = kWarps * RPW, keys = 32 * KPL;
-  // the longest row: 64 cache rows a tile are for r + d_r <= 192 (simt_dispatch), d_r <= 256
-  constexpr int most = KPL == 2 ? 192 : 32 * RW + 256;
-  static_assert(simt_smem(M, keys, most) <= 227 * 1024 - sizeof(int) * keys, "shared memory");
+  const int M = kWarps * RPW, keys = 32 * KPL;
+  const size_t smem = sizeof(float) * ((size_t)M * p.D + keys * (p.D + 4) + M * keys);
   static std::atomic<unsigned long long> devices{0};
   auto k = tree_simt_kernel<T, RPW, KPL, RW>;
-  const cudaError_t e = raise_smem_limit((const void*)k, simt_smem(M, keys, most), devices);
+  const cudaError_t e = raise_smem_limit((const void*)k, devices);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3((unsigned)(p.batch * p.tiles * p.splits)), dim3(kWarps * 32),
-                    simt_smem(M, keys, p.D), st, p);
+  return launch_pdl(k, dim3((unsigned)(p.batch * p.tiles * p.splits)), dim3(kWarps * 32), smem,
+                    st, p);
 }
 
 template <typename T, int NT>
 cudaError_t simt_out(const TreeParams& p, const void* w_uv, int dv, void* o, cudaStream_t st) {
-  constexpr size_t most_w = 64 * 1024;
   const size_t w_bytes = (size_t)dv * (p.r * sizeof(T) + 16);
-  const int stage = w_bytes <= most_w;
+  const int stage = w_bytes <= 64 * 1024;
   const size_t smem = sizeof(float) * NT * p.r + (stage ? w_bytes : 0);
+  static std::atomic<unsigned long long> devices{0};
   auto k = tree_simt_out_kernel<T, NT>;
-  if (smem > 40 * 1024) {
-    static std::atomic<unsigned long long> devices{0};
-    const cudaError_t e =
-        raise_smem_limit((const void*)k, sizeof(float) * NT * 1024 + most_w, devices);  // r <= 1024
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = raise_smem_limit((const void*)k, devices);
+  if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3((unsigned)(p.H * ((p.BT + NT - 1) / NT))), dim3(128), smem, st, p,
                     (const T*)w_uv, (T*)o, dv, stage);
 }

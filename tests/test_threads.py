@@ -91,3 +91,45 @@ def test_a_threads_first_call(mla, name):
     t.join()
     torch.cuda.synchronize()
     assert not caught, caught
+
+
+PAIRS = {  # function of the library, two calls of it through the same kernels
+    "absorb_query bf16": lambda m: (_absorb(m, "bf16", 1, 128, 512, 64), _absorb(m, "bf16", 64, 256, 512, 64)),
+    "absorb_query f32": lambda m: (_absorb(m, "f32", 9, 800, 64, 32), _absorb(m, "f32", 9, 1024, 64, 32)),
+    "output bf16": lambda m: (_output(m, "bf16", 1, 512), _output(m, "bf16", 64, 512)),
+    "output f32": lambda m: (_output(m, "f32", 9, 800), _output(m, "f32", 9, 1024)),
+    "decode_stages f32": lambda m: (_decode(m, 0), _decode(m, 128)),
+    "project bf16": lambda m: (_project(m, 1, 512), _project(m, 64, 512)),
+    "project f32": lambda m: (_project(m, 2, 1024, "f32"), _project(m, 2, 8192, "f32"))}
+
+
+@pytest.mark.parametrize("pair", PAIRS)
+def test_two_threads_at_sizes_of_their_own(mla, pair):
+    """Each with its stream and buffers: no launch may depend on the other thread's. The calls' arguments
+    are taken down once and the library called with them, as a C program would."""
+    name = "mla_" + pair.split()[0]
+    fn, args = getattr(mla.lib, name), []
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for call, s in zip(PAIRS[pair](mla), streams):
+        call(s)
+        mla.lib.__dict__[name] = lambda *a: args.append((a, call)) or mla.MLA_OK
+        try:
+            call(s)
+        finally:
+            mla.lib.__dict__[name] = fn
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(a):
+        for _ in range(6000):
+            st = fn(*a)
+            if st:
+                failed.append(st)
+
+    threads = [threading.Thread(target=run, args=(a,)) for a, _ in args]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, (len(failed), failed[0])
