@@ -28,6 +28,9 @@
  *     an impossible sequence length, a bounded wait that gave up) set bits in *dev_err
  *     (atomicOr) and skip the affected work; kernels never trap. The caller clears *dev_err.
  *   - Empty work (n_tokens == 0, batch == 0) returns MLA_OK without launching.
+ *   - Any host thread may call, and several at once, each with a stream and a workspace of its own
+ *     (mla_decode_static_workspace has one for all). A thread that has no CUDA context yet gets its
+ *     current device's.
  */
 #ifndef MLA_H_
 #define MLA_H_

@@ -21,7 +21,7 @@
 //
 // What bounds it. 32 sequences x 16384 rows x 4 tokens of 128 heads take 571 us when run for
 // seconds, 1.02 PFLOP/s, 0.73 of the measured sustained rate (the power limit holds the clock near
-// 1.4 GHz), and 477 us in bursts of a few launches. A tile takes about 7k cycles for 4.35k of
+// 1.4 GHz), and 477 to 509 us, by GPU, in bursts of a few. A tile takes about 7k cycles for 4.35k of
 // products. Beside them its softmax takes 4.3k (scores out of TMEM and the maximum 1.7k,
 // exponentials 1.7k, P 0.4k, waits), so that any instruction more in it shows: scores read twice to
 // save registers 516 us against 493, exponentials begun before the two halves' maxima are exchanged
