@@ -57,7 +57,7 @@ print(json.dumps([list(g) == list(w) if isinstance(g, list) else g == w for g, w
 
 
 @GPU
-@pytest.mark.parametrize("batch", [3046, 3047, 3071, 3072])
+@pytest.mark.parametrize("batch", [3046, 3047, 3071, 3080])
 def test_tables_where_shared_memory_passes_the_default_limit(batch):
     """In a process of its own: a larger call before would have raised the kernel's limit."""
     out = subprocess.run([sys.executable, "-c",
